@@ -41,15 +41,16 @@
  *   zsp_gather_list_create, owns memory of its own) and, from its first
  *   checkpoint save or load, the checkpoint staging (pinned host chunks,
  *   streams, events); zsp_destroy frees them. The other hot-path calls
- *   (reduce, Adam, the range and single gathers, schedule acquire and
- *   release) allocate nothing; checkpoint calls also use host memory for
- *   their own duration. The reduce, Adam, range and single gather calls,
- *   zsp_gather_list_run, and zsp_gather_many on lists of at most 64
- *   parameters, only check
+ *   (reduce, norm, Adam, the range and single gathers, schedule acquire and
+ *   release) allocate nothing on the device; checkpoint calls also use host
+ *   memory for their own duration. The reduce, norm, clip, Adam, range and
+ *   single gather calls, zsp_gather_list_run, and zsp_gather_many on lists of
+ *   at most 64 parameters, only check
  *   arguments and launch kernels (no host wait, no copy, no memset), so they
  *   can be captured into a HIP graph; Adam's scalars (lr, betas, eps and the
  *   step's bias corrections) are kernel arguments, so a replay repeats the
- *   step it was captured with.
+ *   step it was captured with (a clipped step reads its coefficient from
+ *   device memory, so a replay uses the one that is there then).
  *   Every device pointer must be 16-byte aligned (torch allocations are).
  *   State arrays bound for all ranks hold nd*S elements, rank r at
  *   [r*S, (r+1)*S); bound for one rank j they hold that rank's S elements.
@@ -68,8 +69,8 @@
  *   recent failure. Values are not checked: NaN and Inf propagate.
  *
  * Threads
- *   The reduce, Adam and gather calls (whole-model and _params forms, list
- *   gathers, prepared-list create and run) and zsp_load_params only read
+ *   The reduce, norm, Adam and gather calls (whole-model and _params forms,
+ *   list gathers, prepared-list create and run) and zsp_load_params only read
  *   the plan (zsp_gather_many takes the plan's staging slots under a lock
  *   of their own): several threads may issue them on one plan at once, e.g.
  *   one thread per rank, each on its own stream (work that writes the same
@@ -92,6 +93,7 @@ extern "C" {
 typedef struct zsp_plan zsp_plan;
 typedef struct zsp_sched zsp_sched;
 typedef struct zsp_gather_list zsp_gather_list;
+typedef struct zsp_tensor_list zsp_tensor_list;
 
 typedef enum {
     ZSP_OK = 0,
@@ -115,6 +117,18 @@ typedef enum {
     ZSP_SRC_MASTER = 1,  /* fp32 master parameters */
     ZSP_SRC_ACC = 2      /* fp32 gradient accumulator: each rank's reduced slice */
 } zsp_source;
+
+typedef enum {
+    ZSP_NORM_L2 = 0, /* square root of the sum of squares */
+    ZSP_NORM_MAX = 1 /* largest absolute value */
+} zsp_norm_kind;
+
+/* What a norm call leaves in device memory (see "Gradient norm and clipping"). */
+typedef struct zsp_clip {
+    double total; /* ZSP_NORM_L2: the sum of squares; ZSP_NORM_MAX: the largest |g| */
+    float norm;   /* infinity where it is beyond fp32; total and coef still hold */
+    float coef;   /* 1, or max_norm / norm where norm > max_norm; NaN: norm not finite */
+} zsp_clip;
 
 #define ZSP_ALL_RANKS (-1)
 #define ZSP_MAX_RANKS 256
@@ -330,6 +344,134 @@ zsp_status zsp_gather_list_create(zsp_plan* plan, const int32_t* ids, int32_t n,
                                   zsp_gather_list** list);
 zsp_status zsp_gather_list_run(zsp_gather_list* list, void* stream);
 void zsp_gather_list_destroy(zsp_gather_list* list);
+
+/* ---- Gradient norm and clipping --------------------------------------------
+ * The global norm of the gradients, and the step with gradients scaled down
+ * to a largest norm:
+ *   ZSP_NORM_L2   total = sum of g*g, norm = sqrt(total)
+ *   ZSP_NORM_MAX  total = largest |g|, norm = total
+ *   coef = 1 if norm <= max_norm, else max_norm / norm
+ * Squares are summed in 64 bits, so no finite gradient's square is lost or
+ * overflows; coef is computed in 64 bits and rounded once to fp32. If the
+ * total is infinite or NaN, coef is NaN, and a call that takes the record
+ * then changes nothing: the update of a step whose gradients are not finite
+ * is skipped. max_norm >= 0 (INFINITY: only the norm is wanted, coef is 1
+ * for every finite norm). Nothing here waits for the device or brings a
+ * value to the host: the record (zsp_clip) stays in device memory, from where
+ * the clipped calls read the coefficient.
+ *   Every call that makes a norm writes one record to `out` (device memory,
+ * 16-byte aligned) and uses a workspace `ws` (device memory, 16-byte aligned,
+ * ws_bytes >= what zsp_norm_workspace says; its contents mean nothing between
+ * calls). Calls in one stream's order may share a workspace; calls that may
+ * run at the same time, replays of captured graphs among them, each need
+ * their own. Equal inputs and sizes give equal bits: no atomics.
+ *   Errors beside each call's own: ZSP_EINVAL for a bad kind, a negative or
+ * NaN max_norm, a NULL or misaligned ws, out or clip; ZSP_ERANGE if ws_bytes
+ * is too small. */
+
+/* Workspace bytes for the norm calls on `plan` as it is bound now (before
+ * it is bound: as for all ranks), or, with plan NULL, for norms of lists of
+ * tensors: 8 bytes per 256 elements of the bound state, and about 20 KB.
+ * Host only. A plan's workspace also serves lists. */
+zsp_status zsp_norm_workspace(const zsp_plan* plan, int64_t* bytes);
+
+/* Norm of the bound accumulator's real elements (pad slots are left out,
+ * whatever they hold), of one rank or all, whole-model or parameters
+ * [first_param, first_param + n_params). Needs an accumulator bound. */
+zsp_status zsp_grad_norm(zsp_plan* plan, int32_t rank_or_all, zsp_norm_kind kind, float max_norm,
+                         void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
+zsp_status zsp_grad_norm_params(zsp_plan* plan, int32_t rank_or_all, int32_t first_param,
+                                int32_t n_params, zsp_norm_kind kind, float max_norm, void* ws,
+                                int64_t ws_bytes, zsp_clip* out, void* stream);
+
+/* zsp_reduce_shard (_params) with the norm of the accumulator elements it
+ * writes, in the same pass over the gradients: grad_acc is what
+ * zsp_reduce_shard leaves, bit for bit. */
+zsp_status zsp_reduce_shard_norm(zsp_plan* plan, int32_t rank_or_all, const void* const* grads,
+                                 zsp_dtype dtype, zsp_grad_layout layout, int32_t accumulate,
+                                 zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                                 zsp_clip* out, void* stream);
+zsp_status zsp_reduce_shard_norm_params(zsp_plan* plan, int32_t rank_or_all, int32_t first_param,
+                                        int32_t n_params, const void* const* grads,
+                                        zsp_dtype dtype, zsp_grad_layout layout,
+                                        int32_t accumulate, zsp_norm_kind kind, float max_norm,
+                                        void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
+
+/* The norm of the gradient that zsp_reduce_adam_step (use_acc likewise) would
+ * use, writing nothing but the record: with zsp_reduce_adam_step_clip, the
+ * clipped step of a caller that keeps no accumulator. Reads the gradients
+ * once more than an unclipped step. */
+zsp_status zsp_reduce_norm(zsp_plan* plan, int32_t rank_or_all, const void* const* grads,
+                           zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
+                           zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                           zsp_clip* out, void* stream);
+
+/* Joins the totals of n >= 0 records into one: the layers' records of a
+ * backward pass that reduced layer by layer, or one record whose total was
+ * summed (ZSP_NORM_MAX: maximised) over the processes of a data-parallel
+ * group. parts: n records in device memory, 16-byte aligned; only their
+ * totals are read. out may be one of them. No records: norm 0. */
+zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+                            zsp_clip* out, void* stream);
+
+/* zsp_adam_step and zsp_reduce_adam_step (_params) with the gradient g
+ * replaced by g * coef (one fp32 rounding), coef read from *clip in device
+ * memory when the kernel runs. coef NaN: no state of the named slots
+ * changes. The accumulator keeps the gradient as it was. A record of the
+ * whole model's norm clips every call of a step, layer by layer or whole. */
+zsp_status zsp_adam_step_clip(zsp_plan* plan, int32_t rank_or_all, const zsp_clip* clip, float lr,
+                              float beta1, float beta2, float eps, int64_t step, void* stream);
+zsp_status zsp_adam_step_clip_params(zsp_plan* plan, int32_t rank_or_all, int32_t first_param,
+                                     int32_t n_params, const zsp_clip* clip, float lr,
+                                     float beta1, float beta2, float eps, int64_t step,
+                                     void* stream);
+zsp_status zsp_reduce_adam_step_clip(zsp_plan* plan, int32_t rank_or_all,
+                                     const void* const* grads, zsp_dtype dtype,
+                                     zsp_grad_layout layout, int32_t use_acc,
+                                     const zsp_clip* clip, float lr, float beta1, float beta2,
+                                     float eps, int64_t step, void* stream);
+zsp_status zsp_reduce_adam_step_clip_params(zsp_plan* plan, int32_t rank_or_all,
+                                            int32_t first_param, int32_t n_params,
+                                            const void* const* grads, zsp_dtype dtype,
+                                            zsp_grad_layout layout, int32_t use_acc,
+                                            const zsp_clip* clip, float lr, float beta1,
+                                            float beta2, float eps, int64_t step, void* stream);
+
+/* The same for gradients that are not sharded (stages 0 and 1): the norm of
+ * n tensors taken together, and their scaling in place by a record's coef
+ * (x = x * coef in fp32, rounded once more to bf16 for a bf16 tensor; coef 1
+ * or NaN: nothing is written). Tensor i is numel[i] contiguous elements of
+ * type dtype[i] (a zsp_dtype) at x[i], which needs the alignment of its
+ * element type only; NULL is allowed for empty ones. The three arrays are
+ * host arrays, read during the call. The same tensor twice counts twice in a
+ * norm; a clip refuses tensors that overlap (ZSP_EINVAL). Tensors travel in
+ * kernel arguments, 128 per launch (launches follow one another on the
+ * stream); a list that is used again and again is better prepared.
+ * ZSP_EINVAL: n < 0, NULL arrays with n > 0, a negative numel, a bad dtype, a
+ * NULL or misaligned tensor; ZSP_ERANGE: 2^31 chunks of 4096 elements or
+ * more, counted per tensor. No plan is involved: all tensors, ws, out and
+ * clip are on the current device. */
+zsp_status zsp_norm_many(const void* const* x, const int64_t* numel, const int32_t* dtype,
+                         int32_t n, zsp_norm_kind kind, float max_norm, void* ws,
+                         int64_t ws_bytes, zsp_clip* out, void* stream);
+zsp_status zsp_clip_many(void* const* x, const int64_t* numel, const int32_t* dtype, int32_t n,
+                         const zsp_clip* clip, void* stream);
+
+/* A list of tensors prepared once: zsp_tensor_list_create takes the arrays of
+ * zsp_norm_many, with the same checks, and keeps on the current device a
+ * record of 16 bytes per 4096 elements of each tensor (allocated, filled on
+ * `stream` and waited for before it returns). _norm and _clip are then as
+ * zsp_norm_many and zsp_clip_many, each over the whole list in one pass, and
+ * need that device current (ZSP_ESTATE). The tensors must stay allocated.
+ * Calls only read the list: several threads and streams may use it at once,
+ * each norm with a workspace of its own. _destroy frees it (NULL is a no-op);
+ * calls on it must have finished. */
+zsp_status zsp_tensor_list_create(void* const* x, const int64_t* numel, const int32_t* dtype,
+                                  int32_t n, void* stream, zsp_tensor_list** list);
+zsp_status zsp_tensor_list_norm(const zsp_tensor_list* list, zsp_norm_kind kind, float max_norm,
+                                void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
+zsp_status zsp_tensor_list_clip(const zsp_tensor_list* list, const zsp_clip* clip, void* stream);
+void zsp_tensor_list_destroy(zsp_tensor_list* list);
 
 /* ---- Per-layer gather schedule with prefetch ------------------------------
  * [ZS3] on-demand fetch list (gather layer l before its computation, discard

@@ -1,0 +1,698 @@
+"""Global gradient norm, clipping and clipped updates on the GPU.
+
+References: the gradients summed by zsp_reduce_shard (itself bit for bit the
+oracle's) with the sum of squares, the norm and the coefficient taken in 64
+bits on the host; clipped updates against the unclipped ones of a twin plan
+whose accumulator was scaled first, bit for bit.
+
+Tolerances. The squares of fp32 values are exact in 64 bits but for one
+rounding each (2^-53), and a sum of N of them is off by at most N * 2^-53 of
+itself: total within (N + 2) * 2^-53. norm and coef are one 64-bit square
+root or quotient of that (half its relative error, plus two 64-bit
+roundings) and one rounding to fp32 (2^-24): both within
+2^-24 + (N + 4) * 2^-53. A largest absolute value is exact.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import zero_sharded_mixed_pad_amd as zsp
+from zero_sharded_mixed_pad_amd import binding, synth
+
+from test_gpu_parity import HP, Mirror, assert_bits, dev, np_of
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+STATE = ("g_master", "g_m", "g_v", "g_work", "g_acc")
+
+
+def rec_of(rec):
+    t, n, c = zsp.clip_values(rec)
+    return float(t[0]), np.float32(n[0].item()), np.float32(c[0].item())
+
+
+def expect(vals, kind):
+    """total in 64 bits of fp32 values (numpy)."""
+    v = np.abs(vals.astype(np.float64))
+    if v.size == 0:
+        return 0.0
+    return float(math.fsum(v * v)) if kind == "l2" and np.isfinite(v).all() else \
+        float((v * v).sum()) if kind == "l2" else float(v.max())
+
+
+def check_record(rec, vals, kind, max_norm):
+    total, norm, coef = rec_of(rec)
+    want = expect(vals, kind)
+    n = vals.size
+    if not math.isfinite(want):
+        assert not math.isfinite(total) and math.isnan(total) == math.isnan(want)
+        assert np.isnan(coef)
+        return
+    wn = math.sqrt(want) if kind == "l2" else want
+    tol = 2.0 ** -24 + (n + 4) * 2.0 ** -53
+    if kind == "max":
+        assert total == want
+    else:
+        assert abs(total - want) <= (n + 2) * 2.0 ** -53 * want
+    # 2^-150: half the smallest subnormal, where norm or coef is that small
+    if wn >= 2.0 ** 128 * (1 - 2.0 ** -25):
+        assert np.isposinf(norm)     # rounds past the largest fp32; total and coef do not
+    else:
+        assert abs(float(norm) - wn) <= tol * wn + 2.0 ** -150
+    wc = 1.0 if wn <= max_norm else max_norm / wn
+    assert abs(float(coef) - wc) <= tol * wc + 2.0 ** -150
+
+
+def real_mask(L, ranks, first=0, n=None):
+    """Positions of real elements of parameters [first, first + n) in the bound state."""
+    out = []
+    last = L.T if n is None else first + n
+    for i, r in enumerate(ranks):
+        for t in range(first, last):
+            s = int(L.shard_len[t])
+            real = max(0, min(s, int(L.numel[t]) - r * s))
+            b = i * L.S + int(L.shard_off[t])
+            out.append(np.arange(b, b + real))
+    return np.concatenate(out) if out else np.zeros(0, np.int64)
+
+
+def grads_of(M, *args, **kw):
+    """The Mirror's gradients on the GPU; a model without elements still names
+    buffers (a NULL gradient is refused)."""
+    return [g.to(dev()) if g.numel() else torch.zeros(8, dtype=g.dtype, device=dev())
+            for g in M.grads(*args, **kw)]
+
+
+LAYOUTS = [
+    ([1003, 64, 5, 0, 3 * 4096 + 1], 4),
+    ([1], 1), ([1], 7), ([3], 2), ([0, 0], 3),
+    ([4096 * 3, 11008 * 2, 4096, 4096], 8),
+    ([50021, 511, 513, 1025], 3),
+    (synth.small_tensor_sizes(count=300, lo=1, hi=900, seed=5), 8),   # short pieces
+    ([70001, 9, 12345], 17),
+    ([70001, 9, 12345], 70),
+    ([262147, 65536 * 2 + 8], 2),
+]
+
+
+# ---- lists of tensors ----------------------------------------------------------------
+
+def make_list(sizes, dtypes, seed, offset=0, sigma=1e-2):
+    """Tensors as views into guarded buffers, each `offset` elements past 16 bytes."""
+    bufs, xs = [], []
+    for i, (n, dt) in enumerate(zip(sizes, dtypes)):
+        o = 16 + offset * ((i % 3) + 1)
+        b = torch.full((n + o + 16,), 7.25, dtype=dt, device=dev())
+        b[o:o + n] = synth.normal(n, sigma, dt, synth.derive_seed("list", seed, i)).to(dev())
+        bufs.append((b, o, n))
+        xs.append(b[o:o + n])
+    return bufs, xs
+
+
+def values(xs):
+    return np.concatenate([x.float().cpu().numpy().ravel() for x in xs] or [np.zeros(0)])
+
+
+SIZES = [
+    [], [0], [1], [0, 5, 0], [7, 8, 9, 63, 64, 65, 511, 512, 513],
+    [4095, 4096, 4097, 8192, 12289], [1 << 20],
+    synth.small_tensor_sizes(count=128, lo=1, hi=3000, seed=1),
+    synth.small_tensor_sizes(count=129, lo=1, hi=3000, seed=2),
+    synth.small_tensor_sizes(count=700, lo=1, hi=9000, seed=3),
+]
+BF, FP = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("types", ["bf16", "fp32", "mixed"])
+@pytest.mark.parametrize("case", range(len(SIZES)))
+def test_list_norm_and_clip(case, types, kind):
+    sizes = SIZES[case]
+    dts = [{"bf16": BF, "fp32": FP, "mixed": (BF, FP, BF)[i % 3]}[types]
+           for i in range(len(sizes))]
+    for offset in (0, 1):
+        bufs, xs = make_list(sizes, dts, (case, types), offset)
+        before = [b.clone() for b, _, _ in bufs]
+        vals = values(xs)
+        n0 = math.sqrt(expect(vals, "l2")) if kind == "l2" else expect(vals, "max")
+        max_norm = 0.37 * float(np.float32(n0))
+        ws = zsp.norm_workspace()
+        ws.fill_(0xff)                       # whatever a workspace holds
+        one, prep = zsp.clip_record(), zsp.clip_record()
+        zsp.norm_many(xs, one, ws, max_norm=max_norm, kind=kind)
+        check_record(one, vals, kind, float(np.float32(max_norm)))
+        tl = zsp.TensorList(xs)
+        ws.fill_(0xff)
+        tl.norm(prep, ws, max_norm=max_norm, kind=kind)
+        check_record(prep, vals, kind, float(np.float32(max_norm)))
+        for b, w in zip((b for b, _, _ in bufs), before):
+            assert torch.equal(b, w)         # a norm writes nothing
+        coef = zsp.clip_values(prep)[2]
+        for clip in (lambda: zsp.clip_many(xs, prep), lambda: tl.clip(prep)):
+            want = []
+            for b, o, n in bufs:
+                w = b.clone()
+                w[o:o + n] = (b[o:o + n].float() * coef).to(b.dtype)
+                want.append(w)
+            clip()
+            for (b, _, _), w in zip(bufs, want):
+                assert_bits(np_of(b), np_of(w), f"clip, offset {offset}")   # guards included
+        tl.close()
+
+
+def test_list_clip_coefficients():
+    """1 and NaN leave every bit, NaN payloads too; 0 gives zeros; the rest one rounding."""
+    x = torch.tensor([1.0, -2.0, INF, float("nan"), 1e-40, -0.0, 3e38, 5.0, 2.5],
+                     device=dev())
+    for dt in (FP, BF):
+        for c in (1.0, float("nan"), 0.0, 0.5, 0.3333333432674408):
+            t = x.to(dt)
+            rec = zsp.clip_record()
+            rec.view(torch.float32)[0, 3] = c
+            keep = c == 1.0 or math.isnan(c)
+            want = t.clone() if keep else (t.float() * torch.tensor(c, device=dev())).to(dt)
+            got = t.clone()
+            zsp.clip_many([got], rec)
+            torch.cuda.synchronize()
+            nan = torch.isnan(want)
+            assert torch.equal(torch.isnan(got), nan)
+            assert_bits(np_of(got[~nan]), np_of(want[~nan]), f"coef {c}")
+
+
+@pytest.mark.parametrize("dt", [FP, BF])
+def test_list_norm_special_values(dt):
+    """Values whose squares leave fp32's range, subnormals, infinities, NaN of
+    either sign, and the largest value in the last element of a chunk."""
+    big, tiny = 3e38, 1e-40
+    cases = [([big, -big, 1.0], True), ([tiny] * 5, True), ([-0.0, 0.0], True),
+             ([1.0, -INF], False), ([1.0, float("nan"), 2.0], False),
+             ([-float("nan"), INF], False), ([1e-30] * 100, True)]
+    for vals, finite in cases:
+        for pad in (0, 4097):
+            t = torch.zeros(len(vals) + pad, dtype=dt)
+            t[pad:] = torch.tensor(vals).to(dt)
+            if any(math.isnan(v) for v in vals):    # a NaN with its sign set
+                i = next(i for i, v in enumerate(vals) if math.isnan(v))
+                bits = t.view(torch.int32 if dt == FP else torch.int16)
+                bits[pad + i] = -0x200000 if dt == FP else -0x40
+            x = t.to(dev())
+            for kind in ("l2", "max"):
+                rec, ws = zsp.clip_record(), zsp.norm_workspace()
+                zsp.norm_many([x], rec, ws, max_norm=1.5, kind=kind)
+                check_record(rec, t.float().numpy(), kind, 1.5)
+                assert np.isnan(rec_of(rec)[2]) != finite
+
+
+def test_coefficient_rules():
+    x = torch.full((4,), 2.0, device=dev())            # norm 4
+    ws, rec = zsp.norm_workspace(), zsp.clip_record()
+    for max_norm, want in ((4.0, 1.0), (INF, 1.0), (2.0, 0.5), (0.0, 0.0), (3.9999998, None)):
+        zsp.norm_many([x], rec, ws, max_norm=max_norm)
+        total, norm, coef = rec_of(rec)
+        assert total == 16.0 and norm == 4.0
+        if want is not None:
+            assert coef == want
+        else:
+            assert coef == np.float32(float(np.float32(max_norm)) / 4.0)
+    zsp.norm_many([torch.zeros(5, device=dev())], rec, ws, max_norm=0.0)
+    assert rec_of(rec) == (0.0, 0.0, 1.0)              # nothing to clip
+
+
+def test_the_same_tensor_twice():
+    """Counts twice in a norm, whichever form; a clip refuses it."""
+    _, xs = make_list([5000, 77], [BF, FP], "twice")
+    xs = xs + xs[:1]
+    ws, rec = zsp.norm_workspace(), zsp.clip_record()
+    zsp.norm_many(xs, rec, ws)
+    check_record(rec, values(xs), "l2", INF)
+    tl = zsp.TensorList(xs)
+    tl.norm(rec, ws, kind="max")
+    check_record(rec, values(xs), "max", INF)
+    for call in (lambda: zsp.clip_many(xs, rec), lambda: tl.clip(rec)):
+        with pytest.raises(zsp.ZspError) as e:
+            call()
+        assert e.value.status == binding.EINVAL
+
+
+def test_list_past_2_32_elements():
+    """A tensor of 2^32 + 4099 bf16 elements between two small ones: the far
+    end counts and is clipped."""
+    n = (1 << 32) + 4099
+    x = torch.zeros(n, dtype=BF, device=dev())
+    x[0], x[1 << 31], x[n - 1] = 3.0, 4.0, 12.0
+    small = torch.full((5,), 0.5, device=dev())
+    ws, rec = zsp.norm_workspace(), zsp.clip_record()
+    tl = zsp.TensorList([small, x, small.clone()])
+    zsp.norm_many([small, x], rec, ws)
+    assert rec_of(rec)[0] == 169.0 + 1.25
+    tl.norm(rec, ws, max_norm=1.0)
+    assert rec_of(rec)[0] == 169.0 + 2.5
+    rec.view(torch.float32)[0, 3] = 0.5
+    tl.clip(rec)
+    zsp.clip_many([x], rec)
+    assert (x[0].item(), x[1 << 31].item(), x[n - 1].item()) == (0.75, 1.0, 3.0)
+    zsp.norm_many([x], rec, ws, kind="max")
+    assert rec_of(rec)[0] == 3.0
+
+
+# ---- the accumulator's norm ---------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("case", range(len(LAYOUTS)))
+def test_grad_norm(case, kind):
+    numels, nd = LAYOUTS[case]
+    for rank_local in (None, nd - 1):
+        M = Mirror(numels, nd, rank_local=rank_local)
+        acc = synth.normal(M.n, 1e-2, FP, synth.derive_seed("acc", case)).numpy()
+        g = np.full(M.g_acc.numel(), np.nan, np.float32)     # pads and guards: NaN
+        at = real_mask(M.L, M.ranks)
+        g[at] = acc[at]
+        M.g_acc.copy_(torch.from_numpy(g))
+        ws, rec = M.plan.norm_workspace(), zsp.clip_record()
+        ws.fill_(0xff)
+        rank = zsp.ALL_RANKS if rank_local is None else rank_local
+        M.plan.grad_norm(rank, rec, ws, max_norm=0.01, kind=kind)
+        check_record(rec, acc[at], kind, float(np.float32(0.01)))
+        T = len(numels)
+        subs = {(0, 1), (T - 1, 1), (0, T), (T // 2, max(1, T // 3)), (min(1, T - 1), T - min(1, T - 1))}
+        for first, n in subs:
+            if first + n > T:
+                continue
+            M.plan.grad_norm_params(rank, first, n, rec, ws, max_norm=0.01, kind=kind)
+            check_record(rec, acc[real_mask(M.L, M.ranks, first, n)], kind,
+                         float(np.float32(0.01)))
+        if rank_local is None:
+            j = nd // 2
+            M.plan.grad_norm(j, rec, ws, kind=kind)
+            sub = real_mask(M.L, [j]) + j * M.L.S
+            check_record(rec, acc[sub], kind, INF)
+            M.plan.grad_norm_params(j, T // 2, 1, rec, ws, kind=kind)
+            check_record(rec, acc[real_mask(M.L, [j], T // 2, 1) + j * M.L.S], kind, INF)
+
+
+# ---- norms of the reduce --------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("layout", ["full", "shard"])
+@pytest.mark.parametrize("case", range(len(LAYOUTS)))
+def test_reduce_norms(case, layout, dt, kind):
+    """reduce_shard_norm leaves reduce_shard's accumulator, bit for bit, and
+    the norm of it; reduce_norm gives the same record and writes nothing."""
+    numels, nd = LAYOUTS[case]
+    for rank_local in (None, 0):
+        A = Mirror(numels, nd, rank_local=rank_local)
+        B = Mirror(numels, nd, rank_local=rank_local)
+        grads = grads_of(A, dt, ("norm", case), layout)
+        rank = zsp.ALL_RANKS if rank_local is None else rank_local
+        at = real_mask(A.L, A.ranks)
+        ws, rec, rec2 = A.plan.norm_workspace(), zsp.clip_record(), zsp.clip_record()
+        start = synth.normal(A.g_acc.numel(), 1e-2, FP, 11).to(dev())
+        for accumulate in (False, True):
+            A.g_acc.copy_(start)
+            B.g_acc.copy_(start)
+            ws.fill_(0xff)
+            A.plan.reduce_norm(rank, grads, rec2, ws, layout=layout, use_acc=accumulate,
+                               max_norm=0.02, kind=kind)
+            assert torch.equal(A.g_acc, start)
+            A.plan.reduce_shard_norm(rank, grads, rec, ws, layout=layout, accumulate=accumulate,
+                                     max_norm=0.02, kind=kind)
+            B.plan.reduce_shard(rank, grads, layout=layout, accumulate=accumulate)
+            assert_bits(np_of(A.g_acc), np_of(B.g_acc), "accumulator")
+            vals = np_of(B.g_acc)[at]
+            check_record(rec, vals, kind, float(np.float32(0.02)))
+            check_record(rec2, vals, kind, float(np.float32(0.02)))
+
+
+@pytest.mark.parametrize("case", [0, 6, 7, 8])
+def test_reduce_norm_by_layers_and_ranks(case):
+    """Parameter by parameter group and rank by rank, with the records joined."""
+    numels, nd = LAYOUTS[case]
+    A, B = Mirror(numels, nd), Mirror(numels, nd)
+    grads = grads_of(A, BF, ("layers", case))
+    B.plan.reduce_shard(zsp.ALL_RANKS, grads)
+    T = len(numels)
+    cut = sorted({0, 1, T // 3, T // 2, T})
+    groups = [(a, b - a) for a, b in zip(cut[:-1], cut[1:])]
+    ws = A.plan.norm_workspace()
+    for kind in ("l2", "max"):
+        A.g_acc.zero_()
+        parts = zsp.clip_record(len(groups) * nd)
+        i = 0
+        for first, n in groups:
+            for r in range(nd):
+                A.plan.reduce_shard_norm_params(r, first, n, grads, parts[i:i + 1], ws, kind=kind)
+                i += 1
+        out = zsp.clip_record()
+        zsp.clip_combine(parts, out, max_norm=0.03, kind=kind)
+        assert_bits(np_of(A.g_acc[:A.n]), np_of(B.g_acc[:B.n]), "accumulator")
+        check_record(out, np_of(B.g_acc)[real_mask(A.L, A.ranks)], kind, float(np.float32(0.03)))
+        parts2 = zsp.clip_record(len(groups))
+        for i, (first, n) in enumerate(groups):      # all ranks of a group in one call
+            A.plan.reduce_shard_norm_params(zsp.ALL_RANKS, first, n, grads, parts2[i:i + 1], ws,
+                                            kind=kind)
+        zsp.clip_combine(parts2, parts2[:1], max_norm=0.03, kind=kind)     # in place
+        check_record(parts2[:1], np_of(B.g_acc)[real_mask(A.L, A.ranks)], kind,
+                     float(np.float32(0.03)))
+
+
+def test_combine():
+    ws = torch.tensor([[4.0, 0.0], [5.0, 0.0], [7.0, 0.0]], dtype=torch.float64, device=dev())
+    out = zsp.clip_record()
+    zsp.clip_combine(ws, out, max_norm=2.0)
+    assert rec_of(out) == (16.0, 4.0, 0.5)
+    zsp.clip_combine(ws, out, max_norm=14.0, kind="max")
+    assert rec_of(out) == (7.0, 7.0, 1.0)
+    ws[1, 0] = float("nan")
+    for kind in ("l2", "max"):
+        zsp.clip_combine(ws, out, kind=kind)
+        assert np.isnan(rec_of(out)[2]) and math.isnan(rec_of(out)[0])
+    many = torch.ones(5003, 2, dtype=torch.float64, device=dev())
+    zsp.clip_combine(many, out)
+    assert rec_of(out)[0] == 5003.0
+    zsp.clip_combine(torch.zeros(0, 2, dtype=torch.float64, device=dev()), out, max_norm=0.0)
+    assert rec_of(out) == (0.0, 0.0, 1.0)
+
+
+def test_max_counts_every_place():
+    """One element larger than the rest, in turn at every kind of place: the
+    first and last of tiles, pieces, ranks and the whole state."""
+    numels, nd = [1300, 64, 5, 3 * 4096 + 1], 3
+    M = Mirror(numels, nd)
+    L = M.L
+    at = real_mask(L, M.ranks)
+    places = {int(at[0]), int(at[-1])}
+    for r in range(nd):
+        for t in range(L.T):
+            s = int(L.shard_len[t])
+            real = max(0, min(s, int(L.numel[t]) - r * s))
+            b = r * L.S + int(L.shard_off[t])
+            if real:
+                places |= {b, b + real - 1, min(b + real - 1, (b // 512 + 1) * 512),
+                           b + real // 2}
+    ws, rec = M.plan.norm_workspace(), zsp.clip_record()
+    base = torch.full((M.g_acc.numel(),), 0.25, device=dev())
+    for i, p in enumerate(sorted(places)):
+        M.g_acc.copy_(base)
+        M.g_acc[p] = -2.0 - i
+        M.plan.grad_norm(zsp.ALL_RANKS, rec, ws, kind="max")
+        assert rec_of(rec)[0] == 2.0 + i, p
+
+
+# ---- clipped updates -------------------------------------------------------------------
+
+def same_state(A, B, what, names=STATE):
+    for k in names:
+        assert_bits(np_of(getattr(A, k)[:A.n]), np_of(getattr(B, k)[:B.n]), f"{what}: {k}")
+
+
+@pytest.mark.parametrize("coef", [0.25, 0.3333333432674408, 1.0, 0.0])
+@pytest.mark.parametrize("case", range(len(LAYOUTS)))
+def test_clipped_updates(case, coef):
+    numels, nd = LAYOUTS[case]
+    for rank_local, dt, layout in ((None, BF, "full"), (nd - 1, FP, "shard")):
+        A, B = (Mirror(numels, nd, rank_local=rank_local) for _ in range(2))
+        rank = zsp.ALL_RANKS if rank_local is None else rank_local
+        grads = grads_of(A, dt, ("clip", case), layout)
+        rec = zsp.clip_record()
+        rec.view(torch.float32)[0, 3] = coef
+        T = len(numels)
+        step = 0
+
+        def twin(first, n, use_acc):
+            """The unclipped update from a scaled accumulator."""
+            keep = B.g_acc.clone()
+            B.plan.reduce_shard_params(rank, first, n, grads, layout=layout, accumulate=use_acc)
+            B.g_acc.mul_(coef)
+            B.plan.adam_step_params(rank, first, n, step=step, **HP)
+            B.g_acc.copy_(keep)
+
+        for use_acc in (False, True):
+            step += 1
+            A.plan.reduce_adam_step_clip(rank, grads, rec, step=step, layout=layout,
+                                         use_acc=use_acc, **HP)
+            twin(0, T, use_acc)
+            same_state(A, B, f"fused, use_acc {use_acc}")
+            step += 1
+            first, n = T // 3, max(1, T // 2)
+            A.plan.reduce_adam_step_clip_params(rank, first, n, grads, rec, step=step,
+                                                layout=layout, use_acc=use_acc, **HP)
+            twin(first, n, use_acc)
+            same_state(A, B, f"fused params, use_acc {use_acc}")
+            # the accumulator: reduced gradients for what follows
+            for M in (A, B):
+                M.plan.reduce_shard(rank, grads, layout=layout)
+        step += 1
+        A.plan.adam_step_clip(rank, rec, step=step, **HP)
+        A.plan.adam_step_clip_params(rank, T // 3, max(1, T // 2), rec, step=step + 1, **HP)
+        keep = B.g_acc.clone()
+        B.g_acc.mul_(coef)
+        B.plan.adam_step(rank, step=step, **HP)
+        B.plan.adam_step_params(rank, T // 3, max(1, T // 2), step=step + 1, **HP)
+        B.g_acc.copy_(keep)
+        same_state(A, B, "from the accumulator")
+
+
+@pytest.mark.parametrize("bad", [INF, float("nan")])
+@pytest.mark.parametrize("case", [0, 5, 7, 9])
+def test_step_is_skipped_when_the_norm_is_not_finite(case, bad):
+    numels, nd = LAYOUTS[case]
+    A, B = Mirror(numels, nd), Mirror(numels, nd)
+    grads = grads_of(A, BF, ("skip", case))
+    grads[nd - 1][0] = bad            # element 0 of parameter 0
+    ws, rec = A.plan.norm_workspace(), zsp.clip_record()
+    for kind in ("l2", "max"):
+        A.plan.reduce_norm(zsp.ALL_RANKS, grads, rec, ws, max_norm=1.0, kind=kind)
+        assert np.isnan(rec_of(rec)[2])
+        A.plan.reduce_adam_step_clip(zsp.ALL_RANKS, grads, rec, step=1, **HP)
+        A.plan.reduce_shard_norm(zsp.ALL_RANKS, grads, rec, ws, max_norm=1.0, kind=kind)
+        assert np.isnan(rec_of(rec)[2])
+        A.plan.adam_step_clip(zsp.ALL_RANKS, rec, step=1, **HP)
+        same_state(A, B, "skipped", STATE[:4])
+
+
+# ---- as they are used ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("case", [0, 5, 7])
+def test_a_run_of_clipped_steps(case):
+    """Three steps, each of two micro-batches reduced layer by layer, the last
+    with its norms; the records joined; the clipped update; the gather. A twin
+    does it with unclipped calls, its coefficient taken on the host."""
+    numels, nd = LAYOUTS[case]
+    A, B = Mirror(numels, nd), Mirror(numels, nd)
+    T = len(numels)
+    half = max(1, T // 2)
+    groups = [(0, half)] + ([(half, T - half)] if T > half else [])
+    ws, parts, rec = A.plan.norm_workspace(), zsp.clip_record(len(groups)), zsp.clip_record()
+    at = real_mask(A.L, A.ranks)
+    out = [torch.empty(max(A.L.total_numel, 8), dtype=BF, device=dev()) for _ in range(2)]
+    for step in (1, 2, 3):
+        mb = [grads_of(A, BF, ("run", case, step, i)) for i in range(2)]
+        A.plan.reduce_shard(zsp.ALL_RANKS, mb[0])
+        for i, (first, n) in enumerate(groups):
+            A.plan.reduce_shard_norm_params(zsp.ALL_RANKS, first, n, mb[1], parts[i:i + 1], ws,
+                                            accumulate=True)
+        zsp.clip_combine(parts, rec, max_norm=0.5)
+        A.plan.adam_step_clip(zsp.ALL_RANKS, rec, step=step, **HP)
+        B.plan.reduce_shard(zsp.ALL_RANKS, mb[0])
+        B.plan.reduce_shard(zsp.ALL_RANKS, mb[1], accumulate=True)
+        vals = np_of(B.g_acc)[at]
+        check_record(rec, vals, "l2", 0.5)
+        assert rec_of(rec)[2] < 1
+        B.g_acc.mul_(float(rec_of(rec)[2]))
+        B.plan.adam_step(zsp.ALL_RANKS, step=step, **HP)
+        same_state(A, B, f"step {step}", STATE[:4])
+        for M, o in zip((A, B), out):
+            M.plan.gather_range(0, T, o[:A.L.total_numel])
+        assert_bits(np_of(out[0][:A.L.total_numel]), np_of(out[1][:A.L.total_numel]), "gathered")
+
+
+def test_stage_one_replica():
+    """Gradients completed on every rank (the accumulator gathered), their norm
+    and clipping as a list: the norm of the sharded accumulator."""
+    numels, nd = [1003, 64, 5, 3 * 4096 + 1, 777], 4
+    M = Mirror(numels, nd)
+    grads = grads_of(M, BF, "stage1")
+    ws, a, b = M.plan.norm_workspace(), zsp.clip_record(), zsp.clip_record()
+    M.plan.reduce_shard_norm(zsp.ALL_RANKS, grads, a, ws, max_norm=0.3)
+    flat = torch.empty(M.L.total_numel, device=dev())
+    M.plan.gather_range(0, len(numels), flat, "acc")
+    views = list(torch.split(flat, numels))            # any element offset
+    zsp.norm_many(views, b, ws, max_norm=0.3)
+    n = M.L.total_numel
+    assert abs(rec_of(a)[0] - rec_of(b)[0]) <= 2 * (n + 2) * 2.0 ** -53 * rec_of(a)[0]
+    want = flat * zsp.clip_values(b)[2]
+    zsp.TensorList(views).clip(b)
+    assert_bits(np_of(flat), np_of(want), "clipped replica")
+
+
+@pytest.mark.parametrize("case", [0, 5, 7])
+def test_capture_and_replay(case):
+    """A clipped step and a clipped list captured into a graph; each of three
+    replays equals the eager calls made between them, with gradients that
+    change from replay to replay."""
+    numels, nd = LAYOUTS[case]
+    A, B = Mirror(numels, nd), Mirror(numels, nd)
+    grads = grads_of(A, BF, ("graph", case), poison=False)
+    _, xs = make_list(SIZES[7], [(BF, FP)[i % 2] for i in range(len(SIZES[7]))], "graph", 1)
+    _, ys = make_list(SIZES[7], [(BF, FP)[i % 2] for i in range(len(SIZES[7]))], "graph", 1)
+    la, lb = zsp.TensorList(xs), zsp.TensorList(ys)
+    wa, wb = A.plan.norm_workspace(), B.plan.norm_workspace()
+    ra, rb = zsp.clip_record(4), zsp.clip_record(4)
+    torch.cuda.synchronize()
+
+    def step(M, tl, ts, ws, rec, stream):
+        M.plan.reduce_shard_norm(zsp.ALL_RANKS, grads, rec[0:1], ws, max_norm=0.1, stream=stream)
+        M.plan.adam_step_clip(zsp.ALL_RANKS, rec[0:1], step=3, stream=stream, **HP)
+        M.plan.reduce_norm(zsp.ALL_RANKS, grads, rec[1:2], ws, use_acc=True, max_norm=0.2,
+                           kind="max", stream=stream)
+        M.plan.reduce_adam_step_clip(zsp.ALL_RANKS, grads, rec[1:2], step=4, use_acc=True,
+                                     stream=stream, **HP)
+        M.plan.grad_norm(zsp.ALL_RANKS, rec[2:3], ws, stream=stream)
+        tl.norm(rec[2:3], ws, max_norm=0.05, stream=stream)
+        tl.clip(rec[2:3], stream=stream)
+        zsp.norm_many(ts, rec[3:4], ws, max_norm=0.04, stream=stream)
+        zsp.clip_many(ts, rec[3:4], stream=stream)
+        zsp.clip_combine(rec, rec[3:4], max_norm=1.0, stream=stream)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            step(A, la, xs, wa, ra, s)
+    torch.cuda.synchronize()
+    scratch = torch.empty(1 << 20, device=dev())
+    for rep in range(3):
+        for r in range(nd):
+            grads[r].mul_(1.25)
+        for x, y in zip(xs, ys):
+            x.mul_(2.0)
+            y.mul_(2.0)
+        torch.cuda.synchronize()
+        g.replay()
+        step(B, lb, ys, wb, rb, torch.cuda.current_stream())
+        scratch.uniform_()
+        torch.cuda.synchronize()
+        same_state(A, B, f"replay {rep}")
+        assert torch.equal(ra.view(torch.int64), rb.view(torch.int64)), f"replay {rep}"
+        for x, y in zip(xs, ys):
+            assert_bits(np_of(x), np_of(y), f"replay {rep}: list")
+    del g
+
+
+def test_two_streams_and_the_caller_s_stream():
+    """Norms on two streams at once, each with its own workspace, behind slow
+    work that makes their inputs."""
+    _, xs = make_list([1 << 20, 70000], [FP, BF], "streams")
+    tl = zsp.TensorList(xs)
+    numels, nd = [50021, 511, 1025], 8
+    M = Mirror(numels, nd)
+    want = zsp.clip_record(2)
+    ws = [M.plan.norm_workspace() for _ in range(2)]
+    M.g_acc.fill_(0.5)
+    tl.norm(want[0:1], ws[0])
+    M.plan.grad_norm(zsp.ALL_RANKS, want[1:2], ws[0])
+    got = zsp.clip_record(2)
+    M.g_acc.zero_()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            torch.empty(1 << 26, device=dev()).normal_()
+            M.g_acc.fill_(0.5)
+            M.plan.grad_norm(zsp.ALL_RANKS, got[1:2], ws[1], stream=s1)
+        for _ in range(5):
+            tl.norm(got[0:1], ws[0], stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int64), want.view(torch.int64))
+
+
+def test_equal_inputs_give_equal_bits():
+    numels, nd = LAYOUTS[7]
+    M = Mirror(numels, nd)
+    grads = grads_of(M, BF, "again")
+    recs, ws = zsp.clip_record(8), M.plan.norm_workspace()
+    for i in range(8):
+        M.plan.reduce_shard_norm(zsp.ALL_RANKS, grads, recs[i:i + 1], ws)
+    assert len(set(recs[:, 0].tolist())) == 1
+
+
+# ---- refusals on a bound plan ----------------------------------------------------------
+
+def test_refusals_on_a_bound_plan():
+    M = Mirror([100, 7], 4)
+    h = M.plan.handle
+    N = Mirror([100, 7], 4, with_acc=False)
+    R = Mirror([100, 7], 4, rank_local=1)
+    lib = binding.lib
+    rec = zsp.clip_record()
+    ws = M.plan.norm_workspace()
+    W, B = ws.data_ptr(), ws.numel()
+    out = rec.data_ptr()
+    g = (ctypes.c_void_p * 4)(*[M.g_master.data_ptr()] * 4)
+    E, RG, S = binding.EINVAL, binding.ERANGE, binding.ESTATE
+
+    def norms(kind=0, max_norm=1.0, w=W, b=B, o=out):
+        n = (kind, max_norm, w, b, o, None)
+        return {lib.zsp_grad_norm(h, -1, *n), lib.zsp_grad_norm_params(h, -1, 0, 1, *n),
+                lib.zsp_reduce_shard_norm(h, -1, g, 0, 1, 0, *n),
+                lib.zsp_reduce_shard_norm_params(h, -1, 0, 1, g, 0, 1, 0, *n),
+                lib.zsp_reduce_norm(h, -1, g, 0, 1, 0, *n)}
+
+    M.g_acc.fill_(2.0)
+    assert norms(kind=2) == {E} and norms(max_norm=-1.0) == {E}
+    assert norms(max_norm=float("nan")) == {E}
+    assert norms(w=None) == {E} and norms(w=W + 8) == {E} and norms(b=B - 8) == {RG}
+    assert norms(o=None) == {E} and norms(o=out + 8) == {E}
+    n = (0, 1.0, W, B, out, None)
+    hp = (1e-3, 0.9, 0.999, 1e-8, 1, None)
+    bad0 = (1e-3, 0.9, 0.999, 1e-8, 0, None)
+    assert lib.zsp_grad_norm_params(h, -1, 1, 2, *n) == RG
+    assert lib.zsp_grad_norm_params(h, -1, 0, 0, *n) == RG
+    assert lib.zsp_grad_norm(h, 4, *n) == E
+    assert lib.zsp_reduce_norm(h, -1, None, 0, 1, 0, *n) == E
+    assert lib.zsp_reduce_norm(h, -1, g, 2, 1, 0, *n) == E
+    assert lib.zsp_adam_step_clip(h, -1, out, *bad0) == E
+    assert lib.zsp_adam_step_clip(h, -1, out + 4, *hp) == E
+    assert lib.zsp_adam_step_clip_params(h, -1, 2, 1, out, *hp) == RG
+    assert lib.zsp_reduce_adam_step_clip(h, -1, g, 0, 1, 0, None, *hp) == E
+    nh = N.plan.handle
+    assert lib.zsp_grad_norm(nh, -1, *n) == S
+    assert lib.zsp_reduce_shard_norm(nh, -1, g, 0, 1, 0, *n) == S
+    assert lib.zsp_reduce_norm(nh, -1, g, 0, 1, 1, *n) == S
+    assert lib.zsp_adam_step_clip(nh, -1, out, *hp) == S
+    assert lib.zsp_reduce_adam_step_clip(nh, -1, g, 0, 1, 1, out, *hp) == S
+    rh = R.plan.handle
+    assert lib.zsp_grad_norm(rh, 0, *n) == S and lib.zsp_grad_norm(rh, -1, *n) == S
+    torch.cuda.synchronize()
+    assert (M.g_acc == 2.0).all() and not rec.any()
+
+
+def test_binding_refuses_wrong_tensors():
+    ws, rec = zsp.norm_workspace(), zsp.clip_record()
+    x = torch.zeros(8, 8, device=dev())
+    with pytest.raises(ValueError):
+        zsp.norm_many([x.t()], rec, ws)
+    with pytest.raises(TypeError):
+        zsp.norm_many([x.half()], rec, ws)
+    with pytest.raises(ValueError):
+        zsp.norm_many([x.cpu()], rec, ws)
+    with pytest.raises(TypeError):
+        zsp.norm_many([x], rec.float(), ws)
+    with pytest.raises(ValueError):
+        zsp.norm_many([x], zsp.clip_record(2), ws)
+    with pytest.raises(ValueError):
+        zsp.clip_many([x], torch.zeros(1, 2, dtype=torch.float64))
+    with pytest.raises(zsp.ZspError):
+        zsp.norm_many([x], rec, ws[:-16])
+    with pytest.raises(KeyError):
+        zsp.norm_many([x], rec, ws, kind="l1")
+    tl = zsp.TensorList([x])
+    tl.close()
+    with pytest.raises(ValueError):
+        tl.norm(rec, ws)

@@ -18,6 +18,7 @@ OK, EINVAL, ERANGE, ENOMEM, EHIP, ESTATE, EIO = 0, -1, -2, -3, -4, -5, -6
 F32, BF16 = 0, 1
 GRADS_FULL, GRADS_SHARD = 0, 1
 SRC_WORK, SRC_MASTER, SRC_ACC = 0, 1, 2
+NORM_L2, NORM_MAX = 0, 1
 ALL_RANKS = -1
 MAX_RANKS = 256
 
@@ -62,6 +63,26 @@ def _load():
         "zsp_gather_list_create": (i32, [vp, i32p, i32, i32, vpp, vp, ctypes.POINTER(vp)]),
         "zsp_gather_list_run": (i32, [vp, vp]),
         "zsp_gather_list_destroy": (None, [vp]),
+        "zsp_norm_workspace": (i32, [vp, i64p]),
+        "zsp_grad_norm": (i32, [vp, i32, i32, f32, vp, i64, vp, vp]),
+        "zsp_grad_norm_params": (i32, [vp, i32, i32, i32, i32, f32, vp, i64, vp, vp]),
+        "zsp_reduce_shard_norm": (i32, [vp, i32, vpp, i32, i32, i32, i32, f32, vp, i64, vp, vp]),
+        "zsp_reduce_shard_norm_params": (i32, [vp, i32, i32, i32, vpp, i32, i32, i32, i32, f32,
+                                               vp, i64, vp, vp]),
+        "zsp_reduce_norm": (i32, [vp, i32, vpp, i32, i32, i32, i32, f32, vp, i64, vp, vp]),
+        "zsp_clip_combine": (i32, [vp, i32, i32, f32, vp, vp]),
+        "zsp_adam_step_clip": (i32, [vp, i32, vp, f32, f32, f32, f32, i64, vp]),
+        "zsp_adam_step_clip_params": (i32, [vp, i32, i32, i32, vp, f32, f32, f32, f32, i64, vp]),
+        "zsp_reduce_adam_step_clip": (i32, [vp, i32, vpp, i32, i32, i32, vp, f32, f32, f32, f32,
+                                            i64, vp]),
+        "zsp_reduce_adam_step_clip_params": (i32, [vp, i32, i32, i32, vpp, i32, i32, i32, vp, f32,
+                                                   f32, f32, f32, i64, vp]),
+        "zsp_norm_many": (i32, [vpp, i64p, i32p, i32, i32, f32, vp, i64, vp, vp]),
+        "zsp_clip_many": (i32, [vpp, i64p, i32p, i32, vp, vp]),
+        "zsp_tensor_list_create": (i32, [vpp, i64p, i32p, i32, vp, ctypes.POINTER(vp)]),
+        "zsp_tensor_list_norm": (i32, [vp, i32, f32, vp, i64, vp, vp]),
+        "zsp_tensor_list_clip": (i32, [vp, vp, vp]),
+        "zsp_tensor_list_destroy": (None, [vp]),
         "zsp_checkpoint_write_host": (i32, [vp, i32, ctypes.c_char_p, i64, vp, vp, vp, vp]),
         "zsp_checkpoint_read_host": (i32, [vp, i32, ctypes.c_char_p, i64p, vp, vp, vp, vp]),
         "zsp_checkpoint_save": (i32, [vp, i32, ctypes.c_char_p, i64, vp]),
@@ -352,6 +373,219 @@ def zsp_checkpoint_load(h, rank, directory, stream=None):
     return step.value
 
 
+# ---- gradient norm and clipping ----------------------------------------------
+
+_KINDS = {"l2": NORM_L2, "max": NORM_MAX, NORM_L2: NORM_L2, NORM_MAX: NORM_MAX}
+
+
+def clip_record(n=1, device="cuda"):
+    """n clip records (zsp_clip) in device memory: a float64 tensor [n, 2]
+    whose second column holds the norm and the coefficient, two float32 each.
+    clip_values() gives the fields as views; parts[i:i + 1] is one record."""
+    return torch.zeros(n, 2, dtype=torch.float64, device=device)
+
+
+def clip_values(rec):
+    """(total, norm, coef) of records: views of shape [n], no copy, no wait."""
+    f = rec.view(torch.float32)
+    return rec[:, 0], f[:, 2], f[:, 3]
+
+
+def _here(t, what):
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}; the current device is "
+                         f"{torch.cuda.current_device()}")
+
+
+def _rec(rec, what, n=1):
+    p = _ptr(rec, torch.float64, what)
+    if rec.numel() != 2 * n:
+        raise ValueError(f"{what} must be {'one clip record' if n == 1 else f'{n} clip records'}")
+    _here(rec, what)
+    return p
+
+
+def _norm_args(out, ws, max_norm, kind, stream):
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous torch tensor on the GPU")
+    _here(ws, "ws")
+    return (_KINDS[kind], float(max_norm), ctypes.c_void_p(ws.data_ptr()),
+            ws.numel() * ws.element_size(), _rec(out, "out"), _stream(stream))
+
+
+def zsp_norm_workspace(h=None):
+    """Bytes of workspace the norm calls on plan handle h need; without one,
+    those on lists of tensors."""
+    n = ctypes.c_int64()
+    _check(lib.zsp_norm_workspace(h, ctypes.byref(n)))
+    return n.value
+
+
+def norm_workspace(device="cuda"):
+    """A workspace for norms of lists of tensors (Plan.norm_workspace: of a
+    plan's gradients). Calls that may run at the same time, or captured graphs
+    that may be replayed so, each need their own."""
+    return torch.empty(zsp_norm_workspace(), dtype=torch.uint8, device=device)
+
+
+def zsp_grad_norm(h, rank, out, ws, max_norm=float("inf"), kind="l2", stream=None):
+    _check(lib.zsp_grad_norm(h, int(rank), *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_grad_norm_params(h, rank, first, n, out, ws, max_norm=float("inf"), kind="l2",
+                         stream=None):
+    _check(lib.zsp_grad_norm_params(h, int(rank), int(first), int(n),
+                                    *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_reduce_shard_norm(h, n_d, rank, grads, out, ws, layout="full", accumulate=False,
+                          max_norm=float("inf"), kind="l2", stream=None, min_elems=0):
+    arr, code = _grad_array(grads, n_d, min_elems)
+    _check(lib.zsp_reduce_shard_norm(h, int(rank), arr, code, _LAYOUTS[layout],
+                                     int(bool(accumulate)),
+                                     *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_reduce_shard_norm_params(h, n_d, rank, first, n, grads, out, ws, layout="full",
+                                 accumulate=False, max_norm=float("inf"), kind="l2", stream=None,
+                                 min_elems=0):
+    arr, code = _grad_array(grads, n_d, min_elems)
+    _check(lib.zsp_reduce_shard_norm_params(h, int(rank), int(first), int(n), arr, code,
+                                            _LAYOUTS[layout], int(bool(accumulate)),
+                                            *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_reduce_norm(h, n_d, rank, grads, out, ws, layout="full", use_acc=False,
+                    max_norm=float("inf"), kind="l2", stream=None, min_elems=0):
+    arr, code = _grad_array(grads, n_d, min_elems)
+    _check(lib.zsp_reduce_norm(h, int(rank), arr, code, _LAYOUTS[layout], int(bool(use_acc)),
+                               *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_clip_combine(parts, out, max_norm=float("inf"), kind="l2", stream=None):
+    n = parts.shape[0] if isinstance(parts, torch.Tensor) and parts.dim() == 2 else 1
+    _check(lib.zsp_clip_combine(_rec(parts, "parts", n), n, _KINDS[kind], float(max_norm),
+                                _rec(out, "out"), _stream(stream)))
+
+
+clip_combine = zsp_clip_combine
+
+
+def zsp_adam_step_clip(h, rank, clip, lr, beta1, beta2, eps, step, stream=None):
+    _check(lib.zsp_adam_step_clip(h, int(rank), _rec(clip, "clip"), float(lr), float(beta1),
+                                  float(beta2), float(eps), int(step), _stream(stream)))
+
+
+def zsp_adam_step_clip_params(h, rank, first, n, clip, lr, beta1, beta2, eps, step, stream=None):
+    _check(lib.zsp_adam_step_clip_params(h, int(rank), int(first), int(n), _rec(clip, "clip"),
+                                         float(lr), float(beta1), float(beta2), float(eps),
+                                         int(step), _stream(stream)))
+
+
+def zsp_reduce_adam_step_clip(h, n_d, rank, grads, clip, lr, beta1, beta2, eps, step,
+                              layout="full", use_acc=False, stream=None, min_elems=0):
+    arr, code = _grad_array(grads, n_d, min_elems)
+    _check(lib.zsp_reduce_adam_step_clip(h, int(rank), arr, code, _LAYOUTS[layout],
+                                         int(bool(use_acc)), _rec(clip, "clip"), float(lr),
+                                         float(beta1), float(beta2), float(eps), int(step),
+                                         _stream(stream)))
+
+
+def zsp_reduce_adam_step_clip_params(h, n_d, rank, first, n, grads, clip, lr, beta1, beta2, eps,
+                                     step, layout="full", use_acc=False, stream=None,
+                                     min_elems=0):
+    arr, code = _grad_array(grads, n_d, min_elems)
+    _check(lib.zsp_reduce_adam_step_clip_params(h, int(rank), int(first), int(n), arr, code,
+                                                _LAYOUTS[layout], int(bool(use_acc)),
+                                                _rec(clip, "clip"), float(lr), float(beta1),
+                                                float(beta2), float(eps), int(step),
+                                                _stream(stream)))
+
+
+def _tensor_arrays(tensors):
+    n = len(tensors)
+    dev = torch.cuda.current_device()
+    ptrs, sizes, codes = [], [], []
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"tensors[{i}] must be a torch tensor")
+        codes.append(_dtype_code(t))
+        if not t.is_contiguous():
+            raise ValueError(f"tensors[{i}] must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"tensors[{i}] is on {t.device}; the current device is {dev}")
+        ptrs.append(t.data_ptr())
+        sizes.append(t.numel())
+    m = max(n, 1)
+    return ((ctypes.c_void_p * m)(*ptrs), (ctypes.c_int64 * m)(*sizes),
+            (ctypes.c_int32 * m)(*codes), n)
+
+
+def zsp_norm_many(tensors, out, ws, max_norm=float("inf"), kind="l2", stream=None):
+    """Norm of a list of tensors (float32 and bfloat16, contiguous) taken
+    together, into the record `out`."""
+    _check(lib.zsp_norm_many(*_tensor_arrays(tensors),
+                             *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_clip_many(tensors, clip, stream=None):
+    """Every tensor of the list times the record's coefficient, in place."""
+    _check(lib.zsp_clip_many(*_tensor_arrays(tensors), _rec(clip, "clip"), _stream(stream)))
+
+
+norm_many, clip_many = zsp_norm_many, zsp_clip_many
+
+
+def zsp_tensor_list_create(tensors, stream=None):
+    out = ctypes.c_void_p()
+    _check(lib.zsp_tensor_list_create(*_tensor_arrays(tensors), _stream(stream),
+                                      ctypes.byref(out)))
+    return out
+
+
+def zsp_tensor_list_norm(tl, out, ws, max_norm=float("inf"), kind="l2", stream=None):
+    _check(lib.zsp_tensor_list_norm(tl, *_norm_args(out, ws, max_norm, kind, stream)))
+
+
+def zsp_tensor_list_clip(tl, clip, stream=None):
+    _check(lib.zsp_tensor_list_clip(tl, _rec(clip, "clip"), _stream(stream)))
+
+
+def zsp_tensor_list_destroy(tl):
+    lib.zsp_tensor_list_destroy(tl)
+
+
+class TensorList:
+    """A list of tensors prepared once (zsp_tensor_list_create) for a caller
+    that takes the norm of the same gradients, and clips them, every step.
+    Keeps the tensors alive; frees the native list when collected or closed."""
+
+    def __init__(self, tensors, stream=None):
+        self._tl = None
+        self.tensors = list(tensors)
+        self._tl = zsp_tensor_list_create(self.tensors, stream)
+
+    def _live(self):
+        if self._tl is None:
+            raise ValueError("tensor list is closed")
+        return self._tl
+
+    def norm(self, out, ws, max_norm=float("inf"), kind="l2", stream=None):
+        zsp_tensor_list_norm(self._live(), out, ws, max_norm, kind, stream)
+
+    def clip(self, clip, stream=None):
+        zsp_tensor_list_clip(self._live(), clip, stream)
+
+    def close(self):
+        """Frees the native list; calls already enqueued must have finished."""
+        if getattr(self, "_tl", None) is not None:
+            zsp_tensor_list_destroy(self._tl)
+            self._tl = None
+
+    def __del__(self):
+        self.close()
+
+
 # ---- per-layer gather schedule -----------------------------------------------
 
 def _i32_array(xs):
@@ -578,6 +812,55 @@ class Plan:
                                 layout="full", use_acc=False, stream=None):
         zsp_reduce_adam_step_params(self._h, self.n_d, rank, first, n, grads, lr, beta1, beta2,
                                     eps, step, layout, use_acc, stream, self._grad_elems(layout))
+
+    def norm_workspace(self, device="cuda"):
+        """A workspace for this plan's norm calls, as it is bound now."""
+        return torch.empty(zsp_norm_workspace(self._h), dtype=torch.uint8, device=device)
+
+    def grad_norm(self, rank, out, ws, max_norm=float("inf"), kind="l2", stream=None):
+        """The accumulator's norm into the clip record `out`."""
+        zsp_grad_norm(self._h, rank, out, ws, max_norm, kind, stream)
+
+    def grad_norm_params(self, rank, first, n, out, ws, max_norm=float("inf"), kind="l2",
+                         stream=None):
+        zsp_grad_norm_params(self._h, rank, first, n, out, ws, max_norm, kind, stream)
+
+    def reduce_shard_norm(self, rank, grads, out, ws, layout="full", accumulate=False,
+                          max_norm=float("inf"), kind="l2", stream=None):
+        """reduce_shard, with the norm of what it writes."""
+        zsp_reduce_shard_norm(self._h, self.n_d, rank, grads, out, ws, layout, accumulate,
+                              max_norm, kind, stream, self._grad_elems(layout))
+
+    def reduce_shard_norm_params(self, rank, first, n, grads, out, ws, layout="full",
+                                 accumulate=False, max_norm=float("inf"), kind="l2", stream=None):
+        zsp_reduce_shard_norm_params(self._h, self.n_d, rank, first, n, grads, out, ws, layout,
+                                     accumulate, max_norm, kind, stream,
+                                     self._grad_elems(layout))
+
+    def reduce_norm(self, rank, grads, out, ws, layout="full", use_acc=False,
+                    max_norm=float("inf"), kind="l2", stream=None):
+        """The norm of the gradient reduce_adam_step would use; writes only `out`."""
+        zsp_reduce_norm(self._h, self.n_d, rank, grads, out, ws, layout, use_acc, max_norm, kind,
+                        stream, self._grad_elems(layout))
+
+    def adam_step_clip(self, rank, clip, lr, beta1, beta2, eps, step, stream=None):
+        zsp_adam_step_clip(self._h, rank, clip, lr, beta1, beta2, eps, step, stream)
+
+    def adam_step_clip_params(self, rank, first, n, clip, lr, beta1, beta2, eps, step,
+                              stream=None):
+        zsp_adam_step_clip_params(self._h, rank, first, n, clip, lr, beta1, beta2, eps, step,
+                                  stream)
+
+    def reduce_adam_step_clip(self, rank, grads, clip, lr, beta1, beta2, eps, step, layout="full",
+                              use_acc=False, stream=None):
+        zsp_reduce_adam_step_clip(self._h, self.n_d, rank, grads, clip, lr, beta1, beta2, eps,
+                                  step, layout, use_acc, stream, self._grad_elems(layout))
+
+    def reduce_adam_step_clip_params(self, rank, first, n, grads, clip, lr, beta1, beta2, eps,
+                                     step, layout="full", use_acc=False, stream=None):
+        zsp_reduce_adam_step_clip_params(self._h, self.n_d, rank, first, n, grads, clip, lr,
+                                         beta1, beta2, eps, step, layout, use_acc, stream,
+                                         self._grad_elems(layout))
 
     def gather(self, param_id, out, source="work", stream=None):
         if 0 <= param_id < len(self.numel):

@@ -164,6 +164,25 @@ zsp_status set_hip_error(hipError_t e, const char* what) { return fail_hip(e, wh
 
 zsp_status check_bound(const zsp_plan* P) { return ::check_bound(P); }
 
+zsp_status check_clip(const zsp_clip* clip, const char* what) {
+    if (!clip) return fail(ZSP_EINVAL, "%s is NULL", what);
+    if (!aligned16(clip)) return fail(ZSP_EINVAL, "%s is not 16-byte aligned", what);
+    return ZSP_OK;
+}
+
+zsp_status check_norm(const NormCall& c, int64_t parts) {
+    if (c.kind != ZSP_NORM_L2 && c.kind != ZSP_NORM_MAX)
+        return fail(ZSP_EINVAL, "bad norm kind %d", c.kind);
+    if (!(c.max_norm >= 0.0f))
+        return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", double(c.max_norm));
+    if (!c.ws) return fail(ZSP_EINVAL, "ws is NULL");
+    if (!aligned16(c.ws)) return fail(ZSP_EINVAL, "ws is not 16-byte aligned");
+    if (c.ws_bytes < norm_ws_bytes(parts))
+        return fail(ZSP_ERANGE, "workspace of %lld bytes; %lld are needed",
+                    (long long)c.ws_bytes, (long long)norm_ws_bytes(parts));
+    return check_clip(c.out, "out");
+}
+
 }  // namespace zsp
 
 extern "C" {
@@ -188,6 +207,7 @@ zsp_status zsp_partition(const int64_t* numel, int32_t n_params, int32_t n_d, zs
         P->flat_off.assign(n_params + 1, 0);
         P->piece_off.assign(n_params + 1, 0);
         P->slot_off.assign(n_params + 1, 0);
+        P->pad_off.assign(n_params + 1, 0);
         const int64_t kMax = int64_t(1) << 60;
         for (int32_t t = 0; t < n_params; ++t) {
             const int64_t n = numel[t];
@@ -209,6 +229,7 @@ zsp_status zsp_partition(const int64_t* numel, int32_t n_params, int32_t n_d, zs
             const int64_t s_t = P->shard_len[t];
             P->piece_off[t + 1] = P->piece_off[t] + (n == 0 ? 0 : (n + s_t - 1) / s_t);
             P->slot_off[t + 1] = P->slot_off[t] + (s_t > 0 ? 1 : 0);
+            P->pad_off[t + 1] = P->pad_off[t] + pad;
         }
         P->S = P->shard_off[n_params];
         P->total_padded = P->full_off[n_params];
@@ -413,46 +434,129 @@ zsp_status param_spans(const zsp_plan* P, int32_t rank_or_all, int32_t first, in
     if (n < 1 || first < 0 || first > P->T - n)
         return fail(ZSP_ERANGE, "parameters [%d, %d+%d) outside [0, %d)", first, first, n, P->T);
     spans->clear();
-    if (first == 0 && n == P->T) {
-        spans->emplace_back(b, e);
-        return ZSP_OK;
+    try {
+        if (first == 0 && n == P->T) {
+            spans->emplace_back(b, e);
+            return ZSP_OK;
+        }
+        const int64_t lo = P->shard_off[size_t(first)], hi = P->shard_off[size_t(first + n)];
+        for (int64_t base = b; base < e; base += P->S) spans->emplace_back(base + lo, base + hi);
+    } catch (const std::bad_alloc&) {
+        return fail(ZSP_ENOMEM, "out of host memory");
     }
-    const int64_t lo = P->shard_off[size_t(first)], hi = P->shard_off[size_t(first + n)];
-    for (int64_t base = b; base < e; base += P->S) spans->emplace_back(base + lo, base + hi);
     return ZSP_OK;
 }
 
+// One launch per span; the norm ops' partials of the spans follow one another.
 zsp_status launch_spans(zsp::ShardLaunch L, const std::vector<std::pair<int64_t, int64_t>>& spans,
                         zsp::ShardOp op, zsp_dtype dtype, void* stream, const char* what) {
+    double* const part = L.part;
     for (const auto& sp : spans) {
         L.e_begin = sp.first;
         L.e_end = sp.second;
+        if (L.nparts) L.part = part + *L.nparts;
         const hipError_t e = zsp::launch_shard_op(L, op, dtype, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return fail_hip(e, what);
     }
     return ZSP_OK;
 }
 
+// Partials that the norm calls on a plan may write, and so its workspace.
+int64_t plan_parts(const zsp_plan* P) {
+    const bool one = P->bound && P->bind_rank != ZSP_ALL_RANKS;
+    return zsp::norm_parts(one ? P->S : int64_t(P->nd) * P->S, P->nd);
+}
+
+zsp_status finish_norm(const zsp_plan* P, const zsp::NormCall& nc, int64_t nparts, void* stream) {
+    const hipError_t e =
+        zsp::launch_finish(static_cast<double*>(nc.ws), nparts, plan_parts(P), nc.kind,
+                           nc.max_norm, nc.out, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail_hip(e, "norm launch");
+    return ZSP_OK;
+}
+
+// nc: also the norm of the accumulator elements written, or NULL.
 zsp_status reduce_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n,
                          const void* const* grads, zsp_dtype dtype, zsp_grad_layout layout,
-                         int32_t accumulate, void* stream) {
+                         int32_t accumulate, const zsp::NormCall* nc, void* stream) {
     zsp_status st = check_bound(P);
     if (st != ZSP_OK) return st;
     if (!P->acc) return fail(ZSP_ESTATE, "reduce_shard needs a bound grad_acc");
     std::vector<std::pair<int64_t, int64_t>> spans;
     if ((st = param_spans(P, rank_or_all, first, n, &spans)) != ZSP_OK) return st;
     if ((st = check_grads(P, grads, dtype, layout)) != ZSP_OK) return st;
+    if (nc && (st = zsp::check_norm(*nc, plan_parts(P))) != ZSP_OK) return st;
     zsp::ShardLaunch L = base_launch(P);
     L.grads = grads;
     L.shard_layout = layout == ZSP_GRADS_SHARD;
     L.grad_len = grad_len(P, layout);
     L.short_pieces = short_pieces(P, first, n);
-    return launch_spans(L, spans, accumulate ? zsp::OP_REDUCE_ACC : zsp::OP_REDUCE_SET, dtype,
-                        stream, "reduce launch");
+    if (!nc)
+        return launch_spans(L, spans, accumulate ? zsp::OP_REDUCE_ACC : zsp::OP_REDUCE_SET, dtype,
+                            stream, "reduce launch");
+    int64_t nparts = 0;
+    L.kind = nc->kind;
+    L.part = static_cast<double*>(nc->ws);
+    L.nparts = &nparts;
+    st = launch_spans(L, spans, accumulate ? zsp::OP_REDUCE_ACC_NORM : zsp::OP_REDUCE_SET_NORM,
+                      dtype, stream, "reduce launch");
+    return st != ZSP_OK ? st : finish_norm(P, *nc, nparts, stream);
 }
 
-zsp_status adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n, float lr,
-                       float beta1, float beta2, float eps, int64_t step, void* stream) {
+zsp_status reduce_norm(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
+                       zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
+                       const zsp::NormCall& nc, void* stream) {
+    zsp_status st = check_bound(P);
+    if (st != ZSP_OK) return st;
+    if (use_acc && !P->acc) return fail(ZSP_ESTATE, "use_acc needs a bound grad_acc");
+    std::vector<std::pair<int64_t, int64_t>> spans;
+    if ((st = param_spans(P, rank_or_all, 0, P->T, &spans)) != ZSP_OK) return st;
+    if ((st = check_grads(P, grads, dtype, layout)) != ZSP_OK) return st;
+    if ((st = zsp::check_norm(nc, plan_parts(P))) != ZSP_OK) return st;
+    zsp::ShardLaunch L = base_launch(P);
+    int64_t nparts = 0;
+    L.grads = grads;
+    L.shard_layout = layout == ZSP_GRADS_SHARD;
+    L.grad_len = grad_len(P, layout);
+    L.short_pieces = short_pieces(P, 0, P->T);
+    L.kind = nc.kind;
+    L.part = static_cast<double*>(nc.ws);
+    L.nparts = &nparts;
+    st = launch_spans(L, spans, use_acc ? zsp::OP_NORM_ACC : zsp::OP_NORM, dtype, stream,
+                      "reduce norm launch");
+    return st != ZSP_OK ? st : finish_norm(P, nc, nparts, stream);
+}
+
+zsp_status acc_norm(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n,
+                    const zsp::NormCall& nc, void* stream) {
+    zsp_status st = check_bound(P);
+    if (st != ZSP_OK) return st;
+    if (!P->acc) return fail(ZSP_ESTATE, "grad_norm reads grad_acc, which is not bound");
+    std::vector<std::pair<int64_t, int64_t>> spans;
+    if ((st = param_spans(P, rank_or_all, first, n, &spans)) != ZSP_OK) return st;
+    if ((st = zsp::check_norm(nc, plan_parts(P))) != ZSP_OK) return st;
+    zsp::AccNormLaunch L;
+    L.tab = P->shard;
+    L.acc = P->acc;
+    L.stride = P->S;
+    L.spans = static_cast<int32_t>(spans.size());  // none for a model without elements
+    if (!spans.empty()) {
+        L.e_begin = spans[0].first;
+        L.e_len = spans[0].second - spans[0].first;
+    }
+    L.pads = P->pad_off[size_t(first + n)] > P->pad_off[size_t(first)];
+    L.kind = nc.kind;
+    L.part = static_cast<double*>(nc.ws);
+    int64_t nparts = 0;
+    const hipError_t e = zsp::launch_acc_norm(L, &nparts, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail_hip(e, "norm launch");
+    return finish_norm(P, nc, nparts, stream);
+}
+
+// clip: a record whose coefficient scales the gradient, or NULL.
+zsp_status adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n,
+                       const zsp_clip* clip, float lr, float beta1, float beta2, float eps,
+                       int64_t step, void* stream) {
     zsp_status st = check_bound(P);
     if (st != ZSP_OK) return st;
     if (!P->acc) return fail(ZSP_ESTATE, "adam_step reads grad_acc, which is not bound");
@@ -460,14 +564,16 @@ zsp_status adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t 
     if ((st = param_spans(P, rank_or_all, first, n, &spans)) != ZSP_OK) return st;
     zsp::ShardLaunch L = base_launch(P);
     if ((st = adam_scalars(lr, beta1, beta2, eps, step, &L.hp)) != ZSP_OK) return st;
+    if (clip) L.coef = &clip->coef;
     L.short_pieces = short_pieces(P, first, n);
-    return launch_spans(L, spans, zsp::OP_ADAM, ZSP_F32, stream, "adam launch");
+    return launch_spans(L, spans, clip ? zsp::OP_ADAM_CLIP : zsp::OP_ADAM, ZSP_F32, stream,
+                        "adam launch");
 }
 
 zsp_status reduce_adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n,
                               const void* const* grads, zsp_dtype dtype, zsp_grad_layout layout,
-                              int32_t use_acc, float lr, float beta1, float beta2, float eps,
-                              int64_t step, void* stream) {
+                              int32_t use_acc, const zsp_clip* clip, float lr, float beta1,
+                              float beta2, float eps, int64_t step, void* stream) {
     zsp_status st = check_bound(P);
     if (st != ZSP_OK) return st;
     if (use_acc && !P->acc) return fail(ZSP_ESTATE, "use_acc needs a bound grad_acc");
@@ -480,8 +586,10 @@ zsp_status reduce_adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, i
     L.shard_layout = layout == ZSP_GRADS_SHARD;
     L.grad_len = grad_len(P, layout);
     L.short_pieces = short_pieces(P, first, n);
-    return launch_spans(L, spans, use_acc ? zsp::OP_FUSED_ACC : zsp::OP_FUSED, dtype, stream,
-                        "fused reduce+adam launch");
+    if (clip) L.coef = &clip->coef;
+    const zsp::ShardOp op = clip ? (use_acc ? zsp::OP_FUSED_ACC_CLIP : zsp::OP_FUSED_CLIP)
+                                 : (use_acc ? zsp::OP_FUSED_ACC : zsp::OP_FUSED);
+    return launch_spans(L, spans, op, dtype, stream, "fused reduce+adam launch");
 }
 
 }  // namespace
@@ -492,26 +600,27 @@ zsp_status zsp_reduce_shard(zsp_plan* P, int32_t rank_or_all, const void* const*
                             zsp_dtype dtype, zsp_grad_layout layout, int32_t accumulate,
                             void* stream) {
     return reduce_params(P, rank_or_all, 0, P ? P->T : 0, grads, dtype, layout, accumulate,
-                         stream);
+                         nullptr, stream);
 }
 
 zsp_status zsp_reduce_shard_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
                                    int32_t n_params, const void* const* grads, zsp_dtype dtype,
                                    zsp_grad_layout layout, int32_t accumulate, void* stream) {
     return reduce_params(P, rank_or_all, first_param, n_params, grads, dtype, layout,
-                         accumulate, stream);
+                         accumulate, nullptr, stream);
 }
 
 zsp_status zsp_adam_step(zsp_plan* P, int32_t rank_or_all, float lr, float beta1, float beta2,
                          float eps, int64_t step, void* stream) {
-    return adam_params(P, rank_or_all, 0, P ? P->T : 0, lr, beta1, beta2, eps, step, stream);
+    return adam_params(P, rank_or_all, 0, P ? P->T : 0, nullptr, lr, beta1, beta2, eps, step,
+                       stream);
 }
 
 zsp_status zsp_adam_step_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
                                 int32_t n_params, float lr, float beta1, float beta2, float eps,
                                 int64_t step, void* stream) {
-    return adam_params(P, rank_or_all, first_param, n_params, lr, beta1, beta2, eps, step,
-                       stream);
+    return adam_params(P, rank_or_all, first_param, n_params, nullptr, lr, beta1, beta2, eps,
+                       step, stream);
 }
 
 zsp_status zsp_reduce_adam_step(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
@@ -519,7 +628,7 @@ zsp_status zsp_reduce_adam_step(zsp_plan* P, int32_t rank_or_all, const void* co
                                 float lr, float beta1, float beta2, float eps, int64_t step,
                                 void* stream) {
     return reduce_adam_params(P, rank_or_all, 0, P ? P->T : 0, grads, dtype, layout, use_acc,
-                              lr, beta1, beta2, eps, step, stream);
+                              nullptr, lr, beta1, beta2, eps, step, stream);
 }
 
 zsp_status zsp_reduce_adam_step_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
@@ -528,7 +637,111 @@ zsp_status zsp_reduce_adam_step_params(zsp_plan* P, int32_t rank_or_all, int32_t
                                        float lr, float beta1, float beta2, float eps,
                                        int64_t step, void* stream) {
     return reduce_adam_params(P, rank_or_all, first_param, n_params, grads, dtype, layout,
-                              use_acc, lr, beta1, beta2, eps, step, stream);
+                              use_acc, nullptr, lr, beta1, beta2, eps, step, stream);
+}
+
+// ---- Gradient norm and clipped updates ----------------------------------------
+
+zsp_status zsp_norm_workspace(const zsp_plan* P, int64_t* bytes) {
+    if (!bytes) return fail(ZSP_EINVAL, "bytes is NULL");
+    *bytes = zsp::norm_ws_bytes(P ? plan_parts(P) : zsp::norm_parts(0, 0));
+    return ZSP_OK;
+}
+
+zsp_status zsp_grad_norm(zsp_plan* P, int32_t rank_or_all, zsp_norm_kind kind, float max_norm,
+                         void* ws, int64_t ws_bytes, zsp_clip* out, void* stream) {
+    return acc_norm(P, rank_or_all, 0, P ? P->T : 0,
+                    zsp::NormCall{kind, max_norm, ws, ws_bytes, out}, stream);
+}
+
+zsp_status zsp_grad_norm_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
+                                int32_t n_params, zsp_norm_kind kind, float max_norm, void* ws,
+                                int64_t ws_bytes, zsp_clip* out, void* stream) {
+    return acc_norm(P, rank_or_all, first_param, n_params,
+                    zsp::NormCall{kind, max_norm, ws, ws_bytes, out}, stream);
+}
+
+zsp_status zsp_reduce_shard_norm(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
+                                 zsp_dtype dtype, zsp_grad_layout layout, int32_t accumulate,
+                                 zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                                 zsp_clip* out, void* stream) {
+    const zsp::NormCall nc{kind, max_norm, ws, ws_bytes, out};
+    return reduce_params(P, rank_or_all, 0, P ? P->T : 0, grads, dtype, layout, accumulate, &nc,
+                         stream);
+}
+
+zsp_status zsp_reduce_shard_norm_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
+                                        int32_t n_params, const void* const* grads,
+                                        zsp_dtype dtype, zsp_grad_layout layout,
+                                        int32_t accumulate, zsp_norm_kind kind, float max_norm,
+                                        void* ws, int64_t ws_bytes, zsp_clip* out, void* stream) {
+    const zsp::NormCall nc{kind, max_norm, ws, ws_bytes, out};
+    return reduce_params(P, rank_or_all, first_param, n_params, grads, dtype, layout, accumulate,
+                         &nc, stream);
+}
+
+zsp_status zsp_reduce_norm(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
+                           zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
+                           zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                           zsp_clip* out, void* stream) {
+    return reduce_norm(P, rank_or_all, grads, dtype, layout, use_acc,
+                       zsp::NormCall{kind, max_norm, ws, ws_bytes, out}, stream);
+}
+
+zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+                            zsp_clip* out, void* stream) {
+    if (n < 0) return fail(ZSP_EINVAL, "n = %d is negative", n);
+    if (kind != ZSP_NORM_L2 && kind != ZSP_NORM_MAX) return fail(ZSP_EINVAL, "bad norm kind %d", kind);
+    if (!(max_norm >= 0.0f))
+        return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", double(max_norm));
+    zsp_status st = n > 0 ? zsp::check_clip(parts, "parts") : ZSP_OK;
+    if (st == ZSP_OK) st = zsp::check_clip(out, "out");
+    if (st != ZSP_OK) return st;
+    const hipError_t e =
+        zsp::launch_combine(parts, n, kind, max_norm, out, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail_hip(e, "combine launch");
+    return ZSP_OK;
+}
+
+zsp_status zsp_adam_step_clip(zsp_plan* P, int32_t rank_or_all, const zsp_clip* clip, float lr,
+                              float beta1, float beta2, float eps, int64_t step, void* stream) {
+    const zsp_status st = zsp::check_clip(clip, "clip");
+    return st != ZSP_OK ? st
+                        : adam_params(P, rank_or_all, 0, P ? P->T : 0, clip, lr, beta1, beta2, eps,
+                                      step, stream);
+}
+
+zsp_status zsp_adam_step_clip_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
+                                     int32_t n_params, const zsp_clip* clip, float lr,
+                                     float beta1, float beta2, float eps, int64_t step,
+                                     void* stream) {
+    const zsp_status st = zsp::check_clip(clip, "clip");
+    return st != ZSP_OK ? st
+                        : adam_params(P, rank_or_all, first_param, n_params, clip, lr, beta1,
+                                      beta2, eps, step, stream);
+}
+
+zsp_status zsp_reduce_adam_step_clip(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
+                                     zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
+                                     const zsp_clip* clip, float lr, float beta1, float beta2,
+                                     float eps, int64_t step, void* stream) {
+    const zsp_status st = zsp::check_clip(clip, "clip");
+    return st != ZSP_OK ? st
+                        : reduce_adam_params(P, rank_or_all, 0, P ? P->T : 0, grads, dtype, layout,
+                                             use_acc, clip, lr, beta1, beta2, eps, step, stream);
+}
+
+zsp_status zsp_reduce_adam_step_clip_params(zsp_plan* P, int32_t rank_or_all,
+                                            int32_t first_param, int32_t n_params,
+                                            const void* const* grads, zsp_dtype dtype,
+                                            zsp_grad_layout layout, int32_t use_acc,
+                                            const zsp_clip* clip, float lr, float beta1,
+                                            float beta2, float eps, int64_t step, void* stream) {
+    const zsp_status st = zsp::check_clip(clip, "clip");
+    return st != ZSP_OK
+               ? st
+               : reduce_adam_params(P, rank_or_all, first_param, n_params, grads, dtype, layout,
+                                    use_acc, clip, lr, beta1, beta2, eps, step, stream);
 }
 
 zsp_status zsp_gather_range(zsp_plan* P, int32_t first_param, int32_t n_params, zsp_source src,

@@ -17,6 +17,19 @@ zsp_status set_hip_error(hipError_t e, const char* what);
 // ZSP_OK if the plan has state bound on the current device, else the error.
 zsp_status check_bound(const zsp_plan* P);
 
+// What every norm call takes besides its data.
+struct NormCall {
+    zsp_norm_kind kind;
+    float max_norm;
+    void* ws;
+    int64_t ws_bytes;
+    zsp_clip* out;
+};
+// ZSP_OK if the arguments are good and ws holds `parts` partials.
+zsp_status check_norm(const NormCall& c, int64_t parts);
+// ZSP_OK if a record pointer is good.
+zsp_status check_clip(const zsp_clip* clip, const char* what);
+
 // Locates the no-alloc list gather's static device array on the current
 // device (zsp_noalloc.hip); ZSP_OK once done.
 zsp_status noalloc_setup();

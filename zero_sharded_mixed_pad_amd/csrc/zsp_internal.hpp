@@ -172,7 +172,16 @@ enum ShardOp : int {
     OP_REDUCE_ACC = 2,  // acc = acc + sum_r grads
     OP_FUSED = 3,       // g = sum_r grads; Adam; cast
     OP_FUSED_ACC = 4,   // g = acc + sum_r grads; Adam; cast
-    OP_ADAM = 5         // g = acc; Adam; cast
+    OP_ADAM = 5,        // g = acc; Adam; cast
+    // the reduces with the norm of what they write, and the norm alone
+    OP_REDUCE_SET_NORM = 6,
+    OP_REDUCE_ACC_NORM = 7,
+    OP_NORM = 8,      // sum_r grads: only its norm
+    OP_NORM_ACC = 9,  // acc + sum_r grads: only its norm
+    // the updates with g scaled by a clip record's coefficient
+    OP_FUSED_CLIP = 10,
+    OP_FUSED_ACC_CLIP = 11,
+    OP_ADAM_CLIP = 12
 };
 
 struct AdamScalars {
@@ -196,6 +205,13 @@ struct ShardLaunch {
     const void* const* grads = nullptr;  // host array of nd device pointers
     int64_t grad_len = 0;  // elements of each gradient buffer
     bool short_pieces = false;  // pieces in range average under kShortPiece elements
+    // OP_*_CLIP: the coefficient (device); a NaN leaves everything as it is.
+    const float* coef = nullptr;
+    // Norm ops: one partial per wave is written from part[0] on, and the
+    // launch adds their number to *nparts (host).
+    zsp_norm_kind kind = ZSP_NORM_L2;
+    double* part = nullptr;
+    int64_t* nparts = nullptr;
 };
 
 struct GatherLaunch {
@@ -307,6 +323,70 @@ hipError_t launch_shard_op(const ShardLaunch& L, ShardOp op, zsp_dtype dtype,
                            hipStream_t stream);
 // Launch a gather; dtype is the element type of src/out.
 hipError_t launch_gather(const GatherLaunch& L, zsp_dtype dtype, hipStream_t stream);
+
+// ---- Norms and clipping (zsp_norm.hip) --------------------------------------
+// A norm is computed in partials, one 64-bit value per wave or workgroup (a
+// sum of squares, or a largest absolute value), joined in a fixed order by
+// launch_finish. The workspace holds the partials, then kFoldBlocks more
+// that join a long list of them first.
+constexpr int kFoldBlocks = 256;
+constexpr int kNormBlocks = 2048;  // workgroups of an accumulator or list norm at most
+// Partials of a norm over E-space of `total` elements in at most nd spans:
+// two per tile a span meets, and what the accumulator norm needs.
+inline int64_t norm_parts(int64_t total, int32_t nd) {
+    const int64_t waves = 2 * (total / kTile) + 4 * int64_t(nd) + 4;
+    return waves > kNormBlocks + ZSP_MAX_RANKS ? waves : kNormBlocks + ZSP_MAX_RANKS;
+}
+inline int64_t norm_ws_bytes(int64_t parts) { return (parts + kFoldBlocks) * 8; }
+
+// The accumulator's norm over elements [e_begin + r*stride, e_begin + r*stride
+// + e_len) of E-space for r = 0 .. spans-1, pad slots left out; adds the
+// partials written to *nparts.
+struct AccNormLaunch {
+    ShardTable tab;
+    const float* acc = nullptr;
+    int64_t e_begin = 0, e_len = 0, stride = 0;
+    int32_t spans = 1;
+    bool pads = false;  // some slot in range may be a pad
+    zsp_norm_kind kind = ZSP_NORM_L2;
+    double* part = nullptr;
+};
+hipError_t launch_acc_norm(const AccNormLaunch& L, int64_t* nparts, hipStream_t stream);
+
+// Joins part[0 .. n) (in place; parts_cap partials, then the fold area) into
+// *out.
+hipError_t launch_finish(double* part, int64_t n, int64_t parts_cap, zsp_norm_kind kind,
+                         float max_norm, zsp_clip* out, hipStream_t stream);
+// Joins the totals of n records into *out.
+hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+                          zsp_clip* out, hipStream_t stream);
+
+// One chunk of a tensor of a list: n <= kListChunk elements from p on.
+constexpr int kListChunk = 4096;
+struct ListChunk {
+    void* p;
+    int32_t n;
+    int32_t dtype;  // zsp_dtype
+};
+// One tensor of a list short enough to travel in the kernel arguments.
+struct ArgTensor {
+    void* p;
+    int64_t numel_type;  // numel * 2 + dtype
+};
+constexpr int kTensorArgMax = 128;
+// A list of tensors: chunks in device memory, or tensors as arguments.
+struct TensorsLaunch {
+    const ListChunk* chunks = nullptr;
+    int64_t nchunk = 0;
+    int32_t n_args = 0;
+    ArgTensor args[kTensorArgMax];
+    int32_t chunk0[kTensorArgMax + 1];  // first chunk of each argument
+};
+// Partials of the list from part[0] on, *nparts of them; add: joined to the
+// *nparts that are there already (which a launch never lowers).
+hipError_t launch_list_norm(const TensorsLaunch& L, zsp_norm_kind kind, double* part,
+                            int64_t* nparts, bool add, hipStream_t stream);
+hipError_t launch_list_clip(const TensorsLaunch& L, const zsp_clip* clip, hipStream_t stream);
 
 // Host layout helpers (zsp_layout.cpp).
 int64_t pad_for(int64_t numel, int32_t nd);

@@ -170,6 +170,9 @@ struct ShardArgs {
     const void* src;
     AdamScalars hp;
     int32_t nd, shard_layout;
+    const float* coef;  // clipped updates
+    double* part;       // norm ops: one partial per wave
+    int32_t kind;       // norm ops: zsp_norm_kind
     const void* grads[CAP];
 };
 
@@ -185,14 +188,53 @@ __device__ __forceinline__ const void* grad_ptr(int r) {
     return reinterpret_cast<const void* const*>(seg + offsetof(ShardArgs<CAP>, grads))[r];
 }
 
-constexpr bool uses_grads(int op) {
-    return op == OP_REDUCE_SET || op == OP_REDUCE_ACC || op == OP_FUSED || op == OP_FUSED_ACC;
+constexpr bool has_norm(int op) {
+    return op == OP_REDUCE_SET_NORM || op == OP_REDUCE_ACC_NORM || op == OP_NORM ||
+           op == OP_NORM_ACC;
 }
+constexpr bool has_clip(int op) {
+    return op == OP_FUSED_CLIP || op == OP_FUSED_ACC_CLIP || op == OP_ADAM_CLIP;
+}
+// The gradient is the accumulator alone.
+constexpr bool from_acc(int op) { return op == OP_ADAM || op == OP_ADAM_CLIP; }
+constexpr bool uses_grads(int op) { return op != OP_COPYIN && !from_acc(op); }
 constexpr bool reads_acc(int op) {
-    return op == OP_REDUCE_ACC || op == OP_FUSED_ACC || op == OP_ADAM;
+    return from_acc(op) || op == OP_REDUCE_ACC || op == OP_FUSED_ACC ||
+           op == OP_REDUCE_ACC_NORM || op == OP_NORM_ACC || op == OP_FUSED_ACC_CLIP;
 }
-constexpr bool is_reduce(int op) { return op == OP_REDUCE_SET || op == OP_REDUCE_ACC; }
-constexpr bool is_adam(int op) { return op == OP_FUSED || op == OP_FUSED_ACC || op == OP_ADAM; }
+// Writes the accumulator.
+constexpr bool is_reduce(int op) {
+    return op == OP_REDUCE_SET || op == OP_REDUCE_ACC || op == OP_REDUCE_SET_NORM ||
+           op == OP_REDUCE_ACC_NORM;
+}
+constexpr bool is_adam(int op) {
+    return op == OP_FUSED || op == OP_FUSED_ACC || op == OP_ADAM || has_clip(op);
+}
+
+// What a wave keeps beside its tile: the clipping coefficient of a clipped
+// update; a norm op's running value. The sum of squares is held in 64 bits:
+// no square of a finite fp32 value leaves their range at either end, and the
+// rounding of a sum of 2^40 of them stays under the last rounding of the
+// norm to fp32. The largest absolute value is kept as its bit pattern, whose
+// integer order puts a NaN above everything.
+template <int OP>
+struct Tally {
+    float coef = 1.0f;
+    double sq = 0.0;
+    uint32_t mx = 0u;
+
+    __device__ __forceinline__ void add(float g, int kind) {
+        if constexpr (has_norm(OP)) {
+            if (kind == ZSP_NORM_MAX) mx = max(mx, __float_as_uint(g) & 0x7fffffffu);
+            else sq = __builtin_fma(double(g), double(g), sq);
+        }
+    }
+    // The gradient the update uses: one fp32 rounding of g * coef.
+    __device__ __forceinline__ float clipped(float g) const {
+        if constexpr (has_clip(OP)) return g * coef;
+        else return g;
+    }
+};
 
 // Sum over the N_d ranks, in rank order, of NQ quads per lane; quad h of
 // rank r starts at element base[h] + off[h] of grads[r]. When base[] is
@@ -277,7 +319,8 @@ __device__ __forceinline__ float reduce1(const ShardArgs<CAP>& a, int64_t sidx) 
 template <int OP, typename GT, int CAP, int NQ, bool TG>
 __device__ __forceinline__ void quads_fast(const ShardArgs<CAP>& a, const int64_t (&Eb)[NQ],
                                            const int64_t (&gb)[NQ], const int64_t (&ib)[NQ],
-                                           const uint32_t (&off)[NQ], const bool (&ok)[NQ]) {
+                                           const uint32_t (&off)[NQ], const bool (&ok)[NQ],
+                                           Tally<OP>& ty) {
     if constexpr (OP == OP_COPYIN) {
 #pragma unroll
         for (int h = 0; h < NQ; ++h) {
@@ -316,19 +359,28 @@ __device__ __forceinline__ void quads_fast(const ShardArgs<CAP>& a, const int64_
         for (int h = 0; h < NQ; ++h) {
 #pragma unroll
             for (int k = 0; k < kQuad; ++k) {
-                if constexpr (OP == OP_ADAM) g[h][k] = c[h][k];
+                if constexpr (from_acc(OP)) g[h][k] = c[h][k];
                 else if constexpr (reads_acc(OP)) g[h][k] = c[h][k] + g[h][k];
+            }
+        }
+        if constexpr (has_norm(OP)) {
+#pragma unroll
+            for (int h = 0; h < NQ; ++h) {
+                if (ok[h])
+#pragma unroll
+                    for (int k = 0; k < kQuad; ++k) ty.add(g[h][k], a.kind);
             }
         }
         if constexpr (is_reduce(OP)) {
 #pragma unroll
             for (int h = 0; h < NQ; ++h)
                 if (ok[h]) st_f32x4(a.acc + Eb[h] + off[h], g[h]);
-        } else {
+        } else if constexpr (is_adam(OP)) {
 #pragma unroll
             for (int h = 0; h < NQ; ++h) {
 #pragma unroll
-                for (int k = 0; k < kQuad; ++k) adam1(p[h][k], m[h][k], v[h][k], g[h][k], a.hp);
+                for (int k = 0; k < kQuad; ++k)
+                    adam1(p[h][k], m[h][k], v[h][k], ty.clipped(g[h][k]), a.hp);
                 if (ok[h]) {
                     st_f32x4(a.master + Eb[h] + off[h], p[h]);
                     st_f32x4(a.m + Eb[h] + off[h], m[h]);
@@ -356,7 +408,7 @@ __device__ __forceinline__ void quad_pad(const ShardArgs<CAP>& a, int64_t E) {
 
 template <int OP, typename GT, int CAP>
 __device__ __forceinline__ void elem_op(const ShardArgs<CAP>& a, int64_t e, bool valid,
-                                        const PieceInfo& pi) {
+                                        const PieceInfo& pi, Tally<OP>& ty) {
     if constexpr (OP == OP_COPYIN) {
         float x = 0.0f;
         uint16_t w = 0;
@@ -376,20 +428,25 @@ __device__ __forceinline__ void elem_op(const ShardArgs<CAP>& a, int64_t e, bool
         float r = 0.0f;
         if (valid) {
             r = reduce1<GT>(a, a.shard_layout ? e : e + pi.gdelta);
-            if constexpr (OP == OP_REDUCE_ACC) r = a.acc[e] + r;
+            if constexpr (reads_acc(OP)) r = a.acc[e] + r;
+            ty.add(r, a.kind);
         }
         a.acc[e] = r;
     } else {
         if (!valid) return;
         float g;
-        if constexpr (OP == OP_ADAM) {
+        if constexpr (from_acc(OP)) {
             g = a.acc[e];
         } else {
             g = reduce1<GT>(a, a.shard_layout ? e : e + pi.gdelta);
-            if constexpr (OP == OP_FUSED_ACC) g = a.acc[e] + g;
+            if constexpr (reads_acc(OP)) g = a.acc[e] + g;
+        }
+        if constexpr (has_norm(OP)) {
+            ty.add(g, a.kind);
+            return;
         }
         float p = a.master[e], m = a.m[e], v = a.v[e];
-        adam1(p, m, v, g, a.hp);
+        adam1(p, m, v, ty.clipped(g), a.hp);
         a.master[e] = p;
         a.m[e] = m;
         a.v[e] = v;
@@ -440,7 +497,7 @@ __device__ __forceinline__ int classify(const ShardArgs<CAP>& a, int64_t E, cons
 // elements keep their state bit for bit (they are loaded and stored back).
 template <int OP, typename GT, int CAP>
 __device__ __forceinline__ void quad_mixed(const ShardArgs<CAP>& a, int64_t E, int p, PieceInfo pi,
-                                           const PieceInfo* info) {
+                                           const PieceInfo* info, Tally<OP>& ty) {
     // Pad elements read element 0 of the same buffer instead (always valid
     // memory, value discarded), so that every load is issued unconditionally:
     // loads under a per-lane condition each get their own wait.
@@ -505,19 +562,20 @@ __device__ __forceinline__ void quad_mixed(const ShardArgs<CAP>& a, int64_t E, i
         }
 #pragma unroll
         for (int k = 0; k < kQuad; ++k) {
-            if constexpr (OP == OP_ADAM) g[k] = c4[k];
+            if constexpr (from_acc(OP)) g[k] = c4[k];
             else if constexpr (reads_acc(OP)) g[k] = c4[k] + g[k];
+            if (valid[k]) ty.add(g[k], a.kind);
         }
         if constexpr (is_reduce(OP)) {
             float r[kQuad];
 #pragma unroll
             for (int k = 0; k < kQuad; ++k) r[k] = valid[k] ? g[k] : 0.0f;
             st_f32x4(a.acc + E, r);
-        } else {
+        } else if constexpr (is_adam(OP)) {
 #pragma unroll
             for (int k = 0; k < kQuad; ++k) {
                 float pk = p4[k], mk = m4[k], vk = v4[k];
-                adam1(pk, mk, vk, g[k], a.hp);
+                adam1(pk, mk, vk, ty.clipped(g[k]), a.hp);
                 if (valid[k]) {
                     p4[k] = pk;
                     m4[k] = mk;
@@ -622,7 +680,7 @@ __device__ __forceinline__ void reduce_two(const ShardArgs<CAP>& a, const QuadPl
 // loaded with the rest and left alone.
 template <int OP, typename GT, int CAP, bool TG>
 __device__ __forceinline__ void quads_planned(const ShardArgs<CAP>& a, const int64_t (&E)[2],
-                                              const QuadPlan (&q)[2]) {
+                                              const QuadPlan (&q)[2], Tally<OP>& ty) {
     float p[2][kQuad], m[2][kQuad], v[2][kQuad], c[2][kQuad], g[2][kQuad];
     if constexpr (is_adam(OP)) {
 #pragma unroll
@@ -651,7 +709,7 @@ __device__ __forceinline__ void quads_planned(const ShardArgs<CAP>& a, const int
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int k = 0; k < kQuad; ++k) {
-            if constexpr (OP == OP_ADAM) g[h][k] = c[h][k];
+            if constexpr (from_acc(OP)) g[h][k] = c[h][k];
             else if constexpr (reads_acc(OP)) g[h][k] = c[h][k] + g[h][k];
         }
     }
@@ -659,12 +717,17 @@ __device__ __forceinline__ void quads_planned(const ShardArgs<CAP>& a, const int
     for (int h = 0; h < 2; ++h) {
         if (q[h].slow) continue;
         const uint32_t val = q[h].valid;
+        if constexpr (has_norm(OP)) {
+#pragma unroll
+            for (int k = 0; k < kQuad; ++k)
+                if ((val >> k) & 1u) ty.add(g[h][k], a.kind);
+        }
         if constexpr (is_reduce(OP)) {
             float r[kQuad];
 #pragma unroll
             for (int k = 0; k < kQuad; ++k) r[k] = (val >> k) & 1u ? g[h][k] : 0.0f;
             st_f32x4(a.acc + E[h], r);
-        } else {
+        } else if constexpr (is_adam(OP)) {
             if (val == 0u) continue;
             float pn[kQuad], mn[kQuad], vn[kQuad];
 #pragma unroll
@@ -672,7 +735,7 @@ __device__ __forceinline__ void quads_planned(const ShardArgs<CAP>& a, const int
                 pn[k] = p[h][k];
                 mn[k] = m[h][k];
                 vn[k] = v[h][k];
-                adam1(pn[k], mn[k], vn[k], g[h][k], a.hp);
+                adam1(pn[k], mn[k], vn[k], ty.clipped(g[h][k]), a.hp);
                 const bool ok = (val >> k) & 1u;
                 pn[k] = ok ? pn[k] : p[h][k];
                 mn[k] = ok ? mn[k] : m[h][k];
@@ -695,18 +758,18 @@ __device__ __forceinline__ void quads_planned(const ShardArgs<CAP>& a, const int
 // One quad of any kind; p is the index of its piece in `info`.
 template <int OP, typename GT, int CAP, bool TG>
 __device__ __forceinline__ void quad_one(const ShardArgs<CAP>& a, int64_t E, int kind, int p,
-                                         PieceInfo pi, const PieceInfo* info) {
+                                         PieceInfo pi, const PieceInfo* info, Tally<OP>& ty) {
     if (kind == Q_FAST) {
         const int64_t Eb[1] = {E};
         const int64_t gb[1] = {a.shard_layout ? E : E + pi.gdelta};
         const int64_t ib[1] = {E + pi.idelta};
         const uint32_t off[1] = {0u};
         const bool ok[1] = {true};
-        quads_fast<OP, GT, CAP, 1, TG>(a, Eb, gb, ib, off, ok);
+        quads_fast<OP, GT, CAP, 1, TG>(a, Eb, gb, ib, off, ok, ty);
     } else if (kind == Q_PAD) {
         quad_pad<OP, CAP>(a, E);
     } else if (kind == Q_MIXED) {
-        quad_mixed<OP, GT, CAP>(a, E, p, pi, info);
+        quad_mixed<OP, GT, CAP>(a, E, p, pi, info, ty);
     } else if (kind == Q_SLOW) {
         // Only quads that cross the call's range boundary: element by element,
         // touching nothing outside the range.
@@ -714,7 +777,7 @@ __device__ __forceinline__ void quad_one(const ShardArgs<CAP>& a, int64_t E, int
             const int64_t e = E + k;
             if (e < a.e_begin || e >= a.e_end) continue;
             while (e >= pi.end) pi = info[++p];
-            elem_op<OP, GT, CAP>(a, e, e < pi.vend, pi);
+            elem_op<OP, GT, CAP>(a, e, e < pi.vend, pi, ty);
         }
     }
 }
@@ -742,17 +805,8 @@ __device__ __forceinline__ int64_t xcd_run_tile(int64_t b) {
 // the 10,000-tensor fused step's read excess from +11.5% to +4.1% (all
 // bytes: +7.7% to +2.7%) for 0.7% of its time.
 template <int OP, typename GT, int CAP, int W, bool TG>
-__global__ __launch_bounds__(kWaveLanes) void shard_kernel(const ShardArgs<CAP> a) {
-    static_assert(W == 1 || W == 2, "one or two waves per tile");
-    __shared__ int64_t s_e0[kStage];
-    __shared__ PieceInfo s_info[kStage];
-    const int lane = threadIdx.x;
-    int64_t tile = a.tile_first + blockIdx.x / W;
-    if constexpr (W == 1 && TG) {
-        tile = a.tile_first + xcd_run_tile(blockIdx.x);
-        if (tile >= a.tile_end) return;  // the grid is rounded up to 8 runs
-    }
-    const int hw = W == 2 ? int(blockIdx.x % 2) : 0;
+__device__ __forceinline__ void shard_tile(const ShardArgs<CAP>& a, int64_t tile, int hw, int lane,
+                                           int64_t* s_e0, PieceInfo* s_info, Tally<OP>& ty) {
     const int64_t E0 = tile * kTile + int64_t(lane) * kQuad;
     // Wave-uniform bracket of the tile's pieces (scalar loads).
     const int lo = a.tile[tile];
@@ -771,14 +825,14 @@ __global__ __launch_bounds__(kWaveLanes) void shard_kernel(const ShardArgs<CAP> 
                 const int64_t ib[1] = {T0 + pi.idelta};
                 const uint32_t off[1] = {uint32_t(lane) * kQuad + uint32_t(hw) * uint32_t(kHalf)};
                 const bool ok[1] = {true};
-                quads_fast<OP, GT, CAP, 1, TG>(a, Eb, gb, ib, off, ok);
+                quads_fast<OP, GT, CAP, 1, TG>(a, Eb, gb, ib, off, ok, ty);
             } else {
                 const int64_t Eb[2] = {T0, T0};
                 const int64_t gb[2] = {gbase, gbase};
                 const int64_t ib[2] = {T0 + pi.idelta, T0 + pi.idelta};
                 const uint32_t off[2] = {uint32_t(lane) * kQuad, uint32_t(lane) * kQuad + kHalf};
                 const bool ok[2] = {true, true};
-                quads_fast<OP, GT, CAP, 2, TG>(a, Eb, gb, ib, off, ok);
+                quads_fast<OP, GT, CAP, 2, TG>(a, Eb, gb, ib, off, ok, ty);
             }
             return;
         }
@@ -815,11 +869,11 @@ __global__ __launch_bounds__(kWaveLanes) void shard_kernel(const ShardArgs<CAP> 
             const PieceInfo ia = info[pa], iz = info[pz];
             const QuadPlan q[2] = {plan_quad<OP>(a, E[0], pa, ia, info),
                                    plan_quad<OP>(a, E[1], pz, iz, info)};
-            quads_planned<OP, GT, CAP, TG>(a, E, q);
+            quads_planned<OP, GT, CAP, TG>(a, E, q, ty);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (h ? q[1].slow : q[0].slow)
-                    quad_mixed<OP, GT, CAP>(a, E[h], h ? pz : pa, h ? iz : ia, info);
+                    quad_mixed<OP, GT, CAP>(a, E[h], h ? pz : pa, h ? iz : ia, info, ty);
             }
             return;
         }
@@ -829,7 +883,47 @@ __global__ __launch_bounds__(kWaveLanes) void shard_kernel(const ShardArgs<CAP> 
         const int64_t E = E0 + h * kHalf;
         const int p = n == 1 ? 0 : find_local(e0, n, E);
         const PieceInfo pi = info[p];
-        quad_one<OP, GT, CAP, TG>(a, E, classify(a, E, pi), p, pi, info);
+        quad_one<OP, GT, CAP, TG>(a, E, classify(a, E, pi), p, pi, info, ty);
+    }
+}
+
+// The wave's value of a norm op, the same in every lane: a sum of squares in
+// a fixed order of lanes, or a largest absolute value.
+template <int OP>
+__device__ __forceinline__ double wave_norm(const Tally<OP>& ty, int kind) {
+    if (kind == ZSP_NORM_MAX) {
+        uint32_t m = ty.mx;
+#pragma unroll
+        for (int d = kWaveLanes / 2; d > 0; d /= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+        return double(__uint_as_float(m));
+    }
+    double s = ty.sq;
+#pragma unroll
+    for (int d = kWaveLanes / 2; d > 0; d /= 2) s += __shfl_xor(s, d);
+    return s;
+}
+
+template <int OP, typename GT, int CAP, int W, bool TG>
+__global__ __launch_bounds__(kWaveLanes) void shard_kernel(const ShardArgs<CAP> a) {
+    static_assert(W == 1 || W == 2, "one or two waves per tile");
+    __shared__ int64_t s_e0[kStage];
+    __shared__ PieceInfo s_info[kStage];
+    const int lane = threadIdx.x;
+    int64_t tile = a.tile_first + blockIdx.x / W;
+    if constexpr (W == 1 && TG) {
+        tile = a.tile_first + xcd_run_tile(blockIdx.x);
+        if (tile >= a.tile_end) return;  // the grid is rounded up to 8 runs
+    }
+    const int hw = W == 2 ? int(blockIdx.x % 2) : 0;
+    Tally<OP> ty;
+    if constexpr (has_clip(OP)) {
+        ty.coef = *a.coef;
+        if (ty.coef != ty.coef) return;  // the norm was not finite: the step is skipped
+    }
+    shard_tile<OP, GT, CAP, W, TG>(a, tile, hw, lane, s_e0, s_info, ty);
+    if constexpr (has_norm(OP)) {
+        const double t = wave_norm(ty, a.kind);
+        if (lane == 0) a.part[(tile - a.tile_first) * W + hw] = t;
     }
 }
 
@@ -1533,7 +1627,7 @@ size_t shard_lds_pad(const ShardLaunch& L, int64_t tiles) {
         if constexpr (W == 1) {
             if (!L.short_pieces || bytes < kShortCapBytes) return 0;
             total = kLdsShortPieces;
-        } else if constexpr (OP == OP_ADAM) {
+        } else if constexpr (from_acc(OP)) {
             total = kLdsAdamAlone;
         } else if constexpr (is_adam(OP)) {
             total = bytes >= kHeavyFusedBytes ? kLdsFusedHeavy : kLdsFused;
@@ -1582,6 +1676,9 @@ hipError_t launch_t(const ShardLaunch& L, hipStream_t stream) {
     a.nd = L.nd;
     a.shard_layout = L.shard_layout;
     a.glen = L.grad_len;
+    a.coef = L.coef;
+    a.part = L.part;
+    a.kind = L.kind;
     if constexpr (uses_grads(OP)) {
         for (int r = 0; r < L.nd; ++r) a.grads[r] = L.grads[r];
     }
@@ -1590,6 +1687,7 @@ hipError_t launch_t(const ShardLaunch& L, hipStream_t stream) {
     if constexpr (kHalfTiles<OP, CAP>) {
         if (!L.short_pieces && 2 * tiles <= kMaxBlocks) {
             const size_t lds_pad = shard_lds_pad<OP, GT, CAP, 2>(L, tiles);
+            if constexpr (has_norm(OP)) *L.nparts += 2 * tiles;
             hipLaunchKernelGGL((shard_kernel<OP, GT, CAP, 2, false>),
                                dim3(static_cast<uint32_t>(2 * tiles)), dim3(kWaveLanes), lds_pad,
                                stream, a);
@@ -1597,6 +1695,7 @@ hipError_t launch_t(const ShardLaunch& L, hipStream_t stream) {
         }
     }
     if (tiles > kMaxBlocks) return hipErrorInvalidValue;
+    if constexpr (has_norm(OP)) *L.nparts += tiles;
     const size_t lds_pad = shard_lds_pad<OP, GT, CAP, 1>(L, tiles);
     if constexpr (kTemporalShort<OP, CAP>) {
         if (L.short_pieces) {
@@ -1632,7 +1731,14 @@ hipError_t launch_dtype(const ShardLaunch& L, ShardOp op, hipStream_t stream) {
         case OP_REDUCE_ACC: return launch_cap<OP_REDUCE_ACC, GT>(L, stream);
         case OP_FUSED: return launch_cap<OP_FUSED, GT>(L, stream);
         case OP_FUSED_ACC: return launch_cap<OP_FUSED_ACC, GT>(L, stream);
-        case OP_ADAM: return launch_cap<OP_ADAM, GT>(L, stream);
+        case OP_REDUCE_SET_NORM: return launch_cap<OP_REDUCE_SET_NORM, GT>(L, stream);
+        case OP_REDUCE_ACC_NORM: return launch_cap<OP_REDUCE_ACC_NORM, GT>(L, stream);
+        case OP_NORM: return launch_cap<OP_NORM, GT>(L, stream);
+        case OP_NORM_ACC: return launch_cap<OP_NORM_ACC, GT>(L, stream);
+        case OP_FUSED_CLIP: return launch_cap<OP_FUSED_CLIP, GT>(L, stream);
+        case OP_FUSED_ACC_CLIP: return launch_cap<OP_FUSED_ACC_CLIP, GT>(L, stream);
+        case OP_ADAM:
+        case OP_ADAM_CLIP: break;  // no gradient type: launched by launch_shard_op
     }
     return hipErrorInvalidValue;
 }
@@ -1643,6 +1749,7 @@ hipError_t launch_shard_op(const ShardLaunch& L, ShardOp op, zsp_dtype dtype,
                            hipStream_t stream) {
     if (L.e_end <= L.e_begin) return hipSuccess;
     if (op == OP_ADAM) return launch_cap<OP_ADAM, float>(L, stream);
+    if (op == OP_ADAM_CLIP) return launch_cap<OP_ADAM_CLIP, float>(L, stream);
     if (dtype == ZSP_BF16) return launch_dtype<uint16_t>(L, op, stream);
     return launch_dtype<float>(L, op, stream);
 }

@@ -448,8 +448,8 @@ zsp_status zsp_reduce_adam_step_clip_params(zsp_plan* plan, int32_t rank_or_all,
  * kernel arguments, 128 per launch (launches follow one another on the
  * stream); a list that is used again and again is better prepared.
  * ZSP_EINVAL: n < 0, NULL arrays with n > 0, a negative numel, a bad dtype, a
- * NULL or misaligned tensor; ZSP_ERANGE: 2^31 chunks of 4096 elements or
- * more, counted per tensor. No plan is involved: all tensors, ws, out and
+ * NULL or misaligned tensor; ZSP_ERANGE: 2^31 chunks of 8 KiB or more,
+ * counted per tensor. No plan is involved: all tensors, ws, out and
  * clip are on the current device. */
 zsp_status zsp_norm_many(const void* const* x, const int64_t* numel, const int32_t* dtype,
                          int32_t n, zsp_norm_kind kind, float max_norm, void* ws,
@@ -459,7 +459,7 @@ zsp_status zsp_clip_many(void* const* x, const int64_t* numel, const int32_t* dt
 
 /* A list of tensors prepared once: zsp_tensor_list_create takes the arrays of
  * zsp_norm_many, with the same checks, and keeps on the current device a
- * record of 16 bytes per 4096 elements of each tensor (allocated, filled on
+ * record of 16 bytes per 8 KiB of each tensor (allocated, filled on
  * `stream` and waited for before it returns). _norm and _clip are then as
  * zsp_norm_many and zsp_clip_many, each over the whole list in one pass, and
  * need that device current (ZSP_ESTATE). The tensors must stay allocated.

@@ -361,8 +361,12 @@ hipError_t launch_finish(double* part, int64_t n, int64_t parts_cap, zsp_norm_ki
 hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
                           zsp_clip* out, hipStream_t stream);
 
-// One chunk of a tensor of a list: n <= kListChunk elements from p on.
-constexpr int kListChunk = 4096;
+// One chunk of a tensor of a list: n elements from p on, at most
+// kListChunkBytes of them.
+constexpr int kListChunkBytes = 8192;
+constexpr int64_t chunk_elems(int32_t dtype) {
+    return kListChunkBytes / (dtype == ZSP_BF16 ? 2 : 4);
+}
 struct ListChunk {
     void* p;
     int32_t n;

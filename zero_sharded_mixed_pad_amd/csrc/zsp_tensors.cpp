@@ -2,8 +2,7 @@
 // (zsp_norm_many, zsp_clip_many and the prepared zsp_tensor_list): argument
 // checks, chunk tables, launches.
 //
-// A list is cut into chunks of kListChunk elements, each inside one tensor;
-// a wave takes a chunk. A one-shot list travels in the kernel arguments,
+// A list is cut into chunks of kListChunkBytes, each inside one tensor. A one-shot list travels in the kernel arguments,
 // kTensorArgMax tensors with elements per launch: nothing is staged, so any
 // list can be captured into a HIP graph. Later launches of a long list join
 // their partials to the first one's. A prepared list keeps one record per
@@ -27,7 +26,10 @@ struct zsp_tensor_list {
 namespace zsp {
 namespace {
 
-int64_t chunks_of(int64_t numel) { return numel / kListChunk + (numel % kListChunk != 0); }
+int64_t chunks_of(int64_t numel, int32_t dtype) {
+    const int64_t c = chunk_elems(dtype);
+    return numel / c + (numel % c != 0);
+}
 int64_t size_of(int32_t dtype) { return dtype == ZSP_BF16 ? 2 : 4; }
 
 // Checks as zsp_norm_many documents them; the number of chunks.
@@ -46,10 +48,11 @@ zsp_status check_tensors(const void* const* x, const int64_t* numel, const int32
         if (!x[i]) return set_error(ZSP_EINVAL, "x[%d] is NULL", i);
         if (reinterpret_cast<uintptr_t>(x[i]) % uintptr_t(size_of(dtype[i])))
             return set_error(ZSP_EINVAL, "x[%d] is not aligned to its element type", i);
-        // each count is at most 2^51, so the sum cannot wrap before the check
-        c += chunks_of(numel[i]);
+        // each count is at most 2^52, so the sum cannot wrap before the check
+        c += chunks_of(numel[i], dtype[i]);
         if (c > INT32_MAX)
-            return set_error(ZSP_ERANGE, "list of 2^31 chunks of %d elements or more", kListChunk);
+            return set_error(ZSP_ERANGE, "list of 2^31 chunks of %d bytes or more",
+                             kListChunkBytes);
     }
     *nchunk = c;
     return ZSP_OK;
@@ -94,7 +97,7 @@ zsp_status for_each_launch(const void* const* x, const int64_t* numel, const int
     for (int32_t i = 0; i < n; ++i) {
         if (numel[i] > 0) {
             L.args[L.n_args] = ArgTensor{const_cast<void*>(x[i]), numel[i] * 2 + dtype[i]};
-            L.nchunk += chunks_of(numel[i]);
+            L.nchunk += chunks_of(numel[i], dtype[i]);
             L.chunk0[++L.n_args] = static_cast<int32_t>(L.nchunk);
         }
         if (L.n_args > 0 && (L.n_args == kTensorArgMax || i == n - 1)) {
@@ -179,9 +182,9 @@ zsp_status zsp_tensor_list_create(void* const* x, const int64_t* numel, const in
         return set_error(ZSP_ENOMEM, "out of host memory (%lld chunks)", (long long)nchunk);
     }
     for (int32_t i = 0; i < n; ++i)
-        for (int64_t at = 0; at < numel[i]; at += kListChunk)
+        for (int64_t at = 0; at < numel[i]; at += chunk_elems(dtype[i]))
             host.push_back(ListChunk{static_cast<char*>(x[i]) + at * size_of(dtype[i]),
-                                     int32_t(std::min<int64_t>(kListChunk, numel[i] - at)),
+                                     int32_t(std::min(chunk_elems(dtype[i]), numel[i] - at)),
                                      dtype[i]});
     zsp_tensor_list* L = new (std::nothrow) zsp_tensor_list();
     if (!L) return set_error(ZSP_ENOMEM, "out of host memory");

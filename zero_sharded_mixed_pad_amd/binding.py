@@ -119,7 +119,9 @@ def _check(status):
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # torch.cuda.current_stream().cuda_stream, without making a Stream object
+        return ctypes.c_void_p(
+            torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -387,8 +389,8 @@ def clip_record(n=1, device="cuda"):
 
 def clip_values(rec):
     """(total, norm, coef) of records: views of shape [n], no copy, no wait."""
-    f = rec.view(torch.float32)
-    return rec[:, 0], f[:, 2], f[:, 3]
+    _, _, norm, coef = rec.view(torch.float32).unbind(1)
+    return rec[:, 0], norm, coef
 
 
 def _here(t, what):
@@ -583,7 +585,10 @@ class TensorList:
             self._tl = None
 
     def __del__(self):
-        self.close()
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 # ---- per-layer gather schedule -----------------------------------------------

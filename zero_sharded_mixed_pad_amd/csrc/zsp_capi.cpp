@@ -447,17 +447,29 @@ zsp_status param_spans(const zsp_plan* P, int32_t rank_or_all, int32_t first, in
     return ZSP_OK;
 }
 
-// One launch per span; the norm ops' partials of the spans follow one another.
 zsp_status launch_spans(zsp::ShardLaunch L, const std::vector<std::pair<int64_t, int64_t>>& spans,
                         zsp::ShardOp op, zsp_dtype dtype, void* stream, const char* what) {
-    double* const part = L.part;
     for (const auto& sp : spans) {
         L.e_begin = sp.first;
         L.e_end = sp.second;
-        if (L.nparts) L.part = part + *L.nparts;
         const hipError_t e = zsp::launch_shard_op(L, op, dtype, static_cast<hipStream_t>(stream));
         if (e != hipSuccess) return fail_hip(e, what);
     }
+    return ZSP_OK;
+}
+
+// The same for the norm and clip ops, whose launch takes every rank's span
+// (the spans are one, S apart).
+zsp_status launch_ranks(const zsp_plan* P, zsp::ShardLaunch L,
+                        const std::vector<std::pair<int64_t, int64_t>>& spans, zsp::ShardOp op,
+                        zsp_dtype dtype, void* stream, const char* what) {
+    if (spans.empty()) return ZSP_OK;
+    L.e_begin = spans[0].first;
+    L.e_end = spans[0].second;
+    L.spans = static_cast<int32_t>(spans.size());
+    L.stride = P->S;
+    const hipError_t e = zsp::launch_shard_op(L, op, dtype, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail_hip(e, what);
     return ZSP_OK;
 }
 
@@ -497,8 +509,9 @@ zsp_status reduce_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_
     int64_t nparts = 0;
     L.kind = nc->kind;
     L.part = static_cast<double*>(nc->ws);
+    L.ticket = zsp::norm_ticket(L.part, plan_parts(P));
     L.nparts = &nparts;
-    st = launch_spans(L, spans, accumulate ? zsp::OP_REDUCE_ACC_NORM : zsp::OP_REDUCE_SET_NORM,
+    st = launch_ranks(P, L, spans, accumulate ? zsp::OP_REDUCE_ACC_NORM : zsp::OP_REDUCE_SET_NORM,
                       dtype, stream, "reduce launch");
     return st != ZSP_OK ? st : finish_norm(P, *nc, nparts, stream);
 }
@@ -521,8 +534,9 @@ zsp_status reduce_norm(zsp_plan* P, int32_t rank_or_all, const void* const* grad
     L.short_pieces = short_pieces(P, 0, P->T);
     L.kind = nc.kind;
     L.part = static_cast<double*>(nc.ws);
+    L.ticket = zsp::norm_ticket(L.part, plan_parts(P));
     L.nparts = &nparts;
-    st = launch_spans(L, spans, use_acc ? zsp::OP_NORM_ACC : zsp::OP_NORM, dtype, stream,
+    st = launch_ranks(P, L, spans, use_acc ? zsp::OP_NORM_ACC : zsp::OP_NORM, dtype, stream,
                       "reduce norm launch");
     return st != ZSP_OK ? st : finish_norm(P, nc, nparts, stream);
 }
@@ -548,9 +562,11 @@ zsp_status acc_norm(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n,
     L.kind = nc.kind;
     L.part = static_cast<double*>(nc.ws);
     int64_t nparts = 0;
-    const hipError_t e = zsp::launch_acc_norm(L, &nparts, static_cast<hipStream_t>(stream));
+    bool done = false;
+    const hipError_t e = zsp::launch_acc_norm(L, nc.max_norm, nc.out, &nparts, &done,
+                                              static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail_hip(e, "norm launch");
-    return finish_norm(P, nc, nparts, stream);
+    return done ? ZSP_OK : finish_norm(P, nc, nparts, stream);
 }
 
 // clip: a record whose coefficient scales the gradient, or NULL.
@@ -564,10 +580,10 @@ zsp_status adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t 
     if ((st = param_spans(P, rank_or_all, first, n, &spans)) != ZSP_OK) return st;
     zsp::ShardLaunch L = base_launch(P);
     if ((st = adam_scalars(lr, beta1, beta2, eps, step, &L.hp)) != ZSP_OK) return st;
-    if (clip) L.coef = &clip->coef;
     L.short_pieces = short_pieces(P, first, n);
-    return launch_spans(L, spans, clip ? zsp::OP_ADAM_CLIP : zsp::OP_ADAM, ZSP_F32, stream,
-                        "adam launch");
+    if (!clip) return launch_spans(L, spans, zsp::OP_ADAM, ZSP_F32, stream, "adam launch");
+    L.coef = &clip->coef;
+    return launch_ranks(P, L, spans, zsp::OP_ADAM_CLIP, ZSP_F32, stream, "adam launch");
 }
 
 zsp_status reduce_adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, int32_t n,
@@ -586,10 +602,12 @@ zsp_status reduce_adam_params(zsp_plan* P, int32_t rank_or_all, int32_t first, i
     L.shard_layout = layout == ZSP_GRADS_SHARD;
     L.grad_len = grad_len(P, layout);
     L.short_pieces = short_pieces(P, first, n);
-    if (clip) L.coef = &clip->coef;
-    const zsp::ShardOp op = clip ? (use_acc ? zsp::OP_FUSED_ACC_CLIP : zsp::OP_FUSED_CLIP)
-                                 : (use_acc ? zsp::OP_FUSED_ACC : zsp::OP_FUSED);
-    return launch_spans(L, spans, op, dtype, stream, "fused reduce+adam launch");
+    if (!clip)
+        return launch_spans(L, spans, use_acc ? zsp::OP_FUSED_ACC : zsp::OP_FUSED, dtype, stream,
+                            "fused reduce+adam launch");
+    L.coef = &clip->coef;
+    return launch_ranks(P, L, spans, use_acc ? zsp::OP_FUSED_ACC_CLIP : zsp::OP_FUSED_CLIP, dtype,
+                        stream, "fused reduce+adam launch");
 }
 
 }  // namespace

@@ -193,6 +193,10 @@ struct ShardLaunch {
     ShardTable tab;
     int64_t e_begin = 0;  // processed range of E-space
     int64_t e_end = 0;
+    // Norm and clip ops: the range and its copies shifted by stride, 2 *
+    // stride, ..., spans in all, in one launch.
+    int32_t spans = 1;
+    int64_t stride = 0;
     float* master = nullptr;
     float* m = nullptr;
     float* v = nullptr;
@@ -207,10 +211,11 @@ struct ShardLaunch {
     bool short_pieces = false;  // pieces in range average under kShortPiece elements
     // OP_*_CLIP: the coefficient (device); a NaN leaves everything as it is.
     const float* coef = nullptr;
-    // Norm ops: one partial per wave is written from part[0] on, and the
-    // launch adds their number to *nparts (host).
+    // Norm ops: one partial per wave is written from part[0] on, and their
+    // number to *nparts (host).
     zsp_norm_kind kind = ZSP_NORM_L2;
     double* part = nullptr;
+    uint32_t* ticket = nullptr;
     int64_t* nparts = nullptr;
 };
 
@@ -327,17 +332,22 @@ hipError_t launch_gather(const GatherLaunch& L, zsp_dtype dtype, hipStream_t str
 // ---- Norms and clipping (zsp_norm.hip) --------------------------------------
 // A norm is computed in partials, one 64-bit value per wave or workgroup (a
 // sum of squares, or a largest absolute value), joined in a fixed order by
-// launch_finish. The workspace holds the partials, then kFoldBlocks more
-// that join a long list of them first.
+// launch_finish. The workspace holds the partials, kFoldBlocks more that join
+// a long list of them first, and the ticket by which the last of the
+// workgroups that do so knows itself: the launch that writes a long list
+// sets it to 0.
 constexpr int kFoldBlocks = 256;
-constexpr int kNormBlocks = 2048;  // workgroups of an accumulator or list norm at most
+constexpr int kNormBlocks = 4096;  // workgroups of an accumulator or list norm at most
 // Partials of a norm over E-space of `total` elements in at most nd spans:
 // two per tile a span meets, and what the accumulator norm needs.
 inline int64_t norm_parts(int64_t total, int32_t nd) {
     const int64_t waves = 2 * (total / kTile) + 4 * int64_t(nd) + 4;
     return waves > kNormBlocks + ZSP_MAX_RANKS ? waves : kNormBlocks + ZSP_MAX_RANKS;
 }
-inline int64_t norm_ws_bytes(int64_t parts) { return (parts + kFoldBlocks) * 8; }
+inline int64_t norm_ws_bytes(int64_t parts) { return (parts + kFoldBlocks) * 8 + 16; }
+inline uint32_t* norm_ticket(double* ws, int64_t parts) {
+    return reinterpret_cast<uint32_t*>(ws + parts + kFoldBlocks);
+}
 
 // The accumulator's norm over elements [e_begin + r*stride, e_begin + r*stride
 // + e_len) of E-space for r = 0 .. spans-1, pad slots left out; adds the
@@ -351,10 +361,13 @@ struct AccNormLaunch {
     zsp_norm_kind kind = ZSP_NORM_L2;
     double* part = nullptr;
 };
-hipError_t launch_acc_norm(const AccNormLaunch& L, int64_t* nparts, hipStream_t stream);
+// A norm small enough for one workgroup writes *out itself: *done.
+hipError_t launch_acc_norm(const AccNormLaunch& L, float max_norm, zsp_clip* out,
+                           int64_t* nparts, bool* done, hipStream_t stream);
 
-// Joins part[0 .. n) (in place; parts_cap partials, then the fold area) into
-// *out.
+// Partials that launch_finish takes without a ticket.
+constexpr int64_t kFinishMax = 8192;
+// Joins part[0 .. n) into *out; the workspace has room for parts_cap.
 hipError_t launch_finish(double* part, int64_t n, int64_t parts_cap, zsp_norm_kind kind,
                          float max_norm, zsp_clip* out, hipStream_t stream);
 // Joins the totals of n records into *out.
@@ -386,10 +399,15 @@ struct TensorsLaunch {
     ArgTensor args[kTensorArgMax];
     int32_t chunk0[kTensorArgMax + 1];  // first chunk of each argument
 };
-// Partials of the list from part[0] on, *nparts of them; add: joined to the
-// *nparts that are there already (which a launch never lowers).
+// Whether launch_list_norm_one takes a list of this many chunks.
+bool list_norm_is_small(int64_t nchunk);
+// The whole norm of a small list in one launch.
+hipError_t launch_list_norm_one(const TensorsLaunch& L, zsp_norm_kind kind, float max_norm,
+                                zsp_clip* out, hipStream_t stream);
+// Partials of the list from part[0] on, joined to the *nparts that are there
+// already; *nparts is never lowered.
 hipError_t launch_list_norm(const TensorsLaunch& L, zsp_norm_kind kind, double* part,
-                            int64_t* nparts, bool add, hipStream_t stream);
+                            int64_t* nparts, hipStream_t stream);
 hipError_t launch_list_clip(const TensorsLaunch& L, const zsp_clip* clip, hipStream_t stream);
 
 // Host layout helpers (zsp_layout.cpp).

@@ -55,6 +55,7 @@
 #include <type_traits>
 
 #include "zsp_internal.hpp"
+#include "zsp_wave.hpp"
 
 namespace zsp {
 namespace {
@@ -170,9 +171,13 @@ struct ShardArgs {
     const void* src;
     AdamScalars hp;
     int32_t nd, shard_layout;
-    const float* coef;  // clipped updates
-    double* part;       // norm ops: one partial per wave
-    int32_t kind;       // norm ops: zsp_norm_kind
+    // norm and clip ops (in_spans):
+    int64_t stride;      // from one span (blockIdx.y) to the next
+    int64_t span_tiles;  // tiles a span meets, at most
+    const float* coef;   // clipped updates
+    double* part;        // norm ops: one partial per wave
+    uint32_t* ticket;    // norm ops: set to 0 for the launch that joins them
+    int32_t kind;        // norm ops: zsp_norm_kind
     const void* grads[CAP];
 };
 
@@ -211,7 +216,11 @@ constexpr bool is_adam(int op) {
     return op == OP_FUSED || op == OP_FUSED_ACC || op == OP_ADAM || has_clip(op);
 }
 
-// What a wave keeps beside its tile: the clipping coefficient of a clipped
+// The launch takes the same run of several ranks' slots (blockIdx.y): ops
+// whose layer-by-layer calls are one launch for all ranks.
+constexpr bool in_spans(int op) { return has_norm(op) || has_clip(op); }
+
+// What a wave keeps beside its tile: the range of its span; the clipping coefficient of a clipped
 // update; a norm op's running value. The sum of squares is held in 64 bits:
 // no square of a finite fp32 value leaves their range at either end, and the
 // rounding of a sum of 2^40 of them stays under the last rounding of the
@@ -219,6 +228,7 @@ constexpr bool is_adam(int op) {
 // integer order puts a NaN above everything.
 template <int OP>
 struct Tally {
+    int64_t e_begin = 0, e_end = 0;
     float coef = 1.0f;
     double sq = 0.0;
     uint32_t mx = 0u;
@@ -363,7 +373,12 @@ __device__ __forceinline__ void quads_fast(const ShardArgs<CAP>& a, const int64_
                 else if constexpr (reads_acc(OP)) g[h][k] = c[h][k] + g[h][k];
             }
         }
-        if constexpr (has_norm(OP)) {
+        if constexpr (is_reduce(OP)) {
+#pragma unroll
+            for (int h = 0; h < NQ; ++h)
+                if (ok[h]) st_f32x4(a.acc + Eb[h] + off[h], g[h]);
+        }
+        if constexpr (has_norm(OP)) {  // the stores are on their way
 #pragma unroll
             for (int h = 0; h < NQ; ++h) {
                 if (ok[h])
@@ -371,11 +386,7 @@ __device__ __forceinline__ void quads_fast(const ShardArgs<CAP>& a, const int64_
                     for (int k = 0; k < kQuad; ++k) ty.add(g[h][k], a.kind);
             }
         }
-        if constexpr (is_reduce(OP)) {
-#pragma unroll
-            for (int h = 0; h < NQ; ++h)
-                if (ok[h]) st_f32x4(a.acc + Eb[h] + off[h], g[h]);
-        } else if constexpr (is_adam(OP)) {
+        if constexpr (is_adam(OP)) {
 #pragma unroll
             for (int h = 0; h < NQ; ++h) {
 #pragma unroll
@@ -480,10 +491,24 @@ __device__ __forceinline__ int find_local(const int64_t* e0, int n, int64_t E) {
     return lo;
 }
 
-template <int CAP>
-__device__ __forceinline__ int classify(const ShardArgs<CAP>& a, int64_t E, const PieceInfo& pi) {
-    if (E >= a.e_end || E + kQuad <= a.e_begin) return Q_OUT;
-    const bool inside = E >= a.e_begin && E + kQuad <= a.e_end;
+// The range the wave may touch.
+template <int OP, int CAP>
+__device__ __forceinline__ int64_t range_begin(const ShardArgs<CAP>& a, const Tally<OP>& ty) {
+    if constexpr (in_spans(OP)) return ty.e_begin;
+    else return a.e_begin;
+}
+template <int OP, int CAP>
+__device__ __forceinline__ int64_t range_end(const ShardArgs<CAP>& a, const Tally<OP>& ty) {
+    if constexpr (in_spans(OP)) return ty.e_end;
+    else return a.e_end;
+}
+
+template <int OP, int CAP>
+__device__ __forceinline__ int classify(const ShardArgs<CAP>& a, int64_t E, const PieceInfo& pi,
+                                        const Tally<OP>& ty) {
+    const int64_t rb = range_begin(a, ty), re = range_end(a, ty);
+    if (E >= re || E + kQuad <= rb) return Q_OUT;
+    const bool inside = E >= rb && E + kQuad <= re;
     if (!inside) return Q_SLOW;
     if (E + kQuad <= pi.vend) return Q_FAST;
     if (E >= pi.vend && E + kQuad <= pi.end) return Q_PAD;
@@ -775,7 +800,7 @@ __device__ __forceinline__ void quad_one(const ShardArgs<CAP>& a, int64_t E, int
         // touching nothing outside the range.
         for (int k = 0; k < kQuad; ++k) {
             const int64_t e = E + k;
-            if (e < a.e_begin || e >= a.e_end) continue;
+            if (e < range_begin(a, ty) || e >= range_end(a, ty)) continue;
             while (e >= pi.end) pi = info[++p];
             elem_op<OP, GT, CAP>(a, e, e < pi.vend, pi, ty);
         }
@@ -815,7 +840,7 @@ __device__ __forceinline__ void shard_tile(const ShardArgs<CAP>& a, int64_t tile
         // Whole tile inside one piece: the common case for large parameters.
         const PieceInfo pi = a.info[lo];
         const int64_t T0 = tile * kTile;
-        if (T0 >= a.e_begin && T0 + kTile <= a.e_end && T0 + kTile <= pi.vend) {
+        if (T0 >= range_begin(a, ty) && T0 + kTile <= range_end(a, ty) && T0 + kTile <= pi.vend) {
             // Every element real and in range: wave-uniform bases (scalar
             // registers) plus the lane's 32-bit offsets.
             const int64_t gbase = a.shard_layout ? T0 : T0 + pi.gdelta;
@@ -862,7 +887,7 @@ __device__ __forceinline__ void shard_tile(const ShardArgs<CAP>& a, int64_t tile
         // buffers, follow on their own. (Not for more than 16 ranks: the
         // registers it takes there would lower the waves per CU.)
         const int64_t T0 = tile * kTile;
-        if (T0 >= a.e_begin && T0 + kTile <= a.e_end) {
+        if (T0 >= range_begin(a, ty) && T0 + kTile <= range_end(a, ty)) {
             const int64_t E[2] = {E0, E0 + kHalf};
             const int pa = n == 1 ? 0 : find_local(e0, n, E[0]);
             const int pz = n == 1 ? 0 : find_local(e0, n, E[1]);
@@ -883,24 +908,15 @@ __device__ __forceinline__ void shard_tile(const ShardArgs<CAP>& a, int64_t tile
         const int64_t E = E0 + h * kHalf;
         const int p = n == 1 ? 0 : find_local(e0, n, E);
         const PieceInfo pi = info[p];
-        quad_one<OP, GT, CAP, TG>(a, E, classify(a, E, pi), p, pi, info, ty);
+        quad_one<OP, GT, CAP, TG>(a, E, classify(a, E, pi, ty), p, pi, info, ty);
     }
 }
 
-// The wave's value of a norm op, the same in every lane: a sum of squares in
-// a fixed order of lanes, or a largest absolute value.
+// The wave's value of a norm op.
 template <int OP>
 __device__ __forceinline__ double wave_norm(const Tally<OP>& ty, int kind) {
-    if (kind == ZSP_NORM_MAX) {
-        uint32_t m = ty.mx;
-#pragma unroll
-        for (int d = kWaveLanes / 2; d > 0; d /= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
-        return double(__uint_as_float(m));
-    }
-    double s = ty.sq;
-#pragma unroll
-    for (int d = kWaveLanes / 2; d > 0; d /= 2) s += __shfl_xor(s, d);
-    return s;
+    if (kind == ZSP_NORM_MAX) return wave_join(double(__uint_as_float(ty.mx)), JoinMax());
+    return wave_join(ty.sq, JoinSum());
 }
 
 template <int OP, typename GT, int CAP, int W, bool TG>
@@ -909,21 +925,39 @@ __global__ __launch_bounds__(kWaveLanes) void shard_kernel(const ShardArgs<CAP> 
     __shared__ int64_t s_e0[kStage];
     __shared__ PieceInfo s_info[kStage];
     const int lane = threadIdx.x;
-    int64_t tile = a.tile_first + blockIdx.x / W;
-    if constexpr (W == 1 && TG) {
-        tile = a.tile_first + xcd_run_tile(blockIdx.x);
-        if (tile >= a.tile_end) return;  // the grid is rounded up to 8 runs
-    }
     const int hw = W == 2 ? int(blockIdx.x % 2) : 0;
     Tally<OP> ty;
-    if constexpr (has_clip(OP)) {
-        ty.coef = *a.coef;
-        if (ty.coef != ty.coef) return;  // the norm was not finite: the step is skipped
-    }
-    shard_tile<OP, GT, CAP, W, TG>(a, tile, hw, lane, s_e0, s_info, ty);
-    if constexpr (has_norm(OP)) {
-        const double t = wave_norm(ty, a.kind);
-        if (lane == 0) a.part[(tile - a.tile_first) * W + hw] = t;
+    if constexpr (in_spans(OP)) {
+        const int64_t i = W == 1 && TG ? xcd_run_tile(blockIdx.x) : int64_t(blockIdx.x / W);
+        if (i >= a.span_tiles) return;  // the grid is rounded up to 8 runs
+        ty.e_begin = a.e_begin + int64_t(blockIdx.y) * a.stride;
+        ty.e_end = a.e_end + int64_t(blockIdx.y) * a.stride;
+        const int64_t tile = ty.e_begin / kTile + i;
+        // spans that start elsewhere in a tile may meet one tile less
+        const bool none = tile * kTile >= ty.e_end;
+        if constexpr (has_clip(OP)) {
+            ty.coef = *a.coef;
+            // NaN: the norm was not finite, the step is skipped
+            if (none || ty.coef != ty.coef) return;
+            shard_tile<OP, GT, CAP, W, TG>(a, tile, hw, lane, s_e0, s_info, ty);
+        } else {
+            if (!none) shard_tile<OP, GT, CAP, W, TG>(a, tile, hw, lane, s_e0, s_info, ty);
+            if (blockIdx.x == 0 && blockIdx.y == 0 && lane == 0) *a.ticket = 0u;
+            const double t = wave_norm(ty, a.kind);
+            // Workgroups go to the XCDs in turn, and a line of partials that
+            // several L2s write goes out in parts: neighbours in the array
+            // come from one XCD (in a TG launch they are on one as it is).
+            const int64_t n = a.span_tiles * W, at = i * W + hw, q = n / 8;
+            const int64_t to = TG || at >= q * 8 ? at : at % 8 * q + at / 8;
+            if (lane == 0) a.part[int64_t(blockIdx.y) * n + to] = t;
+        }
+    } else {
+        int64_t tile = a.tile_first + blockIdx.x / W;
+        if constexpr (W == 1 && TG) {
+            tile = a.tile_first + xcd_run_tile(blockIdx.x);
+            if (tile >= a.tile_end) return;  // the grid is rounded up to 8 runs
+        }
+        shard_tile<OP, GT, CAP, W, TG>(a, tile, hw, lane, s_e0, s_info, ty);
     }
 }
 
@@ -1598,6 +1632,19 @@ constexpr int kHeavyFusedBytes = 40;
 constexpr int kHeavyReduceBytes = 24;
 constexpr int kShortCapBytes = 16;
 constexpr int64_t kCapMinTiles = 8192;
+// The reduces with a norm stay longer after their stores, so more of them
+// are resident. Half-tile waves: 7168 bytes from 12 read per element (the
+// 202 M element layer, 8 ranks of bf16: 646 us, 673 at 10240 and 646 at no
+// cap; accumulating 772, 782 and 780), 10240 for a reduce of 24 or more (16
+// ranks: 1178 us, 1216 at 7168 and 1255 at 13312). Over short pieces: the
+// reduce 13312 from 12 bytes (10,000 tensors, 8 ranks: 341 us, 350 at no
+// cap), 16384 from 24 (16 ranks: 622 and 651); a norm alone is as fast
+// without a cap as with any. At 2 ranks of bf16 every cap costs (462 us
+// without, 530 at 7168).
+constexpr size_t kLdsNorm = 7168;
+constexpr size_t kLdsNormHeavy = 10240;
+constexpr size_t kLdsNormShort = 13312;
+constexpr int kNormCapBytes = 12;
 
 size_t device_lds_per_cu() {
     static std::atomic<int> cache[64];
@@ -1624,7 +1671,12 @@ size_t shard_lds_pad(const ShardLaunch& L, int64_t tiles) {
         const int grad = uses_grads(OP) ? L.nd * int(sizeof(GT)) : 0;
         const int bytes = grad + (is_adam(OP) ? 12 : 0) + (reads_acc(OP) ? 4 : 0);
         size_t total = 0;
-        if constexpr (W == 1) {
+        if constexpr (has_norm(OP)) {
+            if (bytes < kNormCapBytes || (W == 1 && (!L.short_pieces || !is_reduce(OP)))) return 0;
+            const bool heavy = bytes >= kHeavyReduceBytes;
+            if constexpr (W == 1) total = heavy ? kLdsShortPieces : kLdsNormShort;
+            else total = is_reduce(OP) && heavy ? kLdsNormHeavy : kLdsNorm;
+        } else if constexpr (W == 1) {
             if (!L.short_pieces || bytes < kShortCapBytes) return 0;
             total = kLdsShortPieces;
         } else if constexpr (from_acc(OP)) {
@@ -1676,39 +1728,49 @@ hipError_t launch_t(const ShardLaunch& L, hipStream_t stream) {
     a.nd = L.nd;
     a.shard_layout = L.shard_layout;
     a.glen = L.grad_len;
-    a.coef = L.coef;
-    a.part = L.part;
-    a.kind = L.kind;
     if constexpr (uses_grads(OP)) {
         for (int r = 0; r < L.nd; ++r) a.grads[r] = L.grads[r];
     }
-    const int64_t tiles = tile_end - a.tile_first;
+    int64_t tiles = tile_end - a.tile_first;
     if (tiles <= 0) return hipSuccess;
+    uint32_t spans = 1;
+    if constexpr (in_spans(OP)) {
+        // the most tiles a span meets, wherever in a tile it starts
+        if (L.spans > 1) tiles = (L.e_end - L.e_begin + kTile - 2) / kTile + 1;
+        spans = static_cast<uint32_t>(L.spans);
+        a.stride = L.stride;
+        a.span_tiles = tiles;
+        a.coef = L.coef;
+        a.part = L.part;
+        a.ticket = L.ticket;
+        a.kind = L.kind;
+    }
     if constexpr (kHalfTiles<OP, CAP>) {
         if (!L.short_pieces && 2 * tiles <= kMaxBlocks) {
-            const size_t lds_pad = shard_lds_pad<OP, GT, CAP, 2>(L, tiles);
-            if constexpr (has_norm(OP)) *L.nparts += 2 * tiles;
+            const size_t lds_pad = shard_lds_pad<OP, GT, CAP, 2>(L, tiles * spans);
+            if constexpr (has_norm(OP)) *L.nparts = 2 * tiles * spans;
             hipLaunchKernelGGL((shard_kernel<OP, GT, CAP, 2, false>),
-                               dim3(static_cast<uint32_t>(2 * tiles)), dim3(kWaveLanes), lds_pad,
-                               stream, a);
+                               dim3(static_cast<uint32_t>(2 * tiles), spans), dim3(kWaveLanes),
+                               lds_pad, stream, a);
             return hipGetLastError();
         }
     }
     if (tiles > kMaxBlocks) return hipErrorInvalidValue;
-    if constexpr (has_norm(OP)) *L.nparts += tiles;
-    const size_t lds_pad = shard_lds_pad<OP, GT, CAP, 1>(L, tiles);
+    if constexpr (has_norm(OP)) *L.nparts = tiles * spans;
+    const size_t lds_pad = shard_lds_pad<OP, GT, CAP, 1>(L, tiles * spans);
     if constexpr (kTemporalShort<OP, CAP>) {
         if (L.short_pieces) {
             const int64_t grid = (tiles + 8 * kXcdRun - 1) / (8 * kXcdRun) * (8 * kXcdRun);
             if (grid > kMaxBlocks) return hipErrorInvalidValue;
             hipLaunchKernelGGL((shard_kernel<OP, GT, CAP, 1, true>),
-                               dim3(static_cast<uint32_t>(grid)), dim3(kWaveLanes), lds_pad,
+                               dim3(static_cast<uint32_t>(grid), spans), dim3(kWaveLanes), lds_pad,
                                stream, a);
             return hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((shard_kernel<OP, GT, CAP, 1, false>), dim3(static_cast<uint32_t>(tiles)),
-                       dim3(kWaveLanes), lds_pad, stream, a);
+    hipLaunchKernelGGL((shard_kernel<OP, GT, CAP, 1, false>),
+                       dim3(static_cast<uint32_t>(tiles), spans), dim3(kWaveLanes), lds_pad,
+                       stream, a);
     return hipGetLastError();
 }
 

@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "zsp_internal.hpp"
+#include "zsp_wave.hpp"
 
 namespace zsp {
 namespace {
@@ -61,30 +62,23 @@ struct Acc {
     }
 };
 
-// Joins two partials (non-negative, or NaN with a clear sign).
 template <int KIND>
 __device__ __forceinline__ double join(double a, double b) {
-    if constexpr (KIND == ZSP_NORM_MAX) {
-        const uint64_t x = __double_as_longlong(a), y = __double_as_longlong(b);
-        return __longlong_as_double(x > y ? x : y);
-    } else {
-        return a + b;
-    }
+    if constexpr (KIND == ZSP_NORM_MAX) return JoinMax()(a, b);
+    else return JoinSum()(a, b);
 }
 
 // A wave's partial, the same in every lane.
 template <int KIND>
-__device__ __forceinline__ double wave_join(double v) {
-#pragma unroll
-    for (int d = kWaveLanes / 2; d > 0; d /= 2) v = join<KIND>(v, __shfl_xor(v, d));
-    return v;
+__device__ __forceinline__ double wave_value(double v) {
+    return wave_join(v, [](double a, double b) { return join<KIND>(a, b); });
 }
 
 // The workgroup's partial, valid in thread 0.
 template <int KIND, int THREADS>
 __device__ __forceinline__ double block_join(double v) {
     __shared__ double s_part[THREADS / kWaveLanes];
-    v = wave_join<KIND>(v);
+    v = wave_value<KIND>(v);
     const int wave = threadIdx.x / kWaveLanes;
     if (threadIdx.x % kWaveLanes == 0) s_part[wave] = v;
     __syncthreads();
@@ -92,6 +86,22 @@ __device__ __forceinline__ double block_join(double v) {
         for (int w = 1; w < THREADS / kWaveLanes; ++w) v = join<KIND>(v, s_part[w]);
     return v;
 }
+
+__device__ __forceinline__ void write_record(double total, int kind, float max_norm,
+                                             zsp_clip* out) {
+    const double norm = kind == ZSP_NORM_MAX ? total : __builtin_sqrt(total);
+    float coef = 1.0f;
+    if (!(norm <= 1.7976931348623157e308)) coef = __builtin_nanf("");
+    else if (norm > double(max_norm)) coef = float(double(max_norm) / norm);
+    out->total = total;
+    out->norm = float(norm);
+    out->coef = coef;
+}
+
+// The form of a small norm: one workgroup, one batch of loads per wave at
+// most, and no second launch to join partials.
+constexpr int kOneThreads = 1024;
+constexpr int kOneWaves = kOneThreads / kWaveLanes;
 
 // Lists: 16 bytes at any 2-byte offset. Every byte is read once here, and
 // the non-temporal hint raised the read rate of a 0.8 GB norm from 6.3 to
@@ -101,8 +111,10 @@ __device__ __forceinline__ u32x4 ld16(const char* p) {
 }
 
 // ---- The accumulator's norm ----------------------------------------------------
-// One wave per workgroup; a wave takes groups of kGroup elements (one batch
-// of loads), every gridDim.x-th one of its rank's span. No load of the
+// A wave takes groups of kGroup elements (one batch of loads), every n-th one
+// of its rank's span, n the waves of the span. One wave per workgroup; a norm
+// of at most kOneWaves groups is one workgroup, which writes the record
+// itself. No load of the
 // accumulator waits for a table: a group inside one piece needs the table
 // only to know that, and one that meets pad slots marks them in a bitmap in
 // LDS, a lane per piece, and zeroes what it loaded there.
@@ -117,15 +129,24 @@ struct AccNormArgs {
     int64_t ntile;
     int64_t e_begin, e_len, stride;
     double* part;
+    float max_norm;  // of the form that writes the record
+    zsp_clip* out;
 };
 
 // Marks the pad slots of the group at G0, which meets pieces lo .. hi: bit
-// i % 32 of word i / 32 for element G0 + i. No wave reads another's bits.
+// i % 32 of word i / 32 for element G0 + i. The words are the wave's own, and
+// a wave's LDS operations run in order: the fences hold the compiler to that.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ void mark_pads(const AccNormArgs& a, int64_t G0, int lo, int hi,
                                           int lane, uint32_t* bits) {
     static_assert(kGroup / 32 == kWaveLanes, "a word per lane");
+    wave_sync();
     bits[lane] = 0u;
-    __syncthreads();
+    wave_sync();
     for (int p = lo + lane; p <= hi; p += kWaveLanes) {
         const PieceInfo pi = a.info[p];
         int64_t b = pi.vend - G0, e = pi.end - G0;
@@ -138,16 +159,20 @@ __device__ __forceinline__ void mark_pads(const AccNormArgs& a, int64_t G0, int 
             b += n;
         }
     }
-    __syncthreads();
+    wave_sync();
 }
 
-template <int KIND, bool PADS>
-__global__ __launch_bounds__(kWaveLanes) void acc_norm_kernel(const AccNormArgs a) {
-    __shared__ uint32_t s_bits[kGroup / 32];
-    const int lane = threadIdx.x;
+template <int KIND, bool PADS, bool ONE>
+__global__ __launch_bounds__(ONE ? kOneThreads : kWaveLanes) void acc_norm_kernel(
+    const AccNormArgs a) {
+    __shared__ uint32_t s_all[PADS ? (ONE ? kOneWaves : 1) * (kGroup / 32) : 1];
+    const int lane = threadIdx.x % kWaveLanes;
+    const int wave = ONE ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes) : 0;
+    uint32_t* const s_bits = s_all + (PADS ? wave * (kGroup / 32) : 0);
     const int64_t b = a.e_begin + int64_t(blockIdx.y) * a.stride, e = b + a.e_len;
     Acc<KIND> t;
-    for (int64_t g = b / kGroup + blockIdx.x; g * kGroup < e; g += gridDim.x) {
+    for (int64_t g = b / kGroup + (ONE ? wave : int(blockIdx.x)); g * kGroup < e;
+         g += ONE ? kOneWaves : int(gridDim.x)) {
         const int64_t G0 = g * kGroup;
         const bool inside = G0 >= b && G0 + kGroup <= e;
         u32x4 v[kBatch];
@@ -191,8 +216,13 @@ __global__ __launch_bounds__(kWaveLanes) void acc_norm_kernel(const AccNormArgs 
 #pragma unroll
         for (int r = 0; r < kBatch; ++r) t.add4(v[r]);
     }
-    const double v = wave_join<KIND>(t.value());
-    if (lane == 0) a.part[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] = v;
+    if constexpr (ONE) {
+        const double v = block_join<KIND, kOneThreads>(t.value());
+        if (threadIdx.x == 0) write_record(v, KIND, a.max_norm, a.out);
+    } else {
+        const double v = wave_value<KIND>(t.value());
+        if (lane == 0) a.part[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] = v;
+    }
 }
 
 // ---- Lists of tensors -------------------------------------------------------------
@@ -207,13 +237,18 @@ struct TableArgs {
     int64_t nchunk;
     double* part;
     const zsp_clip* clip;
+    zsp_clip* out;   // of the one-workgroup form
+    float max_norm;  // likewise
     int32_t add_to;  // partials already there that a list norm joins
 };
 
 struct TensorArgs {
     int64_t nchunk;
+    int64_t chunk_first;  // of the launch
     double* part;
     const zsp_clip* clip;
+    zsp_clip* out;
+    float max_norm;
     int32_t n;
     int32_t add_to;
     ArgTensor t[kTensorArgMax];
@@ -228,6 +263,7 @@ __device__ __forceinline__ ListChunk get_chunk(const TableArgs& a, int64_t c) {
 }
 
 __device__ __forceinline__ ListChunk get_chunk(const TensorArgs& a, int64_t c) {
+    c += a.chunk_first;
     const char* seg = (const char*)__builtin_amdgcn_kernarg_segment_ptr();
     const int32_t* c0 = reinterpret_cast<const int32_t*>(seg + offsetof(TensorArgs, chunk0));
     const ArgTensor* ts = reinterpret_cast<const ArgTensor*>(seg + offsetof(TensorArgs, t));
@@ -279,15 +315,23 @@ __device__ __forceinline__ void chunk_norm(const ListChunk& c, int lane, Acc<KIN
                  : reinterpret_cast<const float*>(p)[i]);
 }
 
-template <int KIND, typename Args>
-__global__ __launch_bounds__(kWaveLanes) void list_norm_kernel(const Args a) {
-    const int lane = threadIdx.x;
+template <int KIND, bool ONE, typename Args>
+__global__ __launch_bounds__(ONE ? kOneThreads : kWaveLanes) void list_norm_kernel(const Args a) {
+    const int lane = threadIdx.x % kWaveLanes;
+    const int first =
+        ONE ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes) : int(blockIdx.x);
     Acc<KIND> t;
-    for (int64_t c = blockIdx.x; c < a.nchunk; c += gridDim.x) chunk_norm(get_chunk(a, c), lane, t);
-    double v = wave_join<KIND>(t.value());
-    if (lane == 0) {
-        if (int(blockIdx.x) < a.add_to) v = join<KIND>(a.part[blockIdx.x], v);
-        a.part[blockIdx.x] = v;
+    for (int64_t c = first; c < a.nchunk; c += ONE ? kOneWaves : int(gridDim.x))
+        chunk_norm(get_chunk(a, c), lane, t);
+    if constexpr (ONE) {
+        const double v = block_join<KIND, kOneThreads>(t.value());
+        if (threadIdx.x == 0) write_record(v, KIND, a.max_norm, a.out);
+    } else {
+        double v = wave_value<KIND>(t.value());
+        if (lane == 0) {
+            if (int(blockIdx.x) < a.add_to) v = join<KIND>(a.part[blockIdx.x], v);
+            a.part[blockIdx.x] = v;
+        }
     }
 }
 
@@ -329,51 +373,82 @@ __device__ __forceinline__ void chunk_scale(const ListChunk& c, int part, int la
     }
 }
 
+// Workgroups go to the 8 XCDs in turn; each XCD takes runs of kClipRun
+// consecutive waves (64 KiB of a tensor), so that a cache line which two
+// waves share -- a tensor starts at any element -- is written in one L2.
+// 10,000 tensors, every seventh off alignment: 78 us, and 103 with the waves
+// in plain order; 0.8 GB in nine aligned tensors: 242 and 258.
+constexpr int kClipRun = 64;
+
 template <typename Args>
 __global__ __launch_bounds__(kWaveLanes) void list_clip_kernel(const Args a) {
+    const int64_t x = blockIdx.x % 8, i = blockIdx.x / 8;
+    const int64_t w = (i / kClipRun * 8 + x) * kClipRun + i % kClipRun;
+    if (w >= a.nchunk * kBatch) return;  // the grid is rounded up to 8 runs
+    const ListChunk c = get_chunk(a, w / kBatch);
     const float s = a.clip->coef;
     // 1: nothing to change. NaN: the norm was not finite, nothing is changed.
     if (s == 1.0f || s != s) return;
-    for (int64_t w = blockIdx.x; w < a.nchunk * kBatch; w += gridDim.x)
-        chunk_scale(get_chunk(a, w / kBatch), int(w % kBatch), threadIdx.x, s);
+    chunk_scale(c, int(w % kBatch), threadIdx.x, s);
 }
 
 // ---- Joining partials -------------------------------------------------------------
 
 constexpr int kFinishThreads = 1024;
 constexpr int kThreads = 256;
-// Partials that one workgroup joins by itself; more are folded to
-// kFoldBlocks values first.
-constexpr int64_t kFinishMax = 8192;
 
-__device__ __forceinline__ void write_record(double total, int kind, float max_norm,
-                                             zsp_clip* out) {
-    const double norm = kind == ZSP_NORM_MAX ? total : __builtin_sqrt(total);
-    float coef = 1.0f;
-    if (!(norm <= 1.7976931348623157e308)) coef = __builtin_nanf("");
-    else if (norm > double(max_norm)) coef = float(double(max_norm) / norm);
-    out->total = total;
-    out->norm = float(norm);
-    out->coef = coef;
+// Joins part[first], part[first + step], ... below n, eight loads in flight
+// (past the end the last again, unused).
+template <int KIND>
+__device__ __forceinline__ double join_strided(const double* part, int64_t first, int64_t step,
+                                               int64_t n) {
+    double v = 0.0;
+    for (int64_t i = first; i < n; i += step * 8) {
+        double x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t j = i + k * step;
+            x[k] = part[j < n ? j : n - 1];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i + k * step < n) v = join<KIND>(v, x[k]);
+    }
+    return v;
 }
 
-// Workgroup b joins the b-th run of ceil(n / gridDim.x) partials.
+// A long list of partials in one launch: workgroup b joins the b-th run of
+// ceil(n / gridDim.x), and the workgroup that takes the last ticket (0 when
+// the launch begins) joins the runs, in their order whichever it is. No
+// workgroup waits for another.
 template <int KIND>
-__global__ __launch_bounds__(kThreads) void fold_kernel(const double* part, int64_t n,
-                                                        double* out) {
+__global__ __launch_bounds__(kThreads) void fold_kernel(const double* part, int64_t n, double* runs,
+                                                        uint32_t* ticket, float max_norm,
+                                                        zsp_clip* out) {
+    __shared__ uint32_t s_last;
     const int64_t per = (n + gridDim.x - 1) / gridDim.x;
     const int64_t b = per * blockIdx.x, e = b + per < n ? b + per : n;
-    double v = 0.0;
-    for (int64_t i = b + threadIdx.x; i < e; i += kThreads) v = join<KIND>(v, part[i]);
+    double v = block_join<KIND, kThreads>(join_strided<KIND>(part, b + threadIdx.x, kThreads, e));
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(runs + blockIdx.x, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+                 gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    static_assert(kFoldBlocks <= kThreads, "a run per thread");
+    v = threadIdx.x < gridDim.x ? __hip_atomic_load(runs + threadIdx.x, __ATOMIC_RELAXED,
+                                                    __HIP_MEMORY_SCOPE_AGENT)
+                                : 0.0;
     v = block_join<KIND, kThreads>(v);
-    if (threadIdx.x == 0) out[blockIdx.x] = v;
+    if (threadIdx.x == 0) write_record(v, KIND, max_norm, out);
 }
 
 template <int KIND>
 __global__ __launch_bounds__(kFinishThreads) void finish_kernel(const double* part, int64_t n,
                                                                 float max_norm, zsp_clip* out) {
-    double v = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kFinishThreads) v = join<KIND>(v, part[i]);
+    double v = join_strided<KIND>(part, threadIdx.x, kFinishThreads, n);
     v = block_join<KIND, kFinishThreads>(v);
     if (threadIdx.x == 0) write_record(v, KIND, max_norm, out);
 }
@@ -400,23 +475,27 @@ void tensor_args(const TensorsLaunch& L, TensorArgs& a) {
     for (int i = 0; i <= L.n_args; ++i) a.chunk0[i] = L.chunk0[i];
 }
 
-template <int KIND>
+template <int KIND, bool ONE>
 hipError_t list_norm_t(const TensorsLaunch& L, double* part, int64_t blocks, int32_t add_to,
-                       hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(kWaveLanes);
+                       float max_norm, zsp_clip* out, hipStream_t stream) {
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(ONE ? kOneThreads : kWaveLanes);
     if (L.n_args > 0) {
         TensorArgs a{};
         tensor_args(L, a);
         a.part = part;
         a.add_to = add_to;
-        hipLaunchKernelGGL((list_norm_kernel<KIND, TensorArgs>), grid, block, 0, stream, a);
+        a.max_norm = max_norm;
+        a.out = out;
+        hipLaunchKernelGGL((list_norm_kernel<KIND, ONE, TensorArgs>), grid, block, 0, stream, a);
     } else {
         TableArgs a{};
         a.chunks = L.chunks;
         a.nchunk = L.nchunk;
         a.part = part;
         a.add_to = add_to;
-        hipLaunchKernelGGL((list_norm_kernel<KIND, TableArgs>), grid, block, 0, stream, a);
+        a.max_norm = max_norm;
+        a.out = out;
+        hipLaunchKernelGGL((list_norm_kernel<KIND, ONE, TableArgs>), grid, block, 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -425,13 +504,10 @@ template <int KIND>
 hipError_t finish_t(double* part, int64_t n, int64_t parts_cap, float max_norm, zsp_clip* out,
                     hipStream_t stream) {
     if (n > kFinishMax) {
-        double* fold = part + parts_cap;
-        hipLaunchKernelGGL(fold_kernel<KIND>, dim3(kFoldBlocks), dim3(kThreads), 0, stream, part,
-                           n, fold);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        part = fold;
-        n = kFoldBlocks;
+        const int64_t runs = std::min<int64_t>(kFoldBlocks, (n + kThreads * 8 - 1) / (kThreads * 8));
+        hipLaunchKernelGGL(fold_kernel<KIND>, dim3(static_cast<uint32_t>(runs)), dim3(kThreads), 0,
+                           stream, part, n, part + parts_cap, norm_ticket(part, parts_cap), max_norm, out);
+        return hipGetLastError();
     }
     hipLaunchKernelGGL(finish_kernel<KIND>, dim3(1), dim3(kFinishThreads), 0, stream, part, n,
                        max_norm, out);
@@ -439,37 +515,47 @@ hipError_t finish_t(double* part, int64_t n, int64_t parts_cap, float max_norm, 
 }
 
 template <int KIND>
-hipError_t acc_norm_t(const AccNormArgs& a, bool pads, dim3 grid, hipStream_t stream) {
-    if (pads)
-        hipLaunchKernelGGL((acc_norm_kernel<KIND, true>), grid, dim3(kWaveLanes), 0, stream, a);
+hipError_t acc_norm_t(const AccNormArgs& a, bool pads, bool one, dim3 grid, hipStream_t stream) {
+    const dim3 block(one ? kOneThreads : kWaveLanes);
+    if (pads && one)
+        hipLaunchKernelGGL((acc_norm_kernel<KIND, true, true>), grid, block, 0, stream, a);
+    else if (pads)
+        hipLaunchKernelGGL((acc_norm_kernel<KIND, true, false>), grid, block, 0, stream, a);
+    else if (one)
+        hipLaunchKernelGGL((acc_norm_kernel<KIND, false, true>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((acc_norm_kernel<KIND, false>), grid, dim3(kWaveLanes), 0, stream, a);
+        hipLaunchKernelGGL((acc_norm_kernel<KIND, false, false>), grid, block, 0, stream, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_acc_norm(const AccNormLaunch& L, int64_t* nparts, hipStream_t stream) {
+hipError_t launch_acc_norm(const AccNormLaunch& L, float max_norm, zsp_clip* out,
+                           int64_t* nparts, bool* done, hipStream_t stream) {
     *nparts = 0;
+    *done = false;
     if (L.e_len <= 0 || L.spans <= 0) return hipSuccess;
     if (L.spans > ZSP_MAX_RANKS) return hipErrorInvalidValue;
     AccNormArgs a{};
     a.e0 = L.tab.e0;
     a.info = L.tab.info;
     a.tile = L.tab.tile;
+    a.ntile = L.tab.ntile;
     a.acc = L.acc;
     a.e_begin = L.e_begin;
     a.e_len = L.e_len;
     a.stride = L.stride;
-    a.ntile = L.tab.ntile;
     a.part = L.part;
+    a.max_norm = max_norm;
+    a.out = out;
     // workgroups per span: at most kNormBlocks (+ one per span) in all
     const int64_t groups = L.e_len / kGroup + 2;
     const int64_t x = std::min<int64_t>(groups, kNormBlocks / L.spans + 1);
-    *nparts = x * L.spans;
-    const dim3 grid(static_cast<uint32_t>(x), static_cast<uint32_t>(L.spans));
-    return L.kind == ZSP_NORM_MAX ? acc_norm_t<ZSP_NORM_MAX>(a, L.pads, grid, stream)
-                                  : acc_norm_t<ZSP_NORM_L2>(a, L.pads, grid, stream);
+    *done = L.spans == 1 && groups <= kOneWaves;
+    *nparts = *done ? 0 : x * L.spans;
+    const dim3 grid(*done ? 1u : static_cast<uint32_t>(x), static_cast<uint32_t>(L.spans));
+    return L.kind == ZSP_NORM_MAX ? acc_norm_t<ZSP_NORM_MAX>(a, L.pads, *done, grid, stream)
+                                  : acc_norm_t<ZSP_NORM_L2>(a, L.pads, *done, grid, stream);
 }
 
 hipError_t launch_finish(double* part, int64_t n, int64_t parts_cap, zsp_norm_kind kind,
@@ -490,34 +576,52 @@ hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, 
     return hipGetLastError();
 }
 
+bool list_norm_is_small(int64_t nchunk) { return nchunk <= kOneWaves; }
+
+hipError_t launch_list_norm_one(const TensorsLaunch& L, zsp_norm_kind kind, float max_norm,
+                                zsp_clip* out, hipStream_t stream) {
+    return kind == ZSP_NORM_MAX
+               ? list_norm_t<ZSP_NORM_MAX, true>(L, nullptr, 1, 0, max_norm, out, stream)
+               : list_norm_t<ZSP_NORM_L2, true>(L, nullptr, 1, 0, max_norm, out, stream);
+}
+
 hipError_t launch_list_norm(const TensorsLaunch& L, zsp_norm_kind kind, double* part,
-                            int64_t* nparts, bool add, hipStream_t stream) {
+                            int64_t* nparts, hipStream_t stream) {
     if (L.nchunk <= 0) return hipSuccess;
     const int64_t blocks = std::min<int64_t>(L.nchunk, kNormBlocks);
-    const int32_t add_to = add ? static_cast<int32_t>(*nparts) : 0;
+    const int32_t there = static_cast<int32_t>(*nparts);
     *nparts = std::max(*nparts, blocks);
-    return kind == ZSP_NORM_MAX ? list_norm_t<ZSP_NORM_MAX>(L, part, blocks, add_to, stream)
-                                : list_norm_t<ZSP_NORM_L2>(L, part, blocks, add_to, stream);
+    return kind == ZSP_NORM_MAX
+               ? list_norm_t<ZSP_NORM_MAX, false>(L, part, blocks, there, 0, nullptr, stream)
+               : list_norm_t<ZSP_NORM_L2, false>(L, part, blocks, there, 0, nullptr, stream);
 }
 
 hipError_t launch_list_clip(const TensorsLaunch& L, const zsp_clip* clip, hipStream_t stream) {
-    if (L.nchunk <= 0) return hipSuccess;
-    // a wave per run; its work-items must fit in 32 bits
-    const int64_t waves = std::min<int64_t>(L.nchunk * kBatch, int64_t(1) << 25);
-    const dim3 grid(static_cast<uint32_t>(waves)), block(kWaveLanes);
-    if (L.n_args > 0) {
-        TensorArgs a{};
-        tensor_args(L, a);
-        a.clip = clip;
-        hipLaunchKernelGGL((list_clip_kernel<TensorArgs>), grid, block, 0, stream, a);
-    } else {
-        TableArgs a{};
-        a.chunks = L.chunks;
-        a.nchunk = L.nchunk;
-        a.clip = clip;
-        hipLaunchKernelGGL((list_clip_kernel<TableArgs>), grid, block, 0, stream, a);
+    // work-items of a launch must fit in 32 bits: a long list takes several
+    constexpr int64_t kMost = int64_t(1) << 22;
+    for (int64_t at = 0; at < L.nchunk; at += kMost) {
+        const int64_t n = std::min(L.nchunk - at, kMost);
+        const int64_t round = 8 * kClipRun;
+        const int64_t blocks = (n * kBatch + round - 1) / round * round;
+        const dim3 grid(static_cast<uint32_t>(blocks)), block(kWaveLanes);
+        if (L.n_args > 0) {
+            TensorArgs a{};
+            tensor_args(L, a);
+            a.chunk_first = at;
+            a.nchunk = n;
+            a.clip = clip;
+            hipLaunchKernelGGL((list_clip_kernel<TensorArgs>), grid, block, 0, stream, a);
+        } else {
+            TableArgs a{};
+            a.chunks = L.chunks + at;
+            a.nchunk = n;
+            a.clip = clip;
+            hipLaunchKernelGGL((list_clip_kernel<TableArgs>), grid, block, 0, stream, a);
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 }  // namespace zsp

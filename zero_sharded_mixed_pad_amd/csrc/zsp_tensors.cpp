@@ -144,10 +144,13 @@ zsp_status zsp_norm_many(const void* const* x, const int64_t* numel, const int32
     if (st != ZSP_OK) return st;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     int64_t nparts = 0;
+    bool done = false;
     st = for_each_launch(x, numel, dtype, n, [&](const TensorsLaunch& L) {
-        return launch_list_norm(L, kind, static_cast<double*>(ws), &nparts, nparts > 0, hs);
+        done = L.nchunk == nchunk && list_norm_is_small(nchunk);
+        return done ? launch_list_norm_one(L, kind, max_norm, out, hs)
+                    : launch_list_norm(L, kind, static_cast<double*>(ws), &nparts, hs);
     });
-    return st != ZSP_OK ? st : finish(nc, nparts, hs);
+    return st != ZSP_OK || done ? st : finish(nc, nparts, hs);
 }
 
 zsp_status zsp_clip_many(void* const* x, const int64_t* numel, const int32_t* dtype, int32_t n,
@@ -231,10 +234,12 @@ zsp_status zsp_tensor_list_norm(const zsp_tensor_list* list, zsp_norm_kind kind,
     L.chunks = list->dev;
     L.nchunk = list->nchunk;
     int64_t nparts = 0;
+    const bool one = list_norm_is_small(L.nchunk);
     const hipError_t e =
-        launch_list_norm(L, kind, static_cast<double*>(ws), &nparts, false, hs);
+        one ? launch_list_norm_one(L, kind, max_norm, out, hs)
+            : launch_list_norm(L, kind, static_cast<double*>(ws), &nparts, hs);
     if (e != hipSuccess) return set_hip_error(e, "tensor list launch");
-    return finish(nc, nparts, hs);
+    return one ? ZSP_OK : finish(nc, nparts, hs);
 }
 
 zsp_status zsp_tensor_list_clip(const zsp_tensor_list* list, const zsp_clip* clip, void* stream) {

@@ -378,10 +378,10 @@ zsp_status zsp_norm_workspace(const zsp_plan* plan, int64_t* bytes);
 /* Norm of the bound accumulator's real elements (pad slots are left out,
  * whatever they hold), of one rank or all, whole-model or parameters
  * [first_param, first_param + n_params). Needs an accumulator bound. */
-zsp_status zsp_grad_norm(zsp_plan* plan, int32_t rank_or_all, zsp_norm_kind kind, float max_norm,
+zsp_status zsp_grad_norm(zsp_plan* plan, int32_t rank_or_all, zsp_norm_kind kind, double max_norm,
                          void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
 zsp_status zsp_grad_norm_params(zsp_plan* plan, int32_t rank_or_all, int32_t first_param,
-                                int32_t n_params, zsp_norm_kind kind, float max_norm, void* ws,
+                                int32_t n_params, zsp_norm_kind kind, double max_norm, void* ws,
                                 int64_t ws_bytes, zsp_clip* out, void* stream);
 
 /* zsp_reduce_shard (_params) with the norm of the accumulator elements it
@@ -389,12 +389,12 @@ zsp_status zsp_grad_norm_params(zsp_plan* plan, int32_t rank_or_all, int32_t fir
  * zsp_reduce_shard leaves, bit for bit. */
 zsp_status zsp_reduce_shard_norm(zsp_plan* plan, int32_t rank_or_all, const void* const* grads,
                                  zsp_dtype dtype, zsp_grad_layout layout, int32_t accumulate,
-                                 zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                                 zsp_norm_kind kind, double max_norm, void* ws, int64_t ws_bytes,
                                  zsp_clip* out, void* stream);
 zsp_status zsp_reduce_shard_norm_params(zsp_plan* plan, int32_t rank_or_all, int32_t first_param,
                                         int32_t n_params, const void* const* grads,
                                         zsp_dtype dtype, zsp_grad_layout layout,
-                                        int32_t accumulate, zsp_norm_kind kind, float max_norm,
+                                        int32_t accumulate, zsp_norm_kind kind, double max_norm,
                                         void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
 
 /* The norm of the gradient that zsp_reduce_adam_step (use_acc likewise) would
@@ -403,7 +403,7 @@ zsp_status zsp_reduce_shard_norm_params(zsp_plan* plan, int32_t rank_or_all, int
  * once more than an unclipped step. */
 zsp_status zsp_reduce_norm(zsp_plan* plan, int32_t rank_or_all, const void* const* grads,
                            zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
-                           zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                           zsp_norm_kind kind, double max_norm, void* ws, int64_t ws_bytes,
                            zsp_clip* out, void* stream);
 
 /* Joins the totals of n >= 0 records into one: the layers' records of a
@@ -411,7 +411,7 @@ zsp_status zsp_reduce_norm(zsp_plan* plan, int32_t rank_or_all, const void* cons
  * summed (ZSP_NORM_MAX: maximised) over the processes of a data-parallel
  * group. parts: n records in device memory, 16-byte aligned; only their
  * totals are read. out may be one of them. No records: norm 0. */
-zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, double max_norm,
                             zsp_clip* out, void* stream);
 
 /* zsp_adam_step and zsp_reduce_adam_step (_params) with the gradient g
@@ -452,7 +452,7 @@ zsp_status zsp_reduce_adam_step_clip_params(zsp_plan* plan, int32_t rank_or_all,
  * counted per tensor. No plan is involved: all tensors, ws, out and
  * clip are on the current device. */
 zsp_status zsp_norm_many(const void* const* x, const int64_t* numel, const int32_t* dtype,
-                         int32_t n, zsp_norm_kind kind, float max_norm, void* ws,
+                         int32_t n, zsp_norm_kind kind, double max_norm, void* ws,
                          int64_t ws_bytes, zsp_clip* out, void* stream);
 zsp_status zsp_clip_many(void* const* x, const int64_t* numel, const int32_t* dtype, int32_t n,
                          const zsp_clip* clip, void* stream);
@@ -468,7 +468,7 @@ zsp_status zsp_clip_many(void* const* x, const int64_t* numel, const int32_t* dt
  * calls on it must have finished. */
 zsp_status zsp_tensor_list_create(void* const* x, const int64_t* numel, const int32_t* dtype,
                                   int32_t n, void* stream, zsp_tensor_list** list);
-zsp_status zsp_tensor_list_norm(const zsp_tensor_list* list, zsp_norm_kind kind, float max_norm,
+zsp_status zsp_tensor_list_norm(const zsp_tensor_list* list, zsp_norm_kind kind, double max_norm,
                                 void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
 zsp_status zsp_tensor_list_clip(const zsp_tensor_list* list, const zsp_clip* clip, void* stream);
 void zsp_tensor_list_destroy(zsp_tensor_list* list);

@@ -96,6 +96,7 @@ LAYOUTS = [
     ([70001, 9, 12345], 17),
     ([70001, 9, 12345], 70),
     ([262147, 65536 * 2 + 8], 2),
+    ([5003, 300, 17], 256),
 ]
 
 
@@ -144,11 +145,11 @@ def test_list_norm_and_clip(case, types, kind):
         ws.fill_(0xff)                       # whatever a workspace holds
         one, prep = zsp.clip_record(), zsp.clip_record()
         zsp.norm_many(xs, one, ws, max_norm=max_norm, kind=kind)
-        check_record(one, vals, kind, float(np.float32(max_norm)))
+        check_record(one, vals, kind, max_norm)
         tl = zsp.TensorList(xs)
         ws.fill_(0xff)
         tl.norm(prep, ws, max_norm=max_norm, kind=kind)
-        check_record(prep, vals, kind, float(np.float32(max_norm)))
+        check_record(prep, vals, kind, max_norm)
         for b, w in zip((b for b, _, _ in bufs), before):
             assert torch.equal(b, w)         # a norm writes nothing
         coef = zsp.clip_values(prep)[2]
@@ -217,7 +218,7 @@ def test_coefficient_rules():
         if want is not None:
             assert coef == want
         else:
-            assert coef == np.float32(float(np.float32(max_norm)) / 4.0)
+            assert coef == np.float32(max_norm / 4.0)
     zsp.norm_many([torch.zeros(5, device=dev())], rec, ws, max_norm=0.0)
     assert rec_of(rec) == (0.0, 0.0, 1.0)              # nothing to clip
 
@@ -259,6 +260,26 @@ def test_list_past_2_32_elements():
     assert rec_of(rec)[0] == 3.0
 
 
+def test_list_past_one_launch():
+    """More 8 KiB chunks than one clip launch takes (2^22): the chunks behind
+    it are clipped too, from a prepared list and from the arguments."""
+    n = ((1 << 22) + 1) * 4096 + 5
+    x = torch.zeros(n, dtype=BF, device=dev())
+    marks = [0, (1 << 22) * 4096 - 1, (1 << 22) * 4096, n - 6, n - 1]
+    for i in marks:
+        x[i] = 4.0
+    ws, rec = zsp.norm_workspace(), zsp.clip_record()
+    tl = zsp.TensorList([x])
+    for run, left in ((lambda: tl.clip(rec), 2.0), (lambda: zsp.clip_many([x], rec), 1.0)):
+        rec.view(torch.float32)[0, 3] = 0.5
+        run()
+        assert [x[i].item() for i in marks] == [left] * len(marks)
+        zsp.norm_many([x], rec, ws)
+        assert rec_of(rec)[0] == len(marks) * left * left
+        tl.norm(rec, ws, kind="max")
+        assert rec_of(rec)[0] == left
+
+
 # ---- the accumulator's norm ---------------------------------------------------------
 
 @pytest.mark.parametrize("kind", ["l2", "max"])
@@ -276,7 +297,7 @@ def test_grad_norm(case, kind):
         ws.fill_(0xff)
         rank = zsp.ALL_RANKS if rank_local is None else rank_local
         M.plan.grad_norm(rank, rec, ws, max_norm=0.01, kind=kind)
-        check_record(rec, acc[at], kind, float(np.float32(0.01)))
+        check_record(rec, acc[at], kind, 0.01)
         T = len(numels)
         subs = {(0, 1), (T - 1, 1), (0, T), (T // 2, max(1, T // 3)), (min(1, T - 1), T - min(1, T - 1))}
         for first, n in subs:
@@ -284,7 +305,7 @@ def test_grad_norm(case, kind):
                 continue
             M.plan.grad_norm_params(rank, first, n, rec, ws, max_norm=0.01, kind=kind)
             check_record(rec, acc[real_mask(M.L, M.ranks, first, n)], kind,
-                         float(np.float32(0.01)))
+                         0.01)
         if rank_local is None:
             j = nd // 2
             M.plan.grad_norm(j, rec, ws, kind=kind)
@@ -324,8 +345,8 @@ def test_reduce_norms(case, layout, dt, kind):
             B.plan.reduce_shard(rank, grads, layout=layout, accumulate=accumulate)
             assert_bits(np_of(A.g_acc), np_of(B.g_acc), "accumulator")
             vals = np_of(B.g_acc)[at]
-            check_record(rec, vals, kind, float(np.float32(0.02)))
-            check_record(rec2, vals, kind, float(np.float32(0.02)))
+            check_record(rec, vals, kind, 0.02)
+            check_record(rec2, vals, kind, 0.02)
 
 
 @pytest.mark.parametrize("case", [0, 6, 7, 8])
@@ -350,14 +371,55 @@ def test_reduce_norm_by_layers_and_ranks(case):
         out = zsp.clip_record()
         zsp.clip_combine(parts, out, max_norm=0.03, kind=kind)
         assert_bits(np_of(A.g_acc[:A.n]), np_of(B.g_acc[:B.n]), "accumulator")
-        check_record(out, np_of(B.g_acc)[real_mask(A.L, A.ranks)], kind, float(np.float32(0.03)))
+        check_record(out, np_of(B.g_acc)[real_mask(A.L, A.ranks)], kind, 0.03)
         parts2 = zsp.clip_record(len(groups))
         for i, (first, n) in enumerate(groups):      # all ranks of a group in one call
             A.plan.reduce_shard_norm_params(zsp.ALL_RANKS, first, n, grads, parts2[i:i + 1], ws,
                                             kind=kind)
         zsp.clip_combine(parts2, parts2[:1], max_norm=0.03, kind=kind)     # in place
         check_record(parts2[:1], np_of(B.g_acc)[real_mask(A.L, A.ranks)], kind,
-                     float(np.float32(0.03)))
+                     0.03)
+
+
+@pytest.mark.parametrize("numels,nd", [([3_000_017, 70_001], 2),
+                                       # short pieces: whole-tile waves, 4700 and more tiles
+                                       (synth.small_tensor_sizes(count=1200, lo=900, hi=9000,
+                                                                 seed=9), 8)])
+def test_many_partials(numels, nd):
+    """Reduces whose partials are too many for one workgroup to join, eager
+    and replayed from a graph with eager work between: the same bits."""
+    M = Mirror(numels, nd)
+    grads = grads_of(M, BF, "many", poison=False)
+    ws, wsg = M.plan.norm_workspace(), M.plan.norm_workspace()
+    ws.fill_(0xff)
+    wsg.fill_(0xff)
+    rec, recg = zsp.clip_record(4), zsp.clip_record(4)
+    at = real_mask(M.L, M.ranks)
+
+    def calls(rec, ws, stream=None):
+        for i, kind in enumerate(("l2", "max")):
+            M.plan.reduce_shard_norm(zsp.ALL_RANKS, grads, rec[i:i + 1], ws, max_norm=0.5,
+                                     kind=kind, stream=stream)
+            M.plan.reduce_norm(zsp.ALL_RANKS, grads, rec[2 + i:3 + i], ws, max_norm=0.5,
+                               kind=kind, stream=stream)
+
+    calls(rec, ws)
+    vals = np_of(M.g_acc)[at]
+    for i, kind in enumerate(("l2", "max", "l2", "max")):
+        check_record(rec[i:i + 1], vals, kind, 0.5)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(g, stream=s):
+            calls(recg, wsg, s)
+    for rep in range(3):
+        grads[0].mul_(1.5)
+        g.replay()
+        calls(rec, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(rec.view(torch.int64), recg.view(torch.int64)), rep
+    del g
 
 
 def test_combine():
@@ -610,6 +672,45 @@ def test_two_streams_and_the_caller_s_stream():
             tl.norm(got[0:1], ws[0], stream=s2)
     torch.cuda.synchronize()
     assert torch.equal(got.view(torch.int64), want.view(torch.int64))
+
+
+def test_threads_on_one_plan_and_one_list():
+    """One thread per rank, each on its own stream with its own workspace and
+    record, norms of one plan and of one list at once."""
+    import threading
+    numels, nd = [50021, 511, 1025], 4
+    M = Mirror(numels, nd)
+    grads = grads_of(M, BF, "threads")
+    _, xs = make_list([70000, 5, 4097], [FP, BF, FP], "threads")
+    tl = zsp.TensorList(xs)
+    ws = [M.plan.norm_workspace() for _ in range(nd)]
+    rec = [zsp.clip_record(2) for _ in range(nd)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(r):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(10):
+                M.plan.reduce_shard_norm(r, grads, rec[r][0:1], ws[r], stream=s)
+                tl.norm(rec[r][1:2], ws[r], stream=s)
+            s.synchronize()
+        except Exception as e:           # reported by the test, not lost with the thread
+            errors.append(e)
+
+    ts = [threading.Thread(target=work, args=(r,)) for r in range(nd)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not errors
+    for r in range(nd):
+        check_record(rec[r][0:1], np_of(M.g_acc)[real_mask(M.L, [r]) + r * M.L.S], "l2", INF)
+        check_record(rec[r][1:2], values(xs), "l2", INF)
+    all_ranks = torch.cat([rec[r][0:1] for r in range(nd)])
+    out = zsp.clip_record()
+    zsp.clip_combine(all_ranks, out)
+    check_record(out, np_of(M.g_acc)[real_mask(M.L, M.ranks)], "l2", INF)
 
 
 def test_equal_inputs_give_equal_bits():

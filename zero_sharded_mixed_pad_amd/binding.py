@@ -38,6 +38,7 @@ def _load():
             f"{LIB_PATH} is not built; run __graft_entry__.build() (hipcc, gfx950) first")
     L = ctypes.CDLL(LIB_PATH)
     i32, i64, vp, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+    f64 = ctypes.c_double
     i64p = ctypes.POINTER(ctypes.c_int64)
     i32p = ctypes.POINTER(ctypes.c_int32)
     vpp = ctypes.POINTER(ctypes.c_void_p)
@@ -64,23 +65,23 @@ def _load():
         "zsp_gather_list_run": (i32, [vp, vp]),
         "zsp_gather_list_destroy": (None, [vp]),
         "zsp_norm_workspace": (i32, [vp, i64p]),
-        "zsp_grad_norm": (i32, [vp, i32, i32, f32, vp, i64, vp, vp]),
-        "zsp_grad_norm_params": (i32, [vp, i32, i32, i32, i32, f32, vp, i64, vp, vp]),
-        "zsp_reduce_shard_norm": (i32, [vp, i32, vpp, i32, i32, i32, i32, f32, vp, i64, vp, vp]),
-        "zsp_reduce_shard_norm_params": (i32, [vp, i32, i32, i32, vpp, i32, i32, i32, i32, f32,
+        "zsp_grad_norm": (i32, [vp, i32, i32, f64, vp, i64, vp, vp]),
+        "zsp_grad_norm_params": (i32, [vp, i32, i32, i32, i32, f64, vp, i64, vp, vp]),
+        "zsp_reduce_shard_norm": (i32, [vp, i32, vpp, i32, i32, i32, i32, f64, vp, i64, vp, vp]),
+        "zsp_reduce_shard_norm_params": (i32, [vp, i32, i32, i32, vpp, i32, i32, i32, i32, f64,
                                                vp, i64, vp, vp]),
-        "zsp_reduce_norm": (i32, [vp, i32, vpp, i32, i32, i32, i32, f32, vp, i64, vp, vp]),
-        "zsp_clip_combine": (i32, [vp, i32, i32, f32, vp, vp]),
+        "zsp_reduce_norm": (i32, [vp, i32, vpp, i32, i32, i32, i32, f64, vp, i64, vp, vp]),
+        "zsp_clip_combine": (i32, [vp, i32, i32, f64, vp, vp]),
         "zsp_adam_step_clip": (i32, [vp, i32, vp, f32, f32, f32, f32, i64, vp]),
         "zsp_adam_step_clip_params": (i32, [vp, i32, i32, i32, vp, f32, f32, f32, f32, i64, vp]),
         "zsp_reduce_adam_step_clip": (i32, [vp, i32, vpp, i32, i32, i32, vp, f32, f32, f32, f32,
                                             i64, vp]),
         "zsp_reduce_adam_step_clip_params": (i32, [vp, i32, i32, i32, vpp, i32, i32, i32, vp, f32,
                                                    f32, f32, f32, i64, vp]),
-        "zsp_norm_many": (i32, [vpp, i64p, i32p, i32, i32, f32, vp, i64, vp, vp]),
+        "zsp_norm_many": (i32, [vpp, i64p, i32p, i32, i32, f64, vp, i64, vp, vp]),
         "zsp_clip_many": (i32, [vpp, i64p, i32p, i32, vp, vp]),
         "zsp_tensor_list_create": (i32, [vpp, i64p, i32p, i32, vp, ctypes.POINTER(vp)]),
-        "zsp_tensor_list_norm": (i32, [vp, i32, f32, vp, i64, vp, vp]),
+        "zsp_tensor_list_norm": (i32, [vp, i32, f64, vp, i64, vp, vp]),
         "zsp_tensor_list_clip": (i32, [vp, vp, vp]),
         "zsp_tensor_list_destroy": (None, [vp]),
         "zsp_checkpoint_write_host": (i32, [vp, i32, ctypes.c_char_p, i64, vp, vp, vp, vp]),
@@ -153,12 +154,15 @@ def _grad_array(grads, n_d, min_elems=0):
     if len(grads) != n_d:
         raise ValueError(f"need {n_d} gradient buffers, got {len(grads)}")
     dt = grads[0].dtype
-    for i, g in enumerate(grads):
-        if isinstance(g, torch.Tensor) and g.numel() < min_elems:
-            raise ValueError(f"grads[{i}] holds {g.numel()} elements; this layout reads "
-                             f"{min_elems}")
-    ptrs = [_ptr(g, dt, f"grads[{i}]").value for i, g in enumerate(grads)]
-    return (ctypes.c_void_p * n_d)(*ptrs), _dtype_code(grads[0])
+    if not all([isinstance(g, torch.Tensor) and g.dtype is dt and g.is_cuda and
+                g.is_contiguous() and g.numel() >= min_elems for g in grads]):
+        for i, g in enumerate(grads):     # say which, and why
+            if isinstance(g, torch.Tensor) and g.numel() < min_elems:
+                raise ValueError(f"grads[{i}] holds {g.numel()} elements; this layout reads "
+                                 f"{min_elems}")
+        for i, g in enumerate(grads):
+            _ptr(g, dt, f"grads[{i}]")
+    return (ctypes.c_void_p * n_d)(*[g.data_ptr() for g in grads]), _dtype_code(grads[0])
 
 
 def _need(t, n, what):
@@ -400,6 +404,7 @@ def _here(t, what):
 
 
 def _rec(rec, what, n=1):
+    """The address of n records."""
     p = _ptr(rec, torch.float64, what)
     if rec.numel() != 2 * n:
         raise ValueError(f"{what} must be {'one clip record' if n == 1 else f'{n} clip records'}")
@@ -504,23 +509,25 @@ def zsp_reduce_adam_step_clip_params(h, n_d, rank, first, n, grads, clip, lr, be
                                                 _stream(stream)))
 
 
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 def _tensor_arrays(tensors):
-    n = len(tensors)
-    dev = torch.cuda.current_device()
-    ptrs, sizes, codes = [], [], []
-    for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"tensors[{i}] must be a torch tensor")
-        codes.append(_dtype_code(t))
-        if not t.is_contiguous():
-            raise ValueError(f"tensors[{i}] must be contiguous")
-        if t.get_device() != dev:
-            raise ValueError(f"tensors[{i}] is on {t.device}; the current device is {dev}")
-        ptrs.append(t.data_ptr())
-        sizes.append(t.numel())
+    n, dev = len(tensors), torch.cuda.current_device()
+    if not all([isinstance(t, torch.Tensor) and t.is_contiguous() and t.get_device() == dev and
+                t.dtype in _CODES for t in tensors]):
+        for i, t in enumerate(tensors):   # say which, and why
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"tensors[{i}] must be a torch tensor")
+            _dtype_code(t)
+            if not t.is_contiguous():
+                raise ValueError(f"tensors[{i}] must be contiguous")
+            if t.get_device() != dev:
+                raise ValueError(f"tensors[{i}] is on {t.device}; the current device is {dev}")
     m = max(n, 1)
-    return ((ctypes.c_void_p * m)(*ptrs), (ctypes.c_int64 * m)(*sizes),
-            (ctypes.c_int32 * m)(*codes), n)
+    return ((ctypes.c_void_p * m)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int64 * m)(*[t.numel() for t in tensors]),
+            (ctypes.c_int32 * m)(*[_CODES[t.dtype] for t in tensors]), n)
 
 
 def zsp_norm_many(tensors, out, ws, max_norm=float("inf"), kind="l2", stream=None):

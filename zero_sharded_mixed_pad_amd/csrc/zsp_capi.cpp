@@ -173,8 +173,8 @@ zsp_status check_clip(const zsp_clip* clip, const char* what) {
 zsp_status check_norm(const NormCall& c, int64_t parts) {
     if (c.kind != ZSP_NORM_L2 && c.kind != ZSP_NORM_MAX)
         return fail(ZSP_EINVAL, "bad norm kind %d", c.kind);
-    if (!(c.max_norm >= 0.0f))
-        return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", double(c.max_norm));
+    if (!(c.max_norm >= 0.0))
+        return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", c.max_norm);
     if (!c.ws) return fail(ZSP_EINVAL, "ws is NULL");
     if (!aligned16(c.ws)) return fail(ZSP_EINVAL, "ws is not 16-byte aligned");
     if (c.ws_bytes < norm_ws_bytes(parts))
@@ -666,14 +666,14 @@ zsp_status zsp_norm_workspace(const zsp_plan* P, int64_t* bytes) {
     return ZSP_OK;
 }
 
-zsp_status zsp_grad_norm(zsp_plan* P, int32_t rank_or_all, zsp_norm_kind kind, float max_norm,
+zsp_status zsp_grad_norm(zsp_plan* P, int32_t rank_or_all, zsp_norm_kind kind, double max_norm,
                          void* ws, int64_t ws_bytes, zsp_clip* out, void* stream) {
     return acc_norm(P, rank_or_all, 0, P ? P->T : 0,
                     zsp::NormCall{kind, max_norm, ws, ws_bytes, out}, stream);
 }
 
 zsp_status zsp_grad_norm_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
-                                int32_t n_params, zsp_norm_kind kind, float max_norm, void* ws,
+                                int32_t n_params, zsp_norm_kind kind, double max_norm, void* ws,
                                 int64_t ws_bytes, zsp_clip* out, void* stream) {
     return acc_norm(P, rank_or_all, first_param, n_params,
                     zsp::NormCall{kind, max_norm, ws, ws_bytes, out}, stream);
@@ -681,7 +681,7 @@ zsp_status zsp_grad_norm_params(zsp_plan* P, int32_t rank_or_all, int32_t first_
 
 zsp_status zsp_reduce_shard_norm(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
                                  zsp_dtype dtype, zsp_grad_layout layout, int32_t accumulate,
-                                 zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                                 zsp_norm_kind kind, double max_norm, void* ws, int64_t ws_bytes,
                                  zsp_clip* out, void* stream) {
     const zsp::NormCall nc{kind, max_norm, ws, ws_bytes, out};
     return reduce_params(P, rank_or_all, 0, P ? P->T : 0, grads, dtype, layout, accumulate, &nc,
@@ -691,7 +691,7 @@ zsp_status zsp_reduce_shard_norm(zsp_plan* P, int32_t rank_or_all, const void* c
 zsp_status zsp_reduce_shard_norm_params(zsp_plan* P, int32_t rank_or_all, int32_t first_param,
                                         int32_t n_params, const void* const* grads,
                                         zsp_dtype dtype, zsp_grad_layout layout,
-                                        int32_t accumulate, zsp_norm_kind kind, float max_norm,
+                                        int32_t accumulate, zsp_norm_kind kind, double max_norm,
                                         void* ws, int64_t ws_bytes, zsp_clip* out, void* stream) {
     const zsp::NormCall nc{kind, max_norm, ws, ws_bytes, out};
     return reduce_params(P, rank_or_all, first_param, n_params, grads, dtype, layout, accumulate,
@@ -700,18 +700,18 @@ zsp_status zsp_reduce_shard_norm_params(zsp_plan* P, int32_t rank_or_all, int32_
 
 zsp_status zsp_reduce_norm(zsp_plan* P, int32_t rank_or_all, const void* const* grads,
                            zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
-                           zsp_norm_kind kind, float max_norm, void* ws, int64_t ws_bytes,
+                           zsp_norm_kind kind, double max_norm, void* ws, int64_t ws_bytes,
                            zsp_clip* out, void* stream) {
     return reduce_norm(P, rank_or_all, grads, dtype, layout, use_acc,
                        zsp::NormCall{kind, max_norm, ws, ws_bytes, out}, stream);
 }
 
-zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, double max_norm,
                             zsp_clip* out, void* stream) {
     if (n < 0) return fail(ZSP_EINVAL, "n = %d is negative", n);
     if (kind != ZSP_NORM_L2 && kind != ZSP_NORM_MAX) return fail(ZSP_EINVAL, "bad norm kind %d", kind);
-    if (!(max_norm >= 0.0f))
-        return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", double(max_norm));
+    if (!(max_norm >= 0.0))
+        return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", max_norm);
     zsp_status st = n > 0 ? zsp::check_clip(parts, "parts") : ZSP_OK;
     if (st == ZSP_OK) st = zsp::check_clip(out, "out");
     if (st != ZSP_OK) return st;

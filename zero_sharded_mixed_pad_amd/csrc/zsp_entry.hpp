@@ -20,7 +20,7 @@ zsp_status check_bound(const zsp_plan* P);
 // What every norm call takes besides its data.
 struct NormCall {
     zsp_norm_kind kind;
-    float max_norm;
+    double max_norm;
     void* ws;
     int64_t ws_bytes;
     zsp_clip* out;

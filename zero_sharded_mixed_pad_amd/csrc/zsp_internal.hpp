@@ -362,16 +362,16 @@ struct AccNormLaunch {
     double* part = nullptr;
 };
 // A norm small enough for one workgroup writes *out itself: *done.
-hipError_t launch_acc_norm(const AccNormLaunch& L, float max_norm, zsp_clip* out,
+hipError_t launch_acc_norm(const AccNormLaunch& L, double max_norm, zsp_clip* out,
                            int64_t* nparts, bool* done, hipStream_t stream);
 
 // Partials that launch_finish takes without a ticket.
 constexpr int64_t kFinishMax = 8192;
 // Joins part[0 .. n) into *out; the workspace has room for parts_cap.
 hipError_t launch_finish(double* part, int64_t n, int64_t parts_cap, zsp_norm_kind kind,
-                         float max_norm, zsp_clip* out, hipStream_t stream);
+                         double max_norm, zsp_clip* out, hipStream_t stream);
 // Joins the totals of n records into *out.
-hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, double max_norm,
                           zsp_clip* out, hipStream_t stream);
 
 // One chunk of a tensor of a list: n elements from p on, at most
@@ -402,7 +402,7 @@ struct TensorsLaunch {
 // Whether launch_list_norm_one takes a list of this many chunks.
 bool list_norm_is_small(int64_t nchunk);
 // The whole norm of a small list in one launch.
-hipError_t launch_list_norm_one(const TensorsLaunch& L, zsp_norm_kind kind, float max_norm,
+hipError_t launch_list_norm_one(const TensorsLaunch& L, zsp_norm_kind kind, double max_norm,
                                 zsp_clip* out, hipStream_t stream);
 // Partials of the list from part[0] on, joined to the *nparts that are there
 // already; *nparts is never lowered.

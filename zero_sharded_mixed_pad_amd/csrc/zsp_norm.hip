@@ -87,12 +87,12 @@ __device__ __forceinline__ double block_join(double v) {
     return v;
 }
 
-__device__ __forceinline__ void write_record(double total, int kind, float max_norm,
+__device__ __forceinline__ void write_record(double total, int kind, double max_norm,
                                              zsp_clip* out) {
     const double norm = kind == ZSP_NORM_MAX ? total : __builtin_sqrt(total);
     float coef = 1.0f;
     if (!(norm <= 1.7976931348623157e308)) coef = __builtin_nanf("");
-    else if (norm > double(max_norm)) coef = float(double(max_norm) / norm);
+    else if (norm > max_norm) coef = float(max_norm / norm);
     out->total = total;
     out->norm = float(norm);
     out->coef = coef;
@@ -129,7 +129,7 @@ struct AccNormArgs {
     int64_t ntile;
     int64_t e_begin, e_len, stride;
     double* part;
-    float max_norm;  // of the form that writes the record
+    double max_norm;  // of the form that writes the record
     zsp_clip* out;
 };
 
@@ -238,7 +238,7 @@ struct TableArgs {
     double* part;
     const zsp_clip* clip;
     zsp_clip* out;   // of the one-workgroup form
-    float max_norm;  // likewise
+    double max_norm;  // likewise
     int32_t add_to;  // partials already there that a list norm joins
 };
 
@@ -248,7 +248,7 @@ struct TensorArgs {
     double* part;
     const zsp_clip* clip;
     zsp_clip* out;
-    float max_norm;
+    double max_norm;
     int32_t n;
     int32_t add_to;
     ArgTensor t[kTensorArgMax];
@@ -423,7 +423,7 @@ __device__ __forceinline__ double join_strided(const double* part, int64_t first
 // workgroup waits for another.
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void fold_kernel(const double* part, int64_t n, double* runs,
-                                                        uint32_t* ticket, float max_norm,
+                                                        uint32_t* ticket, double max_norm,
                                                         zsp_clip* out) {
     __shared__ uint32_t s_last;
     const int64_t per = (n + gridDim.x - 1) / gridDim.x;
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void fold_kernel(const double* part, int6
 
 template <int KIND>
 __global__ __launch_bounds__(kFinishThreads) void finish_kernel(const double* part, int64_t n,
-                                                                float max_norm, zsp_clip* out) {
+                                                                double max_norm, zsp_clip* out) {
     double v = join_strided<KIND>(part, threadIdx.x, kFinishThreads, n);
     v = block_join<KIND, kFinishThreads>(v);
     if (threadIdx.x == 0) write_record(v, KIND, max_norm, out);
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(kFinishThreads) void finish_kernel(const double* pa
 // written. A total that is no norm's (negative) gives a NaN.
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void combine_kernel(const zsp_clip* parts, int32_t n,
-                                                           float max_norm, zsp_clip* out) {
+                                                           double max_norm, zsp_clip* out) {
     double v = 0.0;
     for (int64_t i = threadIdx.x; i < n; i += kThreads) {
         double t = parts[i].total;
@@ -477,7 +477,7 @@ void tensor_args(const TensorsLaunch& L, TensorArgs& a) {
 
 template <int KIND, bool ONE>
 hipError_t list_norm_t(const TensorsLaunch& L, double* part, int64_t blocks, int32_t add_to,
-                       float max_norm, zsp_clip* out, hipStream_t stream) {
+                       double max_norm, zsp_clip* out, hipStream_t stream) {
     const dim3 grid(static_cast<uint32_t>(blocks)), block(ONE ? kOneThreads : kWaveLanes);
     if (L.n_args > 0) {
         TensorArgs a{};
@@ -501,7 +501,7 @@ hipError_t list_norm_t(const TensorsLaunch& L, double* part, int64_t blocks, int
 }
 
 template <int KIND>
-hipError_t finish_t(double* part, int64_t n, int64_t parts_cap, float max_norm, zsp_clip* out,
+hipError_t finish_t(double* part, int64_t n, int64_t parts_cap, double max_norm, zsp_clip* out,
                     hipStream_t stream) {
     if (n > kFinishMax) {
         const int64_t runs = std::min<int64_t>(kFoldBlocks, (n + kThreads * 8 - 1) / (kThreads * 8));
@@ -530,7 +530,7 @@ hipError_t acc_norm_t(const AccNormArgs& a, bool pads, bool one, dim3 grid, hipS
 
 }  // namespace
 
-hipError_t launch_acc_norm(const AccNormLaunch& L, float max_norm, zsp_clip* out,
+hipError_t launch_acc_norm(const AccNormLaunch& L, double max_norm, zsp_clip* out,
                            int64_t* nparts, bool* done, hipStream_t stream) {
     *nparts = 0;
     *done = false;
@@ -559,13 +559,13 @@ hipError_t launch_acc_norm(const AccNormLaunch& L, float max_norm, zsp_clip* out
 }
 
 hipError_t launch_finish(double* part, int64_t n, int64_t parts_cap, zsp_norm_kind kind,
-                         float max_norm, zsp_clip* out, hipStream_t stream) {
+                         double max_norm, zsp_clip* out, hipStream_t stream) {
     return kind == ZSP_NORM_MAX
                ? finish_t<ZSP_NORM_MAX>(part, n, parts_cap, max_norm, out, stream)
                : finish_t<ZSP_NORM_L2>(part, n, parts_cap, max_norm, out, stream);
 }
 
-hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, float max_norm,
+hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, double max_norm,
                           zsp_clip* out, hipStream_t stream) {
     if (kind == ZSP_NORM_MAX)
         hipLaunchKernelGGL(combine_kernel<ZSP_NORM_MAX>, dim3(1), dim3(kThreads), 0, stream, parts,
@@ -578,7 +578,7 @@ hipError_t launch_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, 
 
 bool list_norm_is_small(int64_t nchunk) { return nchunk <= kOneWaves; }
 
-hipError_t launch_list_norm_one(const TensorsLaunch& L, zsp_norm_kind kind, float max_norm,
+hipError_t launch_list_norm_one(const TensorsLaunch& L, zsp_norm_kind kind, double max_norm,
                                 zsp_clip* out, hipStream_t stream) {
     return kind == ZSP_NORM_MAX
                ? list_norm_t<ZSP_NORM_MAX, true>(L, nullptr, 1, 0, max_norm, out, stream)

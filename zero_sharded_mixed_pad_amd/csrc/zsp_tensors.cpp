@@ -134,7 +134,7 @@ zsp_status finish(const NormCall& nc, int64_t nparts, hipStream_t stream) {
 extern "C" {
 
 zsp_status zsp_norm_many(const void* const* x, const int64_t* numel, const int32_t* dtype,
-                         int32_t n, zsp_norm_kind kind, float max_norm, void* ws,
+                         int32_t n, zsp_norm_kind kind, double max_norm, void* ws,
                          int64_t ws_bytes, zsp_clip* out, void* stream) {
     using namespace zsp;
     const NormCall nc{kind, max_norm, ws, ws_bytes, out};
@@ -222,7 +222,7 @@ zsp_status zsp_tensor_list_create(void* const* x, const int64_t* numel, const in
     return ZSP_OK;
 }
 
-zsp_status zsp_tensor_list_norm(const zsp_tensor_list* list, zsp_norm_kind kind, float max_norm,
+zsp_status zsp_tensor_list_norm(const zsp_tensor_list* list, zsp_norm_kind kind, double max_norm,
                                 void* ws, int64_t ws_bytes, zsp_clip* out, void* stream) {
     using namespace zsp;
     const NormCall nc{kind, max_norm, ws, ws_bytes, out};

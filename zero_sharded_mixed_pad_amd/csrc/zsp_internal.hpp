@@ -336,7 +336,7 @@ hipError_t launch_gather(const GatherLaunch& L, zsp_dtype dtype, hipStream_t str
 // a long list of them first, and the ticket by which the last of the
 // workgroups that do so knows itself: the launch that writes a long list
 // sets it to 0.
-constexpr int kFoldBlocks = 256;
+constexpr int kFoldBlocks = 128;
 constexpr int kNormBlocks = 4096;  // workgroups of an accumulator or list norm at most
 // Partials of a norm over E-space of `total` elements in at most nd spans:
 // two per tile a span meets, and what the accumulator norm needs.

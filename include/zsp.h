@@ -364,7 +364,7 @@ void zsp_gather_list_destroy(zsp_gather_list* list);
  * ws_bytes >= what zsp_norm_workspace says; its contents mean nothing between
  * calls). Calls in one stream's order may share a workspace; calls that may
  * run at the same time, replays of captured graphs among them, each need
- * their own. Equal inputs and sizes give equal bits: no atomics.
+ * their own. Equal inputs give equal bits.
  *   Errors beside each call's own: ZSP_EINVAL for a bad kind, a negative or
  * NaN max_norm, a NULL or misaligned ws, out or clip; ZSP_ERANGE if ws_bytes
  * is too small. */

@@ -709,7 +709,8 @@ zsp_status zsp_reduce_norm(zsp_plan* P, int32_t rank_or_all, const void* const* 
 zsp_status zsp_clip_combine(const zsp_clip* parts, int32_t n, zsp_norm_kind kind, double max_norm,
                             zsp_clip* out, void* stream) {
     if (n < 0) return fail(ZSP_EINVAL, "n = %d is negative", n);
-    if (kind != ZSP_NORM_L2 && kind != ZSP_NORM_MAX) return fail(ZSP_EINVAL, "bad norm kind %d", kind);
+    if (kind != ZSP_NORM_L2 && kind != ZSP_NORM_MAX)
+        return fail(ZSP_EINVAL, "bad norm kind %d", kind);
     if (!(max_norm >= 0.0))
         return fail(ZSP_EINVAL, "max_norm must be >= 0 (got %g)", max_norm);
     zsp_status st = n > 0 ? zsp::check_clip(parts, "parts") : ZSP_OK;

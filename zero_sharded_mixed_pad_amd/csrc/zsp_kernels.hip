@@ -46,6 +46,13 @@
 //    and adds rank r's values strictly after rank r-1's (fixed order,
 //    bit-exact); the ranks are loaded 8 at a time (16 at a time for more
 //    than 16 ranks), so 8 to 32 loads per lane are in flight.
+//  * A norm rides on a reduce: a lane squares what it has just stored, the
+//    wave joins its lanes (zsp_wave.hpp) and writes one 8-byte partial. The
+//    reduce of a 202 M element layer over 8 ranks of bf16 takes 643 us with
+//    the norm and 615 without (accumulating: 763 and 755), joining the
+//    partials included, where reading the accumulator again takes 123. A
+//    clipped update multiplies the gradient by the record's coefficient: no
+//    difference in time (922 us and 925, Adam alone).
 //  * Floating point: built with -ffp-contract=off; division and square root
 //    are the default correctly rounded expansions; bf16 narrowing is the
 //    hardware round-to-nearest-even convert (v_cvt_pk_bf16_f32).
@@ -220,12 +227,12 @@ constexpr bool is_adam(int op) {
 // whose layer-by-layer calls are one launch for all ranks.
 constexpr bool in_spans(int op) { return has_norm(op) || has_clip(op); }
 
-// What a wave keeps beside its tile: the range of its span; the clipping coefficient of a clipped
-// update; a norm op's running value. The sum of squares is held in 64 bits:
-// no square of a finite fp32 value leaves their range at either end, and the
-// rounding of a sum of 2^40 of them stays under the last rounding of the
-// norm to fp32. The largest absolute value is kept as its bit pattern, whose
-// integer order puts a NaN above everything.
+// What a wave keeps beside its tile: the range of its span; the clipping
+// coefficient of a clipped update; a norm op's running value. The sum of
+// squares is held in 64 bits: no square of a finite fp32 value leaves their
+// range at either end, and the roundings of a sum stay far under the norm's
+// last one to fp32. The largest absolute value is kept as its bit pattern,
+// whose integer order puts a NaN above everything.
 template <int OP>
 struct Tally {
     int64_t e_begin = 0, e_end = 0;

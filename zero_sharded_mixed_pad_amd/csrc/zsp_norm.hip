@@ -13,7 +13,7 @@
 // kept as a bit pattern: the integer order of non-negative floats, with
 // every NaN above infinity, so a NaN anywhere comes out as NaN. Partials go
 // to the caller's workspace and are joined in an order fixed by the sizes
-// alone, without atomics: equal inputs give equal bits.
+// alone: equal inputs give equal bits.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -118,10 +118,10 @@ __device__ __forceinline__ u32x4 ld16(const char* p) {
 // A wave takes groups of kGroup elements (one batch of loads), every n-th one
 // of its rank's span, n the waves of the span. One wave per workgroup; a norm
 // of at most kOneWaves groups is one workgroup, which writes the record
-// itself. No load of the
-// accumulator waits for a table: a group inside one piece needs the table
-// only to know that, and one that meets pad slots marks them in a bitmap in
-// LDS, a lane per piece, and zeroes what it loaded there.
+// itself. No load of the accumulator waits for a table: a group inside one
+// piece needs the table only to know that, and one that meets pad slots
+// marks them in a bitmap in LDS, a lane per piece, and zeroes what it loaded
+// there.
 constexpr int kGroup = kBatch * kWaveLanes * 4;
 constexpr int kGroupTiles = kGroup / kTile;
 
@@ -244,9 +244,9 @@ struct TableArgs {
     int64_t nchunk;
     double* part;
     const zsp_clip* clip;
-    zsp_clip* out;   // of the one-workgroup form
+    zsp_clip* out;    // of the one-workgroup form
     double max_norm;  // likewise
-    int32_t add_to;  // partials already there that a list norm joins
+    int32_t add_to;   // partials already there that a list norm joins
 };
 
 struct TensorArgs {
@@ -514,9 +514,11 @@ template <int KIND>
 hipError_t finish_t(double* part, int64_t n, int64_t parts_cap, double max_norm, zsp_clip* out,
                     hipStream_t stream) {
     if (n > kFinishMax) {
-        const int64_t runs = std::min<int64_t>(kFoldBlocks, (n + kThreads * 8 - 1) / (kThreads * 8));
+        const int64_t per = kThreads * 8;  // a round of loads
+        const int64_t runs = std::min<int64_t>(kFoldBlocks, (n + per - 1) / per);
         hipLaunchKernelGGL(fold_kernel<KIND>, dim3(static_cast<uint32_t>(runs)), dim3(kThreads), 0,
-                           stream, part, n, part + parts_cap, norm_ticket(part, parts_cap), max_norm, out);
+                           stream, part, n, part + parts_cap, norm_ticket(part, parts_cap),
+                           max_norm, out);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(finish_kernel<KIND>, dim3(1), dim3(kFinishThreads), 0, stream, part, n,

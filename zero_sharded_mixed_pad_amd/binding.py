@@ -5,6 +5,7 @@ current stream becomes the hipStream_t, Python lists become C arrays. Every
 step of the path runs in libzsp's HIP kernels. There is no fallback: if
 libzsp.so is missing, importing this module raises.
 """
+import array
 import ctypes
 import os
 import weakref
@@ -153,16 +154,21 @@ def _dtype_code(t):
 def _grad_array(grads, n_d, min_elems=0):
     if len(grads) != n_d:
         raise ValueError(f"need {n_d} gradient buffers, got {len(grads)}")
-    dt = grads[0].dtype
-    if not all([isinstance(g, torch.Tensor) and g.dtype is dt and g.is_cuda and
-                g.is_contiguous() and g.numel() >= min_elems for g in grads]):
+    dt, T = grads[0].dtype, torch.Tensor
+    try:                                  # a few passes in C: up to 256 ranks, every step
+        good = (all([g.is_cuda and g.dtype is dt for g in grads]) and
+                all(map(T.is_contiguous, grads)) and min(map(T.numel, grads)) >= min_elems)
+        ptrs = array.array("Q", map(T.data_ptr, grads))
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
         for i, g in enumerate(grads):     # say which, and why
-            if isinstance(g, torch.Tensor) and g.numel() < min_elems:
+            if isinstance(g, T) and g.numel() < min_elems:
                 raise ValueError(f"grads[{i}] holds {g.numel()} elements; this layout reads "
                                  f"{min_elems}")
         for i, g in enumerate(grads):
             _ptr(g, dt, f"grads[{i}]")
-    return (ctypes.c_void_p * n_d)(*[g.data_ptr() for g in grads]), _dtype_code(grads[0])
+    return (ctypes.c_void_p * n_d).from_buffer(ptrs), _dtype_code(grads[0])
 
 
 def _need(t, n, what):
@@ -513,21 +519,25 @@ _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _tensor_arrays(tensors):
-    n, dev = len(tensors), torch.cuda.current_device()
-    if not all([isinstance(t, torch.Tensor) and t.is_contiguous() and t.get_device() == dev and
-                t.dtype in _CODES for t in tensors]):
+    n, dev, T = len(tensors), torch.cuda.current_device(), torch.Tensor
+    try:                                  # a few passes in C: lists may be long
+        codes = array.array("i", [_CODES[t.dtype] for t in tensors])
+        good = all(map(T.is_contiguous, tensors)) and {dev}.issuperset(map(T.get_device, tensors))
+        ptrs = array.array("Q", map(T.data_ptr, tensors))
+        sizes = array.array("q", map(T.numel, tensors))
+    except (AttributeError, KeyError, TypeError):
+        good = False
+    if not good:
         for i, t in enumerate(tensors):   # say which, and why
-            if not isinstance(t, torch.Tensor):
+            if not isinstance(t, T):
                 raise TypeError(f"tensors[{i}] must be a torch tensor")
             _dtype_code(t)
             if not t.is_contiguous():
                 raise ValueError(f"tensors[{i}] must be contiguous")
             if t.get_device() != dev:
                 raise ValueError(f"tensors[{i}] is on {t.device}; the current device is {dev}")
-    m = max(n, 1)
-    return ((ctypes.c_void_p * m)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int64 * m)(*[t.numel() for t in tensors]),
-            (ctypes.c_int32 * m)(*[_CODES[t.dtype] for t in tensors]), n)
+    return ((ctypes.c_void_p * n).from_buffer(ptrs), (ctypes.c_int64 * n).from_buffer(sizes),
+            (ctypes.c_int32 * n).from_buffer(codes), n)
 
 
 def zsp_norm_many(tensors, out, ws, max_norm=float("inf"), kind="l2", stream=None):

@@ -465,6 +465,50 @@ def test_max_counts_every_place():
         assert rec_of(rec)[0] == 2.0 + i, p
 
 
+def test_norms_past_2_32_elements():
+    """A state of more than 2^32 elements over two ranks, one pad slot (NaN):
+    marks at both ends, past 2^31 and past 2^32 all count, in the
+    accumulator's norm and in the reduced gradient's, for either layout."""
+    n, nd = (1 << 32) + 4101, 2
+    plan = zsp.partition([n, 3], nd)
+    S = plan.S
+    assert 2 * S > n + 3                                  # pads
+    acc = torch.zeros(2 * S, device=dev())
+    work = torch.zeros(2 * S, dtype=BF, device=dev())
+    plan.bind_state(zsp.ALL_RANKS, acc, acc, acc, work, acc)   # nothing here writes state
+    s0 = plan.tensor(0)["shard_len"]
+    last = S + (n - s0) - 1                               # parameter 0's last element
+    marks = {0: 3.0, 1 << 31: 4.0, S - 3: 2.0, (1 << 32) + 7: 6.0, last: 12.0}
+    for i, x in marks.items():
+        acc[i] = x
+    acc[last + 1] = float("nan")
+    acc[2 * S - 1] = float("nan")
+    ws, rec = plan.norm_workspace(), zsp.clip_record()
+    total = sum(x * x for x in marks.values())
+    plan.grad_norm(zsp.ALL_RANKS, rec, ws)
+    assert rec_of(rec)[0] == total
+    plan.grad_norm_params(1, 0, 1, rec, ws, kind="max")
+    assert rec_of(rec)[0] == 12.0
+    grads = [work, torch.zeros(2 * S, dtype=BF, device=dev())]
+    for r, g in enumerate(grads):
+        for i, x in marks.items():
+            g[i] = x * (0.25 if r else 0.75)
+        g[last + 1] = float("nan")
+        g[2 * S - 1] = float("nan")
+    plan.reduce_norm(zsp.ALL_RANKS, grads, rec, ws, layout="shard")
+    assert rec_of(rec)[0] == total
+    for g in grads:                                       # the same buffers read as full ones
+        g.zero_()
+        for i, x in ((0, 1.0), (s0 + 5, 2.0), ((1 << 32) + 1, 3.0), (n - 1, 4.0), (n, math.nan),
+                     (n + 1, 5.0)):
+            g[i] = x / 2
+    full = plan.tensor(1)["full_off"]
+    assert full == n + 1                                  # one pad slot behind parameter 0
+    plan.reduce_norm(zsp.ALL_RANKS, grads, rec, ws)
+    assert rec_of(rec)[0] == 1.0 + 4.0 + 9.0 + 16.0 + 25.0
+    plan.destroy()
+
+
 # ---- clipped updates -------------------------------------------------------------------
 
 def same_state(A, B, what, names=STATE):
@@ -600,8 +644,9 @@ def test_capture_and_replay(case):
     numels, nd = LAYOUTS[case]
     A, B = Mirror(numels, nd), Mirror(numels, nd)
     grads = grads_of(A, BF, ("graph", case), poison=False)
-    _, xs = make_list(SIZES[7], [(BF, FP)[i % 2] for i in range(len(SIZES[7]))], "graph", 1)
-    _, ys = make_list(SIZES[7], [(BF, FP)[i % 2] for i in range(len(SIZES[7]))], "graph", 1)
+    types = [(BF, FP)[i % 2] for i in range(len(SIZES[9]))]
+    _, xs = make_list(SIZES[9], types, "graph", 1)       # 700 tensors: six launches one-shot
+    _, ys = make_list(SIZES[9], types, "graph", 1)
     la, lb = zsp.TensorList(xs), zsp.TensorList(ys)
     wa, wb = A.plan.norm_workspace(), B.plan.norm_workspace()
     ra, rb = zsp.clip_record(4), zsp.clip_record(4)

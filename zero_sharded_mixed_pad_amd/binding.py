@@ -122,11 +122,10 @@ def _check(status):
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream, without making a Stream object
-        return ctypes.c_void_p(
-            torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _ptr(t, dtype, what):
@@ -399,8 +398,8 @@ def clip_record(n=1, device="cuda"):
 
 def clip_values(rec):
     """(total, norm, coef) of records: views of shape [n], no copy, no wait."""
-    _, _, norm, coef = rec.view(torch.float32).unbind(1)
-    return rec[:, 0], norm, coef
+    f = rec.view(torch.float32)
+    return rec.select(1, 0), f.select(1, 2), f.select(1, 3)
 
 
 def _here(t, what):
@@ -411,19 +410,21 @@ def _here(t, what):
 
 def _rec(rec, what, n=1):
     """The address of n records."""
-    p = _ptr(rec, torch.float64, what)
+    if (isinstance(rec, torch.Tensor) and rec.dtype is torch.float64 and rec.is_contiguous() and
+            rec.numel() == 2 * n and rec.get_device() == torch.cuda.current_device()):
+        return rec.data_ptr()
+    _ptr(rec, torch.float64, what)        # say why not
     if rec.numel() != 2 * n:
         raise ValueError(f"{what} must be {'one clip record' if n == 1 else f'{n} clip records'}")
     _here(rec, what)
-    return p
 
 
 def _norm_args(out, ws, max_norm, kind, stream):
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
         raise TypeError("ws must be a contiguous torch tensor on the GPU")
     _here(ws, "ws")
-    return (_KINDS[kind], float(max_norm), ctypes.c_void_p(ws.data_ptr()),
-            ws.numel() * ws.element_size(), _rec(out, "out"), _stream(stream))
+    return (_KINDS[kind], float(max_norm), ws.data_ptr(), ws.nbytes, _rec(out, "out"),
+            _stream(stream))
 
 
 def zsp_norm_workspace(h=None):

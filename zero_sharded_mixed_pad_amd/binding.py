@@ -153,8 +153,9 @@ def _dtype_code(t):
 def _grad_array(grads, n_d, min_elems=0):
     if len(grads) != n_d:
         raise ValueError(f"need {n_d} gradient buffers, got {len(grads)}")
-    dt, T = grads[0].dtype, torch.Tensor
+    T = torch.Tensor
     try:                                  # a few passes in C: up to 256 ranks, every step
+        dt = grads[0].dtype
         good = (all([g.is_cuda and g.dtype is dt for g in grads]) and
                 all(map(T.is_contiguous, grads)) and min(map(T.numel, grads)) >= min_elems)
         ptrs = array.array("Q", map(T.data_ptr, grads))
@@ -162,11 +163,15 @@ def _grad_array(grads, n_d, min_elems=0):
         good = False
     if not good:
         for i, g in enumerate(grads):     # say which, and why
-            if isinstance(g, T) and g.numel() < min_elems:
+            if not isinstance(g, T):
+                raise TypeError(f"grads[{i}] must be a torch tensor")
+        for i, g in enumerate(grads):
+            if g.numel() < min_elems:
                 raise ValueError(f"grads[{i}] holds {g.numel()} elements; this layout reads "
                                  f"{min_elems}")
         for i, g in enumerate(grads):
             _ptr(g, dt, f"grads[{i}]")
+        raise TypeError("grads must be torch tensors on the GPU")
     return (ctypes.c_void_p * n_d).from_buffer(ptrs), _dtype_code(grads[0])
 
 

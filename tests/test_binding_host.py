@@ -41,3 +41,22 @@ def test_a_gradient_that_is_no_tensor_is_named(bad, at):
 def test_a_gradient_that_does_not_fit_is_named(bad, kind, says):
     with pytest.raises(kind, match=says):
         binding._grad_array([grad(), bad], 2, 8)
+
+
+@pytest.mark.parametrize("bad", [None, 3, [1.0, 2.0]])
+def test_a_record_that_is_no_tensor_is_named(bad):
+    with pytest.raises(TypeError, match="^clip must be a torch tensor$"):
+        binding._rec(bad, "clip")
+    with pytest.raises(TypeError, match="^parts must be a torch tensor$"):
+        binding.zsp_clip_combine(bad, torch.zeros(1, 2, dtype=torch.float64))
+
+
+@pytest.mark.parametrize("bad,kind,says", [
+    (torch.zeros(1, 2), TypeError, "clip must be torch.float64"),
+    (torch.zeros(2, 2, dtype=torch.float64).t(), ValueError, "clip must be contiguous"),
+    (torch.zeros(1, 2, dtype=torch.float64), ValueError, "clip must be on the GPU"),
+])
+def test_a_record_that_does_not_fit_is_named(bad, kind, says, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(kind, match=says):
+        binding._rec(bad, "clip")

@@ -418,7 +418,9 @@ def _rec(rec, what, n=1):
     if (isinstance(rec, torch.Tensor) and rec.dtype is torch.float64 and rec.is_contiguous() and
             rec.numel() == 2 * n and rec.get_device() == torch.cuda.current_device()):
         return rec.data_ptr()
-    _ptr(rec, torch.float64, what)        # say why not
+    if rec is None:                       # say why not (_ptr lets a None pass)
+        raise TypeError(f"{what} must be a torch tensor")
+    _ptr(rec, torch.float64, what)
     if rec.numel() != 2 * n:
         raise ValueError(f"{what} must be {'one clip record' if n == 1 else f'{n} clip records'}")
     _here(rec, what)

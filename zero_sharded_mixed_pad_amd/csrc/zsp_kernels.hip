@@ -1639,19 +1639,59 @@ constexpr int kHeavyFusedBytes = 40;
 constexpr int kHeavyReduceBytes = 24;
 constexpr int kShortCapBytes = 16;
 constexpr int64_t kCapMinTiles = 8192;
-// The reduces with a norm stay longer after their stores, so more of them
-// are resident. Half-tile waves: 7168 bytes from 12 read per element (the
-// 202 M element layer, 8 ranks of bf16: 646 us, 673 at 10240 and 646 at no
-// cap; accumulating 772, 782 and 780), 10240 for a reduce of 24 or more (16
-// ranks: 1178 us, 1216 at 7168 and 1255 at 13312). Over short pieces: the
-// reduce 13312 from 12 bytes (10,000 tensors, 8 ranks: 341 us, 350 at no
-// cap), 16384 from 24 (16 ranks: 622 and 651); a norm alone is as fast
-// without a cap as with any. At 2 ranks of bf16 every cap costs (462 us
-// without, 530 at 7168).
+// The ops with a norm stay longer after their stores, so more of them are
+// resident, and a cap that does not help costs much. Measured without a cap
+// and under caps of 7168, 10240, 13312 and 16384 bytes, fp32 and bf16, 1 to
+// 16 ranks, launches of 8 to 202 M elements, either gradient layout; us
+// without and with the cap named, 202 M elements where no other size stands.
+// Half-tile waves, 7168: fp32 (1 rank 515 and 514, accumulating 592 and 557;
+// 3 ranks 674 and 663, 782 and 769), and bf16 from 8 ranks (635 and 633,
+// accumulating 757 and 747, norm alone 465 and 454). With fewer bf16 ranks
+// every cap costs: 6 ranks 644 and 664, norm alone 499 and 522; 4 ranks
+// accumulating 542 and 598. From 25 M elements (3 fp32 ranks 82.6 and 80.0;
+// at 17 M 55.0 and 56.7). 10240 instead, from 4 M elements as above, for a
+// reduce that reads 28 (fp32) or 32 bytes (bf16): 6 fp32 ranks accumulating
+// 1167 and 1115, 16 bf16 ranks 1234 and 1175 (at 17 M 106 and 101); 12 bf16
+// ranks, 24 bytes, 1147 and 1163, so those keep 7168 (1128). A norm alone:
+// 10240 likewise for bf16 (16 ranks 923 and 895), no cap for fp32 from 32
+// bytes (45 M elements, 8 ranks 213 and, at 7168, 219).
+// Short pieces, 13312: an accumulating reduce from 20 bytes (10,000 tensors,
+// shard layout: 8 bf16 ranks 397 and 373, 4 fp32 ranks 387 and 367; 6 bf16
+// ranks, 16 bytes, 307 and 323), a reduce alone from 26 (14 bf16 ranks 549 and
+// 545; 10 ranks, 20 bytes, 426 and 441). 16384 from the 28 or 32 above (16
+// bf16 ranks 650 and 596; full layout 778 and 784). From 8 M elements (8 bf16
+// ranks accumulating: 105.3 and 101.7 at 24 M, 49.2 and 47.8 at 12 M, 26.0 and
+// 27.6 at 5 M). A norm alone keeps every wave there: under 32 bytes every cap
+// costs or changes nothing, from 32 16384 gains 2% in the one layout and loses
+// 2% in the other.
 constexpr size_t kLdsNorm = 7168;
 constexpr size_t kLdsNormHeavy = 10240;
 constexpr size_t kLdsNormShort = 13312;
-constexpr int kNormCapBytes = 12;
+constexpr int64_t kNormCapMinTiles = 49152;
+constexpr int64_t kNormShortMinTiles = 16384;
+constexpr int kNormCapGradBytes = 16;    // of the bf16 gradients alone
+constexpr int kNormHeavyBytes = 32;
+constexpr int kNormHeavyF32Bytes = 28;   // fp32 reduces
+constexpr int kNormShortBytes = 26;
+constexpr int kNormShortAccBytes = 20;
+
+// The reservation of an op with a norm: `grad` bytes of gradients per element
+// and `bytes` in all; 0: no cap.
+template <int OP, typename GT, int W>
+size_t norm_lds(const ShardLaunch& L, int64_t tiles, int grad, int bytes) {
+    constexpr bool f32 = sizeof(GT) == 4;
+    const bool heavy = bytes >= (f32 && is_reduce(OP) ? kNormHeavyF32Bytes : kNormHeavyBytes);
+    if constexpr (W == 1) {
+        if (!L.short_pieces || !is_reduce(OP) || tiles < kNormShortMinTiles ||
+            bytes < (reads_acc(OP) ? kNormShortAccBytes : kNormShortBytes))
+            return 0;
+        return heavy ? kLdsShortPieces : kLdsNormShort;
+    } else {
+        if (!f32 && grad < kNormCapGradBytes) return 0;
+        if (heavy) return f32 && !is_reduce(OP) ? 0 : kLdsNormHeavy;
+        return tiles < kNormCapMinTiles ? 0 : kLdsNorm;
+    }
+}
 
 size_t device_lds_per_cu() {
     static std::atomic<int> cache[64];
@@ -1679,10 +1719,7 @@ size_t shard_lds_pad(const ShardLaunch& L, int64_t tiles) {
         const int bytes = grad + (is_adam(OP) ? 12 : 0) + (reads_acc(OP) ? 4 : 0);
         size_t total = 0;
         if constexpr (has_norm(OP)) {
-            if (bytes < kNormCapBytes || (W == 1 && (!L.short_pieces || !is_reduce(OP)))) return 0;
-            const bool heavy = bytes >= kHeavyReduceBytes;
-            if constexpr (W == 1) total = heavy ? kLdsShortPieces : kLdsNormShort;
-            else total = is_reduce(OP) && heavy ? kLdsNormHeavy : kLdsNorm;
+            total = norm_lds<OP, GT, W>(L, tiles, grad, bytes);
         } else if constexpr (W == 1) {
             if (!L.short_pieces || bytes < kShortCapBytes) return 0;
             total = kLdsShortPieces;

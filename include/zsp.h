@@ -398,9 +398,9 @@ zsp_status zsp_reduce_shard_norm_params(zsp_plan* plan, int32_t rank_or_all, int
                                         void* ws, int64_t ws_bytes, zsp_clip* out, void* stream);
 
 /* The norm of the gradient that zsp_reduce_adam_step (use_acc likewise) would
- * use, writing nothing but the record: with zsp_reduce_adam_step_clip, the
- * clipped step of a caller that keeps no accumulator. Reads the gradients
- * once more than an unclipped step. */
+ * use, whole-model, writing nothing but the record: with
+ * zsp_reduce_adam_step_clip, the clipped step of a caller that keeps no
+ * accumulator. Reads the gradients once more than an unclipped step. */
 zsp_status zsp_reduce_norm(zsp_plan* plan, int32_t rank_or_all, const void* const* grads,
                            zsp_dtype dtype, zsp_grad_layout layout, int32_t use_acc,
                            zsp_norm_kind kind, double max_norm, void* ws, int64_t ws_bytes,

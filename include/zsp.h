@@ -370,9 +370,10 @@ void zsp_gather_list_destroy(zsp_gather_list* list);
  * is too small. */
 
 /* Workspace bytes for the norm calls on `plan` as it is bound now (before
- * it is bound: as for all ranks), or, with plan NULL, for norms of lists of
- * tensors: 8 bytes per 256 elements of the bound state, and about 20 KB.
- * Host only. A plan's workspace also serves lists. */
+ * it is bound: as for all ranks): the larger of 35,856 bytes and
+ * 16 * (E / 512) + 32 * nd + 1072, E the elements of the bound state and the
+ * quotient rounded down. With plan NULL, for norms of lists of tensors:
+ * 35,856. Host only. A plan's workspace also serves lists. */
 zsp_status zsp_norm_workspace(const zsp_plan* plan, int64_t* bytes);
 
 /* Norm of the bound accumulator's real elements (pad slots are left out,

@@ -15,7 +15,7 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 def stated():
     """(least, per 512 elements, per rank, constant), in bytes, from the text."""
     with open(HEADER) as f:
-        text = re.sub(r"\s+\*?\s*", " ", f.read())
+        text = re.sub(r"\n \* +", " ", f.read())
     m = re.search(r"the larger of ([\d,]+) bytes and (\d+) \* \(E / 512\) \+ (\d+) \* nd \+ (\d+)",
                   text)
     assert m, "zsp.h does not state the workspace's size"

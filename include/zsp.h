@@ -37,27 +37,29 @@
  *   optimizer state, accumulator, gather outputs, schedule arenas). A plan
  *   owns its host tables, the device copies of its offset tables (allocated
  *   in zsp_bind_state), the staging slots of long zsp_gather_many lists
- *   (allocated when such a list first needs them; a prepared list,
- *   zsp_gather_list_create, owns memory of its own) and, from its first
- *   checkpoint save or load, the checkpoint staging (pinned host chunks,
- *   streams, events); zsp_destroy frees them. The other hot-path calls
- *   (reduce, norm, Adam, the range and single gathers, schedule acquire and
- *   release) allocate nothing on the device; checkpoint calls also use host
- *   memory for their own duration. The reduce, norm, clip, Adam, range and
- *   single gather calls, zsp_gather_list_run, and zsp_gather_many on lists of
- *   at most 64 parameters, only check
- *   arguments and launch kernels (no host wait, no copy, no memset), so they
- *   can be captured into a HIP graph; Adam's scalars (lr, betas, eps and the
- *   step's bias corrections) are kernel arguments, so a replay repeats the
- *   step it was captured with (a clipped step reads its coefficient from
- *   device memory, so a replay uses the one that is there then).
- *   Every device pointer must be 16-byte aligned (torch allocations are).
+ *   (allocated when such a list first needs them; prepared lists,
+ *   zsp_gather_list_create and zsp_tensor_list_create, own memory of their
+ *   own) and, from its first checkpoint save or load, the checkpoint staging
+ *   (pinned host chunks, streams, events); zsp_destroy frees them. The other
+ *   hot-path calls (reduce, norm, clip, Adam, the range and single gathers,
+ *   schedule acquire and release) allocate nothing on the device; checkpoint
+ *   calls also use host memory for their own duration. The reduce, norm, clip,
+ *   Adam, range and single gather calls, zsp_gather_list_run, and
+ *   zsp_gather_many on lists of at most 64 parameters, only check arguments
+ *   and launch kernels (no host wait, no copy, no memset), so they can be
+ *   captured into a HIP graph; Adam's scalars (lr, betas, eps and the step's
+ *   bias corrections) are kernel arguments, so a replay repeats the step it
+ *   was captured with (a clipped step reads its coefficient from device
+ *   memory, so a replay uses the one that is there then).
+ *   Every device pointer must be 16-byte aligned (torch allocations are),
+ *   but for the tensors of a list to clip or to take the norm of.
  *   State arrays bound for all ranks hold nd*S elements, rank r at
  *   [r*S, (r+1)*S); bound for one rank j they hold that rank's S elements.
  *
  * Streams
  *   Every call that touches the device enqueues its kernels on `stream` (a
- *   hipStream_t; NULL is the default stream) and returns without waiting.
+ *   hipStream_t; NULL is the default stream) and returns without waiting,
+ *   unless its own comment says that it waits.
  *   The caller keeps buffers alive until the stream has run them. The plan is
  *   tied to the device that was current at zsp_bind_state; calls made with
  *   another device current fail with ZSP_ESTATE.
@@ -356,9 +358,9 @@ void zsp_gather_list_destroy(zsp_gather_list* list);
  * total is infinite or NaN, coef is NaN, and a call that takes the record
  * then changes nothing: the update of a step whose gradients are not finite
  * is skipped. max_norm >= 0 (INFINITY: only the norm is wanted, coef is 1
- * for every finite norm). Nothing here waits for the device or brings a
- * value to the host: the record (zsp_clip) stays in device memory, from where
- * the clipped calls read the coefficient.
+ * for every finite norm). Nothing here brings a value to the host, and only
+ * zsp_tensor_list_create waits for the device: the record (zsp_clip) stays in
+ * device memory, from where the clipped calls read the coefficient.
  *   Every call that makes a norm writes one record to `out` (device memory,
  * 16-byte aligned) and uses a workspace `ws` (device memory, 16-byte aligned,
  * ws_bytes >= what zsp_norm_workspace says; its contents mean nothing between

@@ -350,8 +350,8 @@ inline uint32_t* norm_ticket(double* ws, int64_t parts) {
 }
 
 // The accumulator's norm over elements [e_begin + r*stride, e_begin + r*stride
-// + e_len) of E-space for r = 0 .. spans-1, pad slots left out; adds the
-// partials written to *nparts.
+// + e_len) of E-space for r = 0 .. spans-1, pad slots left out; the number of
+// partials written goes to *nparts.
 struct AccNormLaunch {
     ShardTable tab;
     const float* acc = nullptr;

@@ -126,7 +126,6 @@ constexpr int kGroup = kBatch * kWaveLanes * 4;
 constexpr int kGroupTiles = kGroup / kTile;
 
 struct AccNormArgs {
-    const int64_t* e0;
     const PieceInfo* info;
     const int32_t* tile;
     const float* acc;
@@ -333,8 +332,8 @@ __device__ __forceinline__ void chunk_norm(const ListChunk& c, int lane, Acc<KIN
 template <int KIND, bool ONE, typename Args>
 __global__ __launch_bounds__(ONE ? kOneThreads : kWaveLanes) void list_norm_kernel(const Args a) {
     const int lane = threadIdx.x % kWaveLanes;
-    const int first =
-        ONE ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes) : norm_place(blockIdx.x, gridDim.x);
+    const int first = ONE ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveLanes)
+                          : norm_place(blockIdx.x, gridDim.x);
     Acc<KIND> t;
     for (int64_t c = first; c < a.nchunk; c += ONE ? kOneWaves : int(gridDim.x))
         chunk_norm(get_chunk(a, c), lane, t);
@@ -557,7 +556,6 @@ hipError_t launch_acc_norm(const AccNormLaunch& L, double max_norm, zsp_clip* ou
     if (L.e_len <= 0 || L.spans <= 0) return hipSuccess;
     if (L.spans > ZSP_MAX_RANKS) return hipErrorInvalidValue;
     AccNormArgs a{};
-    a.e0 = L.tab.e0;
     a.info = L.tab.info;
     a.tile = L.tab.tile;
     a.ntile = L.tab.ntile;

@@ -2,11 +2,12 @@
 // (zsp_norm_many, zsp_clip_many and the prepared zsp_tensor_list): argument
 // checks, chunk tables, launches.
 //
-// A list is cut into chunks of kListChunkBytes, each inside one tensor. A one-shot list travels in the kernel arguments,
-// kTensorArgMax tensors with elements per launch: nothing is staged, so any
-// list can be captured into a HIP graph. Later launches of a long list join
-// their partials to the first one's. A prepared list keeps one record per
-// chunk in device memory and is one launch whatever its length.
+// A list is cut into chunks of kListChunkBytes, each inside one tensor. A
+// one-shot list travels in the kernel arguments, kTensorArgMax tensors with
+// elements per launch: nothing is staged, so any list can be captured into a
+// HIP graph. Later launches of a long list join their partials to the first
+// one's. A prepared list keeps one record per chunk in device memory and is
+// one launch whatever its length.
 #include <algorithm>
 #include <climits>
 #include <new>

@@ -746,13 +746,15 @@ def cpu_baseline(runner, target_s):
 # ---------------------------------------------------------------------------
 
 _OPS = {0: "copy_in", 1: "reduce_set", 2: "reduce_acc", 3: "fused_reduce_adam_cast",
-        4: "fused_reduce_adam_cast_acc", 5: "adam_from_acc"}
+        4: "fused_reduce_adam_cast_acc", 5: "adam_from_acc",
+        6: "reduce_set_norm", 7: "reduce_acc_norm", 8: "norm", 9: "norm_acc",
+        10: "fused_clip", 11: "fused_acc_clip", 12: "adam_clip"}
 
 
 def _short(name):
     """Readable kernel name from a mangled or demangled rocprofv3 name."""
     import re
-    m = re.search(r"shard_kernel(?:ILi|<)(\d)", name)
+    m = re.search(r"shard_kernel(?:ILi|<)(\d+)", name)
     if m:
         dt = "f32" if ("ILi%sEf" % m.group(1)) in name or ", float" in name else "bf16"
         return f"{_OPS[int(m.group(1))]}[{dt}]"

@@ -52,7 +52,8 @@ METRIC = "effective GB/s (and % HBM peak) of shard reduce+Adam+cast step and par
 # Kinds of launch inside one step, in bench.py's event records.
 STEP_KINDS = ("reduce_set", "reduce_acc", "fused", "adam", "gather_acc", "gather")
 KERNEL_SOURCES = ["zero_sharded_mixed_pad_amd/csrc/zsp_kernels.hip",
-                  "zero_sharded_mixed_pad_amd/csrc/zsp_internal.hpp"]
+                  "zero_sharded_mixed_pad_amd/csrc/zsp_internal.hpp",
+                  "zero_sharded_mixed_pad_amd/csrc/zsp_wave.hpp"]
 
 
 def _code_only(text):
@@ -66,9 +67,9 @@ def _code_only(text):
 
 
 def kernel_source_hash():
-    """Hash of what determines the kernels' code: their source and header
-    (comments aside) and the device compile flags (other library sources do
-    not enter it)."""
+    """Hash of what determines the code of the shard and gather kernels: their
+    source and headers (comments aside) and the device compile flags (other
+    library sources do not enter it)."""
     import importlib.util
     h = hashlib.sha256()
     for p in KERNEL_SOURCES:

@@ -41,3 +41,13 @@ def test_shard_ops_are_named():
     assert len(names) == 2 * len(ops)
     assert bench._short(demangled(1, "float")) == "reduce_set[f32]"
     assert bench._short(mangled(4, "t")) == "fused_reduce_adam_cast_acc[bf16]"
+
+
+def test_every_header_of_the_kernels_is_in_their_hash():
+    """Stored counters count as current while the kernels' code is the same:
+    all of it, the headers that zsp_kernels.hip includes among it."""
+    with open(os.path.join(CSRC, "zsp_kernels.hip"), encoding="utf-8") as f:
+        heads = re.findall(r'#include "(zsp_\w+\.hpp)"', f.read())
+    assert "zsp_internal.hpp" in heads
+    for h in heads:
+        assert f"zero_sharded_mixed_pad_amd/csrc/{h}" in bench.KERNEL_SOURCES, h

@@ -30,6 +30,8 @@ Other modes, each printing its own JSON line:
   --prefetch    forward + backward over a Llama-7B stack through the
                 per-layer gather schedule; hidden fraction of gather time
   --checkpoint DIR   sharded checkpoint save / load / reshard-load timings
+  --operators CASES  cases of perf/operators.py (gradient norm, clipping and
+                clipped steps) through the library
   --rocprof-summary DIR, --traffic-from F W   turn rocprofv3 output into the
                 text and JSON summaries kept under profiles/
 """
@@ -120,6 +122,10 @@ def parse():
                          "decoder stack through the per-layer gather schedule at several "
                          "prefetch depths, with a matmul stand-in for the layer compute, and "
                          "print the hidden fraction of gather time as one JSON line")
+    ap.add_argument("--operators", metavar="CASE[,CASE...]", default=None,
+                    help="instead of the step: time --steps passes of cases of "
+                         "perf/operators.py ('all': every one) through the library, over "
+                         "three sets of inputs in turn, and print one JSON line")
     ap.add_argument("--layers", type=int, default=32)
     ap.add_argument("--tokens", type=int, nargs="+", default=[512, 1024, 4096])
     ap.add_argument("--depths", type=int, nargs="+", default=[1, 2])
@@ -763,6 +769,9 @@ def _short(name):
         return "gather[f32]" if ("IfE" in name or "<float>" in name) else "gather[bf16]"
     if "gather_span_kernel" in name:  # the range gather's form over short pieces (bf16)
         return "gather[bf16]"
+    m = re.search(r"zsp.*?(acc_norm|list_norm|list_clip|finish|fold|combine)_kernel", name)
+    if m:
+        return m.group(1)
     m = re.search(r"gather_list_(args|recs)", name)
     if m:
         dt = "f32" if ("IfLb" in name or "<float," in name) else "bf16"
@@ -867,6 +876,58 @@ def load_traffic(workload, kernel):
 
 # ---------------------------------------------------------------------------
 
+def operators_bench(args, say):
+    """Passes of the named cases of perf/operators.py through the library, one
+    after another over three sets of inputs: us per pass (median of five
+    blocks, the device waited for at the end of each) and the host's share."""
+    import importlib.util
+    import statistics
+    import torch
+    spec = importlib.util.spec_from_file_location(
+        "_zsp_operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    cases = {c["name"]: c for c in ops.listed()}
+    names = list(cases) if args.operators == "all" else args.operators.split(",")
+    unknown = [n for n in names if n not in cases]
+    if unknown:
+        raise SystemExit(f"unknown case {unknown[0]}; choose from {', '.join(cases)}")
+    res = {}
+    for name in names:
+        states = [ops.prepare(cases[name], seed) for seed in range(3)]
+        for i in range(max(3, args.warmup)):
+            ops.run(states[i % 3])
+        torch.cuda.synchronize()
+        blocks = []
+        for _ in range(5):
+            t0 = time.perf_counter()
+            for i in range(args.steps):
+                ops.run(states[i % 3])
+            t1 = time.perf_counter()
+            torch.cuda.synchronize()
+            blocks.append((time.perf_counter() - t0, t1 - t0))
+        us, host = (statistics.median(b[k] for b in blocks) * 1e6 / args.steps for k in (0, 1))
+        size = ops.work(cases[name])["bytes"]
+        res[name] = {"us_per_pass": round(us, 2), "host_us": round(host, 2), "bytes": size,
+                     "GBps": round(size / us / 1e3, 1)}
+        say(f"[bench] {name}: {us:.1f} us a pass, {size / us / 1e3:.0f} GB/s")
+        del states
+        torch.cuda.empty_cache()
+    return res
+
+
+def calibration_copies(device):
+    """Three plain 2 GiB device copies, for the byte counters."""
+    import torch
+    src = torch.empty(1 << 30, dtype=torch.bfloat16, device=device)
+    dst = torch.empty_like(src)
+    src.fill_(1.0)
+    for _ in range(3):
+        dst.copy_(src)
+    torch.cuda.synchronize()
+
+
 def time_workload(w, args, device, evict, say):
     """Build the workload's runner, run `warmup` untimed steps and time
     `steps` steps. Returns the runner and the workload's figures."""
@@ -954,6 +1015,13 @@ def main():
     def say(msg):
         print(msg, file=sys.stderr, flush=True)
 
+    if args.operators:
+        torch.cuda.set_device(0)
+        res = operators_bench(args, say)
+        if args.calibrate_copy:
+            calibration_copies(torch.device("cuda:0"))
+        print(json.dumps({"mode": "operators", "steps": args.steps, "cases": res}), flush=True)
+        return 0
     wl = synth.workloads()
     if args.workload not in wl:
         print(f"unknown workload {args.workload}; choose from {sorted(wl)}", file=sys.stderr)
@@ -985,13 +1053,7 @@ def main():
     roof = roofline(r, w, fig)
 
     if args.calibrate_copy:
-        src = torch.empty(1 << 30, dtype=torch.bfloat16, device=device)
-        dst = torch.empty_like(src)
-        src.fill_(1.0)
-        for _ in range(3):
-            dst.copy_(src)
-        torch.cuda.synchronize()
-        del src, dst
+        calibration_copies(device)
 
     cpu = None
     if not args.no_cpu_baseline:

@@ -51,3 +51,11 @@ def test_every_header_of_the_kernels_is_in_their_hash():
     assert "zsp_internal.hpp" in heads
     for h in heads:
         assert f"zero_sharded_mixed_pad_amd/csrc/{h}" in bench.KERNEL_SOURCES, h
+
+
+@pytest.mark.parametrize("kernel", ["acc_norm", "list_norm", "list_clip", "finish", "fold",
+                                    "combine"])
+def test_norm_kernels_are_named(kernel):
+    form = f"void zsp::(anonymous namespace)::{kernel}_kernel<0, false>(zsp::Args)"
+    assert bench._short(form) == kernel
+    assert bench._short(f"_ZN3zsp12_GLOBAL__N_1{len(kernel) + 7}{kernel}_kernelILi0EEEvv") == kernel

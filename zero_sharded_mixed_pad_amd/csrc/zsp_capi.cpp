@@ -35,7 +35,7 @@ zsp_status fail(zsp_status st, const char* fmt, ...) {
 }
 
 zsp_status fail_hip(hipError_t e, const char* what) {
-    return fail(ZSP_EHIP, "%s: %s", what, hipGetErrorString(e));
+    return fail(ZSP_EHIP, "%s: %s", what, zsp::hip_error_text(e));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -161,6 +161,11 @@ zsp_status set_error(zsp_status st, const char* fmt, ...) {
 }
 
 zsp_status set_hip_error(hipError_t e, const char* what) { return fail_hip(e, what); }
+
+const char* hip_error_text(hipError_t e) {
+    (void)hipGetLastError();
+    return hipGetErrorString(e);
+}
 
 zsp_status check_bound(const zsp_plan* P) { return ::check_bound(P); }
 
@@ -334,8 +339,9 @@ zsp_status zsp_bind_state(zsp_plan* P, int32_t rank_or_all, float* master, float
     void* blob = nullptr;
     if (total > 0) {
         e = hipMalloc(&blob, total);
-        if (e != hipSuccess) return fail(ZSP_ENOMEM, "hipMalloc of %zu table bytes: %s", total,
-                                         hipGetErrorString(e));
+        if (e != hipSuccess)
+            return fail(ZSP_ENOMEM, "hipMalloc of %zu table bytes: %s", total,
+                        zsp::hip_error_text(e));
         for (int i = 0; i < kParts; ++i) {
             if (!sz[i]) continue;
             e = hipMemcpy(static_cast<char*>(blob) + off[i], src[i], sz[i],

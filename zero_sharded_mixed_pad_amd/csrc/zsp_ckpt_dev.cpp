@@ -123,7 +123,7 @@ zsp_status follow_caller(CkptStaging* st, int n, hipStream_t caller) {
 }
 
 std::string hip_text(hipError_t e, const char* what) {
-    return std::string(what) + ": " + hipGetErrorString(e);
+    return std::string(what) + ": " + hip_error_text(e);
 }
 
 // Run job(i, lane, &message) for i in [0, n) on up to `lanes` threads (the

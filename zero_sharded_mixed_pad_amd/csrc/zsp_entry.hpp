@@ -13,6 +13,10 @@ namespace zsp {
 
 zsp_status set_error(zsp_status st, const char* fmt, ...);
 zsp_status set_hip_error(hipError_t e, const char* what);
+// The text of an error that the call is about to report. Clears the runtime's
+// record of it, which successful calls leave alone: launches are checked by
+// that record, and the next one would report the same error again.
+const char* hip_error_text(hipError_t e);
 
 // ZSP_OK if the plan has state bound on the current device, else the error.
 zsp_status check_bound(const zsp_plan* P);

@@ -204,7 +204,7 @@ extern "C" zsp_status zsp_gather_many(zsp_plan* P, const int32_t* ids, int32_t n
         s.host_cap = 0;
         if ((e = hipHostMalloc(&s.host, up)) != hipSuccess)
             return set_error(ZSP_ENOMEM, "pinned staging of %zu bytes: %s", up,
-                             hipGetErrorString(e));
+                             hip_error_text(e));
         s.host_cap = up;
     }
     if (s.dev_cap < up + z.recs) {
@@ -213,7 +213,7 @@ extern "C" zsp_status zsp_gather_many(zsp_plan* P, const int32_t* ids, int32_t n
         s.dev_cap = 0;
         if ((e = hipMalloc(&s.dev, up + z.recs)) != hipSuccess)
             return set_error(ZSP_ENOMEM, "device staging of %zu bytes: %s", up + z.recs,
-                             hipGetErrorString(e));
+                             hip_error_text(e));
         s.dev_cap = up + z.recs;
     }
     char* h = static_cast<char*>(s.host);
@@ -291,7 +291,7 @@ extern "C" zsp_status zsp_gather_list_create(zsp_plan* P, const int32_t* ids, in
             G->dev = nullptr;
             delete G;
             return set_error(ZSP_ENOMEM, "device list of %zu bytes: %s", up + z.recs,
-                             hipGetErrorString(e));
+                             hip_error_text(e));
         }
         ListLaunch L = list_base(P, src, lt);
         char* d = static_cast<char*>(G->dev);

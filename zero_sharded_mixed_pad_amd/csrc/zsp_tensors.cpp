@@ -205,7 +205,7 @@ zsp_status zsp_tensor_list_create(void* const* x, const int64_t* numel, const in
         if ((e = hipMalloc(&dev, bytes)) != hipSuccess) {
             delete L;
             return set_error(ZSP_ENOMEM, "device list of %zu bytes: %s", bytes,
-                             hipGetErrorString(e));
+                             hip_error_text(e));
         }
         const hipStream_t hs = static_cast<hipStream_t>(stream);
         e = hipMemcpyAsync(dev, host.data(), bytes, hipMemcpyHostToDevice, hs);

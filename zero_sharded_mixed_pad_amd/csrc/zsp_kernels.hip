@@ -48,11 +48,12 @@
 //    than 16 ranks), so 8 to 32 loads per lane are in flight.
 //  * A norm rides on a reduce: a lane squares what it has just stored, the
 //    wave joins its lanes (zsp_wave.hpp) and writes one 8-byte partial. The
-//    reduce of a 202 M element layer over 8 ranks of bf16 takes 643 us with
-//    the norm and 615 without (accumulating: 763 and 755), joining the
-//    partials included, where reading the accumulator again takes 123. A
-//    clipped update multiplies the gradient by the record's coefficient: no
-//    difference in time (922 us and 925, Adam alone).
+//    reduce of a 202 M element layer over 8 ranks of bf16 takes 646 us with
+//    the norm and 619 without (accumulating: 766 and 756; calls timed in turn
+//    in one process, joining the partials included), where a norm of the
+//    accumulator takes 123. A clipped update multiplies the gradient by the
+//    record's coefficient: no difference in time (938 us and 939, Adam alone,
+//    in the same run).
 //  * Floating point: built with -ffp-contract=off; division and square root
 //    are the default correctly rounded expansions; bf16 narrowing is the
 //    hardware round-to-nearest-even convert (v_cvt_pk_bf16_f32).
@@ -1640,9 +1641,9 @@ constexpr int kHeavyReduceBytes = 24;
 constexpr int kShortCapBytes = 16;
 constexpr int64_t kCapMinTiles = 8192;
 // The ops with a norm stay longer after their stores, so more of them are
-// resident, and a cap that does not help costs much. Measured without a cap
+// resident, and a cap that does not help costs much. One sweep, without a cap
 // and under caps of 7168, 10240, 13312 and 16384 bytes, fp32 and bf16, 1 to
-// 16 ranks, launches of 8 to 202 M elements, either gradient layout; us
+// 16 ranks, launches of 5 to 202 M elements, either gradient layout; us a call
 // without and with the cap named, 202 M elements where no other size stands.
 // Half-tile waves, 7168: fp32 (1 rank 515 and 514, accumulating 592 and 557;
 // 3 ranks 674 and 663, 782 and 769), and bf16 from 8 ranks (635 and 633,

@@ -20,6 +20,7 @@ F32, BF16 = 0, 1
 GRADS_FULL, GRADS_SHARD = 0, 1
 SRC_WORK, SRC_MASTER, SRC_ACC = 0, 1, 2
 NORM_L2, NORM_MAX = 0, 1
+HEAD_GRAD_HIDDEN, HEAD_GRAD_HEAD, HEAD_UNALIGNED = 1, 2, 4
 ALL_RANKS = -1
 MAX_RANKS = 256
 
@@ -85,6 +86,11 @@ def _load():
         "zsp_tensor_list_norm": (i32, [vp, i32, f64, vp, i64, vp, vp]),
         "zsp_tensor_list_clip": (i32, [vp, vp, vp]),
         "zsp_tensor_list_destroy": (None, [vp]),
+        "zsp_head_workspace": (i32, [i64, i64, i64, i32, i32, i32, i64p]),
+        "zsp_head_loss": (i32, [vp, vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp, vp, i64,
+                                vp]),
+        "zsp_head_distill": (i32, [vp, vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, f32, vp, vp,
+                                   vp, vp, vp, i64, vp]),
         "zsp_checkpoint_write_host": (i32, [vp, i32, ctypes.c_char_p, i64, vp, vp, vp, vp]),
         "zsp_checkpoint_read_host": (i32, [vp, i32, ctypes.c_char_p, i64p, vp, vp, vp, vp]),
         "zsp_checkpoint_save": (i32, [vp, i32, ctypes.c_char_p, i64, vp]),
@@ -614,6 +620,95 @@ class TensorList:
             self.close()
         except Exception:
             pass
+
+
+# ---- losses over the head --------------------------------------------------
+
+def zsp_head_workspace(n, v, d, dtype, top=0, grad_hidden=True, grad_head=True, aligned=True):
+    """Bytes of workspace of a head_loss call (top = 0) or a head_distill call
+    with `top` entries per token: n tokens, a head of v rows of d. aligned
+    False: for a head that may start off a 16-byte boundary."""
+    code = {torch.float32: F32, torch.bfloat16: BF16}.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    flags = ((HEAD_GRAD_HIDDEN if grad_hidden else 0) | (HEAD_GRAD_HEAD if grad_head else 0) |
+             (0 if aligned else HEAD_UNALIGNED))
+    out = ctypes.c_int64()
+    _check(lib.zsp_head_workspace(int(n), int(v), int(d), code, int(top), flags,
+                                  ctypes.byref(out)))
+    return out.value
+
+
+def head_workspace(n, v, d, dtype, top=0, grad_hidden=True, grad_head=True, aligned=True,
+                   device="cuda"):
+    """A workspace for such calls. Calls that may run at the same time, or
+    captured graphs that may be replayed so, each need their own."""
+    return torch.empty(zsp_head_workspace(n, v, d, dtype, top, grad_hidden, grad_head, aligned),
+                       dtype=torch.uint8, device=device)
+
+
+def _addr(t, dtype, shape, what):
+    """The address of a contiguous tensor of that type and shape on the
+    current device; 0 for None."""
+    if t is None:
+        return 0
+    try:                                  # checked in a few attribute reads
+        good = (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda and
+                t.get_device() == torch.cuda.current_device())
+    except AttributeError:
+        good = False
+    if not good:
+        _ptr(t, dtype, what)              # say which, and why
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+        _here(t, what)
+    return t.data_ptr()
+
+
+def _head_args(hidden, head, loss, ws, token_weight, lse, grad_hidden, grad_head):
+    for t, what in ((hidden, "hidden"), (head, "head"), (loss, "loss"), (ws, "ws")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch tensor")
+    if hidden.dim() != 2 or head.dim() != 2 or hidden.shape[1] != head.shape[1]:
+        raise ValueError(f"hidden must be [n, d] and head [v, d], got {tuple(hidden.shape)} and "
+                         f"{tuple(head.shape)}")
+    dt, code = hidden.dtype, _dtype_code(hidden)
+    (n, d), v = hidden.shape, head.shape[0]
+    f32 = torch.float32
+    return (n, d, v, code, _addr(hidden, dt, (n, d), "hidden"), _addr(head, dt, (v, d), "head"),
+            _addr(token_weight, f32, (n,), "token_weight"), _addr(loss, f32, (n,), "loss"),
+            _addr(lse, f32, (n,), "lse"), _addr(grad_hidden, dt, (n, d), "grad_hidden"),
+            _addr(grad_head, dt, (v, d), "grad_head"),
+            _addr(ws, torch.uint8, (ws.numel(),), "ws"), ws.numel())
+
+
+def zsp_head_loss(hidden, head, target, loss, ws, token_weight=None, scale=1.0, lse=None,
+                  grad_hidden=None, grad_head=None, stream=None):
+    """Softmax cross entropy of hidden [n, d] over head [v, d] with target [n]
+    (int64): loss, lse [n] (float32) and the gradients of
+    scale * sum(token_weight * loss), in the inputs' type, where given."""
+    n, d, v, code, x, w, tw, lo, ls, gx, gw, wsp, wsn = _head_args(
+        hidden, head, loss, ws, token_weight, lse, grad_hidden, grad_head)
+    _check(lib.zsp_head_loss(x, w, code, n, v, d, _addr(target, torch.int64, (n,), "target"), tw,
+                             float(scale), lo, ls, gx, gw, wsp, wsn, _stream(stream)))
+
+
+def zsp_head_distill(hidden, head, index, logit, loss, ws, temperature=1.0, token_weight=None,
+                     scale=1.0, lse=None, grad_hidden=None, grad_head=None, stream=None):
+    """Distillation over head from a teacher's top logits: logit [n, k]
+    (float32) at index [n, k] (int64); the rest as zsp_head_loss."""
+    n, d, v, code, x, w, tw, lo, ls, gx, gw, wsp, wsn = _head_args(
+        hidden, head, loss, ws, token_weight, lse, grad_hidden, grad_head)
+    if not isinstance(index, torch.Tensor) or index.dim() != 2:
+        raise ValueError("index must be a torch tensor [n, k]")
+    k = index.shape[1]
+    _check(lib.zsp_head_distill(x, w, code, n, v, d, _addr(index, torch.int64, (n, k), "index"),
+                                _addr(logit, torch.float32, (n, k), "logit"), k,
+                                float(temperature), tw, float(scale), lo, ls, gx, gw, wsp, wsn,
+                                _stream(stream)))
+
+
+head_loss, head_distill = zsp_head_loss, zsp_head_distill
 
 
 # ---- per-layer gather schedule -----------------------------------------------

@@ -1,0 +1,196 @@
+// zsp_head.cpp -- entry points of the losses over the head (zsp_head_loss,
+// zsp_head_distill, zsp_head_workspace): argument checks, the layout of the
+// workspace, and how a call is cut.
+#include <algorithm>
+#include <cmath>
+
+#include "zsp_entry.hpp"
+#include "zsp_head.hpp"
+
+namespace zsp {
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxDepth = 65536;
+// The softmax of at most so many bytes is kept at a time.
+constexpr int64_t kKeptBytes = int64_t(1) << 31;
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Parts of a sum of `len` terms so that a product of `tiles` tiles fills the
+// card, each at least 8 stages of 64 long.
+int32_t split_of(int64_t tiles, int64_t len) {
+    const int64_t want = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), len / 512);
+    return int32_t(std::min<int64_t>(std::max<int64_t>(want, 1), kHeadMaxSplit));
+}
+
+zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
+                      int32_t flags, HeadShape* out) {
+    if (dtype != ZSP_F32 && dtype != ZSP_BF16) return set_error(ZSP_EINVAL, "bad dtype %d", dtype);
+    if (n < 0 || v < 1 || d < 1 || top < 0)
+        return set_error(ZSP_EINVAL, "n = %lld, v = %lld, d = %lld, top = %d", (long long)n,
+                         (long long)v, (long long)d, top);
+    if (flags & ~(ZSP_HEAD_GRAD_HIDDEN | ZSP_HEAD_GRAD_HEAD | ZSP_HEAD_UNALIGNED))
+        return set_error(ZSP_EINVAL, "bad flags %d", flags);
+    if (n > kMaxTokens || v > kMaxVocab || d > kMaxDepth || top > kHeadMaxTop)
+        return set_error(ZSP_ERANGE, "n = %lld, v = %lld, d = %lld or top = %d is too large",
+                         (long long)n, (long long)v, (long long)d, top);
+    HeadShape s;
+    s.n = n;
+    s.v = v;
+    s.d = d;
+    s.f32 = dtype == ZSP_F32;
+    s.teacher = top > 0;
+    s.top = std::max(top, 1);
+    s.top_pad = s.top == 1 ? 1 : int32_t(up(s.top, 4));
+    s.grad_hidden = flags & ZSP_HEAD_GRAD_HIDDEN;
+    s.grad_head = flags & ZSP_HEAD_GRAD_HEAD;
+    s.planes = s.f32 ? 3 : 1;
+    s.rows = up(n, kHeadTile);
+    s.vp = up(v, kHeadTile);
+    s.dp = up(d, kHeadDepth);
+    s.pack_head = s.f32 || d % kHeadDepth != 0 || (flags & ZSP_HEAD_UNALIGNED);
+    const bool grads = s.grad_hidden || s.grad_head;
+    // per token: P (and its planes), or the partials alone
+    const int64_t per = grads ? s.vp * (s.f32 ? 4 + 2 * s.planes : 2) : s.vp / kHeadBlock * 8;
+    int64_t chunk = std::max<int64_t>(kKeptBytes / per / kHeadTile * kHeadTile, kHeadTile);
+    s.nchunk = std::max<int64_t>((n + chunk - 1) / chunk, 1);
+    s.chunk = up((n + s.nchunk - 1) / s.nchunk, kHeadTile);
+    if (s.chunk > 0) s.nchunk = std::max<int64_t>((n + s.chunk - 1) / s.chunk, 1);
+    const int64_t da = (s.dp + 127) / 128;
+    if (s.grad_hidden) s.split_hidden = split_of(da * ((s.chunk + 127) / 128), v);
+    if (s.grad_head) s.split_head = split_of(da * ((v + 127) / 128), s.chunk);
+
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at = up(at + bytes, 256);
+        return o;
+    };
+    s.o_count = take(4);
+    s.o_rows = take(s.rows * 4);
+    s.o_coef = take(s.rows * 4);
+    s.o_entry = take(s.rows * s.top_pad * 4);
+    s.o_pick = take(s.rows * s.top_pad * 4);
+    if (s.teacher) s.o_flag = take(n);
+    s.o_x = take(s.rows * s.dp * 2 * s.planes);
+    if (s.pack_head) s.o_w = take(v * s.dp * 2 * s.planes);
+    s.o_part = take(s.chunk * (s.vp / kHeadBlock) * 8);
+    if (grads) s.o_p = take(s.chunk * s.vp * (s.f32 ? 4 : 2));
+    if (grads && s.f32) s.o_g = take(s.chunk * s.vp * 2 * s.planes);
+    int64_t split = 0;
+    if (s.split_hidden > 1) split = s.split_hidden * s.chunk * s.dp * 4;
+    if (s.split_head > 1) split = std::max(split, s.split_head * v * s.dp * 4);
+    s.o_split = take(split);
+    if (s.grad_head && s.nchunk > 1) s.o_acc = take(v * s.dp * 4);
+    s.bytes = at;
+    *out = s;
+    return ZSP_OK;
+}
+
+struct Span {
+    const char* what;
+    const void* p;
+    int64_t bytes;
+    int32_t align;
+    bool written;
+};
+
+// Pointers present and aligned, and nothing written that another argument holds.
+zsp_status check_spans(const Span* s, int n) {
+    for (int i = 0; i < n; ++i) {
+        if (!s[i].p || s[i].bytes == 0) continue;
+        if (reinterpret_cast<uintptr_t>(s[i].p) % uintptr_t(s[i].align))
+            return set_error(ZSP_EINVAL, "%s is not aligned to %d bytes", s[i].what, s[i].align);
+    }
+    for (int i = 0; i < n; ++i) {
+        if (!s[i].written || !s[i].p || s[i].bytes == 0) continue;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), ae = a + uintptr_t(s[i].bytes);
+        for (int j = 0; j < n; ++j) {
+            if (j == i || !s[j].p || s[j].bytes == 0) continue;
+            const uintptr_t b = reinterpret_cast<uintptr_t>(s[j].p);
+            if (a < b + uintptr_t(s[j].bytes) && b < ae)
+                return set_error(ZSP_EINVAL, "%s overlaps %s", s[i].what, s[j].what);
+        }
+    }
+    return ZSP_OK;
+}
+
+zsp_status head_call(HeadCall c, int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
+                     int64_t ws_bytes, void* stream) {
+    int32_t flags = (c.grad_hidden ? ZSP_HEAD_GRAD_HIDDEN : 0) |
+                    (c.grad_head ? ZSP_HEAD_GRAD_HEAD : 0) |
+                    (reinterpret_cast<uintptr_t>(c.head) % 16 ? ZSP_HEAD_UNALIGNED : 0);
+    HeadShape s;
+    zsp_status st = make_shape(n, v, d, dtype, top, flags, &s);
+    if (st != ZSP_OK) return st;
+    if (!std::isfinite(c.scale)) return set_error(ZSP_EINVAL, "scale is not finite");
+    if (!(c.temperature > 0.0f) || !std::isfinite(c.temperature))
+        return set_error(ZSP_EINVAL, "temperature = %g is not above 0", double(c.temperature));
+    if (!c.head) return set_error(ZSP_EINVAL, "head is NULL");
+    if (!c.ws) return set_error(ZSP_EINVAL, "ws is NULL");
+    if (n > 0) {
+        if (!c.hidden) return set_error(ZSP_EINVAL, "hidden is NULL");
+        if (!c.index) return set_error(ZSP_EINVAL, top ? "index is NULL" : "target is NULL");
+        if (top && !c.logit) return set_error(ZSP_EINVAL, "logit is NULL");
+        if (!c.loss) return set_error(ZSP_EINVAL, "loss is NULL");
+    }
+    const int32_t e = s.f32 ? 4 : 2;
+    const Span spans[] = {
+        {"hidden", c.hidden, n * d * e, e, false},
+        {"head", c.head, v * d * e, e, false},
+        {top ? "index" : "target", c.index, n * s.top * 8, 8, false},
+        {"logit", c.logit, n * s.top * 4, 4, false},
+        {"token_weight", c.token_weight, n * 4, 4, false},
+        {"loss", c.loss, n * 4, 4, true},
+        {"lse", c.lse, n * 4, 4, true},
+        {"grad_hidden", c.grad_hidden, n * d * e, e, true},
+        {"grad_head", c.grad_head, v * d * e, e, true},
+        {"ws", c.ws, ws_bytes, 16, true},
+    };
+    if (ws_bytes < s.bytes)
+        return set_error(ZSP_ERANGE, "ws_bytes = %lld, %lld are needed", (long long)ws_bytes,
+                         (long long)s.bytes);
+    if ((st = check_spans(spans, int(sizeof(spans) / sizeof(spans[0])))) != ZSP_OK) return st;
+    const hipError_t err = launch_head(s, c, static_cast<hipStream_t>(stream));
+    if (err != hipSuccess) return set_hip_error(err, "head loss launch");
+    return ZSP_OK;
+}
+
+}  // namespace
+}  // namespace zsp
+
+extern "C" {
+
+zsp_status zsp_head_workspace(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
+                              int32_t flags, int64_t* bytes) {
+    using namespace zsp;
+    if (!bytes) return set_error(ZSP_EINVAL, "bytes is NULL");
+    HeadShape s;
+    const zsp_status st = make_shape(n, v, d, dtype, top, flags, &s);
+    if (st == ZSP_OK) *bytes = s.bytes;
+    return st;
+}
+
+zsp_status zsp_head_loss(const void* hidden, const void* head, zsp_dtype dtype, int64_t n,
+                         int64_t v, int64_t d, const int64_t* target, const float* token_weight,
+                         float scale, float* loss, float* lse, void* grad_hidden, void* grad_head,
+                         void* ws, int64_t ws_bytes, void* stream) {
+    using namespace zsp;
+    const HeadCall c{hidden, head, target, nullptr, token_weight, scale, 1.0f, loss, lse,
+                     grad_hidden, grad_head, static_cast<char*>(ws)};
+    return head_call(c, n, v, d, dtype, 0, ws_bytes, stream);
+}
+
+zsp_status zsp_head_distill(const void* hidden, const void* head, zsp_dtype dtype, int64_t n,
+                            int64_t v, int64_t d, const int64_t* index, const float* logit,
+                            int32_t top, float temperature, const float* token_weight, float scale,
+                            float* loss, float* lse, void* grad_hidden, void* grad_head, void* ws,
+                            int64_t ws_bytes, void* stream) {
+    using namespace zsp;
+    if (top < 1) return set_error(ZSP_EINVAL, "top = %d is below 1", top);
+    const HeadCall c{hidden, head, index, logit, token_weight, scale, temperature, loss, lse,
+                     grad_hidden, grad_head, static_cast<char*>(ws)};
+    return head_call(c, n, v, d, dtype, top, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,57 @@
+// zsp_head.hpp -- what the entry points of the head's losses (zsp_head.cpp)
+// and their kernels (zsp_head.hip) share: one call's arguments, sizes and
+// workspace.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "zsp.h"
+
+namespace zsp {
+
+constexpr int32_t kHeadTile = 256;       // rows and columns of P are padded to it
+constexpr int32_t kHeadBlock = 64;       // vocabulary columns per partial of a softmax
+constexpr int32_t kHeadDepth = 64;       // d is padded to it
+constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
+constexpr int32_t kHeadMaxSplit = 64;
+
+// Sizes of a call, and the byte offsets of its parts of the workspace.
+struct HeadShape {
+    int64_t n = 0, v = 0, d = 0;
+    int32_t top = 1;              // entries per token (a target is one)
+    bool f32 = false, teacher = false;
+    bool grad_hidden = false, grad_head = false;
+    bool pack_head = false;       // the head is copied: fp32, d or its address not aligned
+    int32_t planes = 1;           // bf16 planes of an operand: 3 hold an fp32 value
+    int32_t top_pad = 1;          // entries per row in the workspace
+    int64_t rows = 0;             // n padded to kHeadTile
+    int64_t vp = 0, dp = 0;       // v padded to kHeadTile, d to kHeadDepth
+    int64_t chunk = 0;            // tokens whose softmax is kept at a time
+    int64_t nchunk = 0;
+    int32_t split_hidden = 1, split_head = 1;  // parts of the gradients' long sums
+    // offsets
+    int64_t o_count = 0, o_rows = 0, o_coef = 0, o_entry = 0, o_pick = 0, o_flag = 0, o_x = 0,
+            o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
+    int64_t bytes = 0;
+};
+
+struct HeadCall {
+    const void* hidden;
+    const void* head;
+    const int64_t* index;         // target [n], or the teacher's [n, top]
+    const float* logit;           // the teacher's [n, top], else NULL
+    const float* token_weight;    // [n] or NULL
+    float scale, temperature;
+    float* loss;                  // [n]
+    float* lse;                   // [n] or NULL
+    void* grad_hidden;
+    void* grad_head;
+    char* ws;
+};
+
+// Every launch of a call, in order, on `stream`.
+hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream);
+
+}  // namespace zsp

@@ -512,7 +512,7 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * sums, the losses and a target's own g in 64 bits. For bf16, p and
  * scale * token_weight_i * g_iv are each rounded to bf16 before the two
  * products that make the gradients. Equal inputs give equal bits.
- *   0 <= n <= 2^24 tokens, 1 <= v <= 2^24, 1 <= d <= 65536, top <= 1024.
+ *   0 <= n <= 2^24 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024.
  * Pointers need the alignment of their element type only, ws 16 bytes; a head
  * on 16 bytes whose d is a multiple of 64 is read in place (bf16), any other is
  * copied into the workspace first. No plan is involved: all tensors are on

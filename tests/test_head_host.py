@@ -50,7 +50,7 @@ EINVAL, ERANGE = binding.EINVAL, binding.ERANGE
     (EINVAL, "v = 0", dict(v=0)),
     (EINVAL, "d = 0", dict(d=0)),
     (ERANGE, "too large", dict(n=(1 << 24) + 1)),
-    (ERANGE, "too large", dict(v=(1 << 24) + 1)),
+    (ERANGE, "too large", dict(v=(1 << 22) + 1)),
     (ERANGE, "too large", dict(d=65537)),
     (EINVAL, "hidden is NULL", dict(hidden=None)),
     (EINVAL, "head is NULL", dict(head=None)),

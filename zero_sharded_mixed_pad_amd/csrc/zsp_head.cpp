@@ -10,7 +10,7 @@
 namespace zsp {
 namespace {
 
-constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 24, kMaxDepth = 65536;
+constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 22, kMaxDepth = 65536;
 // The softmax of at most so many bytes is kept at a time.
 constexpr int64_t kKeptBytes = int64_t(1) << 31;
 

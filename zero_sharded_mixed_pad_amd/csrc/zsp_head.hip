@@ -248,6 +248,15 @@ struct GemmArgs {
 
 enum { kLogits = 0, kOut = 1 };
 
+// 16 bytes a lane from base + off to lds + 16 * lane. In assembly: the
+// compiler would wait for every such load before each transposing LDS read.
+// Nothing else here uses m0. The caller waits (wait_stage).
+__device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, ZSP_LDS char* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(uint32_t(uintptr_t(lds)));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off),
+                 "s"(base)
+                 : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_stage() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
@@ -276,7 +285,7 @@ __device__ __forceinline__ void transpose4(uint32_t x[4]) {
 // the groups in a row is changed on the reading side of the load: group c of
 // a row is kept at c ^ s(row), which spreads the lanes of one LDS read over
 // the banks.
-template <int X, int BK, int WAVES, bool MMAJ>
+template <int X, int BK, int WAVES, bool MMAJ, bool CLAMP>
 struct Operand {
     static constexpr int kGroups = X * BK / 8;
     static constexpr int kLoads = kGroups / 64 / WAVES;
@@ -292,49 +301,43 @@ struct Operand {
         return ((k & 3) << 1) | (((k >> 3) & 1) << 3);
     }
 
-    const uint16_t* base;
-    int64_t ld;
-    int64_t off[kLoads];      // M-major: the column; K-major: the element at k = 0
+    const char* base;         // of the tile's first row (M-major: column)
+    int64_t ld;               // bytes
+    uint32_t off[kLoads];     // bytes from base; M-major: of the first row
     int32_t krow[kLoads];     // M-major
-    int64_t klast;
 
     __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int64_t x0, int64_t nx,
-                                         int64_t klast_, int wave, int lane) {
-        base = p;
-        ld = ld_;
-        klast = klast_;
+                                         int wave, int lane) {
+        ld = ld_ * 2;
+        base = reinterpret_cast<const char*>(p) + x0 * (MMAJ ? 2 : ld);
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int q = (wave * kLoads + i) * 64 + lane;
             if constexpr (MMAJ) {
-                const int k = q / (X / 8), c = (q % (X / 8)) ^ m_swizzle(k);
+                const int k = q / (X / 8);
+                int64_t x = ((q % (X / 8)) ^ m_swizzle(k)) * 8;
+                x = x0 + x + 8 <= nx ? x : nx - 8 - x0;
                 krow[i] = k;
-                const int64_t x = x0 + c * 8;
-                off[i] = x + 8 <= nx ? x : nx - 8;
+                off[i] = uint32_t(x * 2 + (CLAMP ? 0 : k * ld));
             } else {
-                const int row = q / (BK / 8), c = (q % (BK / 8)) ^ k_swizzle(row);
-                const int64_t x = x0 + row;
-                off[i] = (x < nx ? x : nx - 1) * ld + c * 8;
+                const int r = q / (BK / 8), c = (q % (BK / 8)) ^ k_swizzle(r);
+                const int64_t x = x0 + r < nx ? r : nx - 1 - x0;
+                off[i] = uint32_t(x * ld + c * 16);
                 krow[i] = 0;
             }
         }
     }
-    // Loads of the stage whose first k is k0 into `lds`.
-    __device__ __forceinline__ void issue(ZSP_LDS char* lds, int64_t plane, int64_t k0, int wave) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint16_t* src;
-            if constexpr (MMAJ) {
-                int64_t k = k0 + krow[i];
-                k = k < klast ? k : klast;
-                src = base + plane + k * ld + off[i];
-            } else {
-                src = base + plane + off[i] + k0;
-            }
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)src,
-                (ZSP_LDS void*)(lds + (wave * kLoads + i) * 1024), 16, 0, 0);
+    // Load i of the stage whose first k is k0 into `lds`. CLAMP: rows past
+    // k_last are read as that one.
+    __device__ __forceinline__ void issue(int i, ZSP_LDS char* lds, int64_t plane, int64_t k0,
+                                          int64_t k_last, int wave) {
+        const char* src = base + 2 * plane + (MMAJ ? k0 * ld : k0 * 2);
+        uint32_t o = off[i];
+        if constexpr (CLAMP) {
+            const int32_t k = k_last - k0 < BK ? int32_t(k_last - k0) : BK;
+            o += uint32_t(krow[i] < k ? krow[i] : k) * uint32_t(ld);
         }
+        load_to_lds(src, o, lds + (wave * kLoads + i) * 1024);
     }
     // The operand's 16 x 32 values for tile `x` (a multiple of 16, of the
     // wave's share at x_wave) and k's [32 kk, 32 kk + 32).
@@ -362,17 +365,17 @@ struct Operand {
 __device__ __forceinline__ int plane_a_of(int seg) { return (0x201010 >> (4 * seg)) & 0xf; }
 __device__ __forceinline__ int plane_b_of(int seg) { return (0x021100 >> (4 * seg)) & 0xf; }
 
-template <int BA, int BB, int WA, int WB, int BK, int NST, bool AM, bool BM, bool F32, int KIND>
+template <int BA, int BB, int WA, int WB, bool AM, bool BM, bool F32, int KIND>
 __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
-    constexpr int kWaves = WA * WB;
+    constexpr int kWaves = WA * WB, BK = kHeadDepth;
     constexpr int EA = BA / WA, EB = BB / WB, TA = EA / 16, TB = EB / 16;
     static_assert(EA == kHeadBlock && TA == 4, "a wave's columns are one block");
-    using OpA = Operand<BA, BK, kWaves, AM>;
-    using OpB = Operand<BB, BK, kWaves, BM>;
+    using OpA = Operand<BA, BK, kWaves, AM, AM && !BM>;  // the head's rows end at v
+    using OpB = Operand<BB, BK, kWaves, BM, false>;
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
     constexpr int kPer = OpA::kLoads + OpB::kLoads;
     constexpr int kSegs = F32 ? 6 : 1;
-    __shared__ __attribute__((aligned(1024))) char s_mem[NST * kStage];
+    __shared__ __attribute__((aligned(1024))) char s_mem[2 * kStage];
 
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -411,50 +414,78 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 
     OpA oa;
     OpB ob;
-    oa.init(g.a, g.lda, a0, g.na, g.k_real - 1, wave, lane);
-    ob.init(g.b, g.ldb, b0, BM ? g.ldb : (b0 + BB), int64_t(1) << 60, wave, lane);
+    oa.init(g.a, g.lda, a0, g.na, wave, lane);
+    ob.init(g.b, g.ldb, b0, BM ? g.ldb : (b0 + BB), wave, lane);
 
-    int i_kt = 0, i_seg = 0;  // the next stage to load
-    auto issue = [&](int buf) {
+    int i_kt = 0, i_seg = 0, i_left = steps;  // the next stage to load
+    auto issue = [&](int buf, int from, int to) {
         ZSP_LDS char* lds = (ZSP_LDS char*)s_mem + buf * kStage;
         const int64_t k0 = int64_t(kt0 + i_kt) * BK;
-        oa.issue(lds, F32 ? plane_a_of(i_seg) * g.plane_a : 0, k0, wave);
-        ob.issue(lds + OpA::kBytes, F32 ? plane_b_of(i_seg) * g.plane_b : 0, k0, wave);
-        if (++i_kt == nkt) {
+#pragma unroll
+        for (int i = from; i < to; ++i) {
+            if (i < OpA::kLoads)
+                oa.issue(i, lds, F32 ? plane_a_of(i_seg) * g.plane_a : 0, k0, g.k_real - 1, wave);
+            else
+                ob.issue(i - OpA::kLoads, lds + OpA::kBytes,
+                         F32 ? plane_b_of(i_seg) * g.plane_b : 0, k0, 0, wave);
+        }
+        // past the last stage it is loaded again: nothing reads it
+        if (to == kPer && --i_left > 0 && ++i_kt == nkt) {
             i_kt = 0;
             ++i_seg;
         }
     };
-    int buf_in = 0, buf = 0;
-    for (int s = 0; s < NST - 1 && s < steps; ++s) issue(buf_in++);
-    for (int it = 0; it < steps; ++it) {
-        // this stage has landed for every wave, and every wave has read the
-        // stage whose buffer is filled next
-        if (it + NST - 2 < steps) wait_stage<(NST - 2) * kPer>();
-        else wait_stage<0>();
+    // Stage s is read from buffer s % 2. Its first half of the k's is read into
+    // registers while the matrix cores work on the stage before, its second
+    // half while they work on the first, so that they wait for neither.
+    bf16x8 fa[2][TA], fb[2][TB];
+    int buf = 0;
+    auto read = [&](int half, int from, int i) {
+        ZSP_LDS const char* la = (ZSP_LDS const char*)s_mem + from * kStage;
+        if (i < TA) fa[half][i] = OpA::frag(la, wa * EA, i * 16, half, lane);
+        else fb[half][i - TA] = OpB::frag(la + OpA::kBytes, wb * EB, (i - TA) * 16, half, lane);
+    };
+    // Half a stage: the tiles of `half` multiplied, with the reads of the
+    // other half (of buffer `from`) and, where `load`, the loads of the stage
+    // after next between them, a quarter of each at a time.
+    constexpr int kParts = 4, kMul = TA * TB / kParts;
+    auto work = [&](auto half_c, int from, auto load_c) {
+        constexpr int half = decltype(half_c)::value;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+#pragma unroll
+            for (int i = (TA + TB) * q / kParts; i < (TA + TB) * (q + 1) / kParts; ++i)
+                read(half ^ 1, from, i);
+            if constexpr (decltype(load_c)::value)
+                issue(from ^ 1, kPer * q / kParts, kPer * (q + 1) / kParts);
+#pragma unroll
+            for (int i = kMul * q; i < kMul * (q + 1); ++i)
+                acc[i % TA][i / TA] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    fa[half][i % TA], fb[half][i / TA], acc[i % TA][i / TA], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    using std::integral_constant;
+    if (steps > 0) {
+        issue(0, 0, kPer);
+        issue(1, 0, kPer);
+        wait_stage<kPer>();
         wg_barrier();
-        if (it + NST - 1 < steps) {
-            issue(buf_in);
-            buf_in = buf_in + 1 == NST ? 0 : buf_in + 1;
-        }
-        ZSP_LDS const char* la = (ZSP_LDS const char*)s_mem + buf * kStage;
-        ZSP_LDS const char* lb = la + OpA::kBytes;
-        buf = buf + 1 == NST ? 0 : buf + 1;
 #pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            bf16x8 fa[TA], fb[TB];
-#pragma unroll
-            for (int i = 0; i < TA; ++i) fa[i] = OpA::frag(la, wa * EA, i * 16, kk, lane);
-#pragma unroll
-            for (int i = 0; i < TB; ++i) fb[i] = OpB::frag(lb, wb * EB, i * 16, kk, lane);
-#pragma unroll
-            for (int b = 0; b < TB; ++b)
-#pragma unroll
-                for (int a = 0; a < TA; ++a)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[a], fb[b], acc[a][b], 0,
-                                                                         0, 0);
-        }
+        for (int i = 0; i < TA + TB; ++i) read(0, 0, i);
     }
+    for (int it = 0; it < steps; ++it) {
+        __builtin_amdgcn_sched_barrier(0);
+        work(integral_constant<int, 0>(), buf, integral_constant<bool, false>());
+        // this wave has read all of this stage, and its part of the next has
+        // landed; then that holds for every wave
+        wait_stage<0>();
+        wg_barrier();
+        buf ^= 1;
+        // behind the last stage: loaded and read, not used
+        work(integral_constant<int, 1>(), buf, integral_constant<bool, true>());
+    }
+    wait_stage<0>();  // no load into LDS outlives the workgroup
 
     // A lane holds, of each 16 x 16 tile, column lane % 16 (a row of the
     // output) at rows 4 (lane / 16) + 0..3 (its columns).
@@ -793,18 +824,28 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 
 // ---- launches ------------------------------------------------------------------------
 
-template <int BA, int BB, int WA, int WB, int BK, int NST, bool AM, bool BM, bool F32, int KIND>
+template <int BA, int BB, int WA, int WB, bool AM, bool BM, bool F32, int KIND>
 hipError_t run_gemm(const GemmArgs& g, hipStream_t stream) {
     const int64_t tiles = (g.na + BA - 1) / BA * ((g.nb + BB - 1) / BB);
     if (tiles == 0) return hipSuccess;
-    gemm_kernel<BA, BB, WA, WB, BK, NST, AM, BM, F32, KIND>
+    gemm_kernel<BA, BB, WA, WB, AM, BM, F32, KIND>
         <<<dim3(uint32_t((tiles + 7) / 8 * 8), uint32_t(g.nsplit)), 64 * WA * WB, 0, stream>>>(g);
     return hipGetLastError();
 }
 
+// Tiles of 256 x 256 (eight waves, one workgroup on a CU) reach 1.3 PFLOP/s
+// on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
+// 1.05: the smaller are taken where the larger leave more of the card idle.
 template <bool AM, bool BM, bool F32, int KIND>
 hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
-    return run_gemm<128, 128, 2, 2, 64, 2, AM, BM, F32, KIND>(g, stream);
+    auto turns = [&](int64_t tile, int64_t at_once) {
+        const int64_t t = (g.na + tile - 1) / tile * ((g.nb + tile - 1) / tile) * g.nsplit;
+        return (t + at_once - 1) / at_once;
+    };
+    // a turn is 65536 outputs on a CU at 130, or 32768 at 105
+    if (turns(256, 256) * 2 * 105 <= turns(128, 512) * 130)
+        return run_gemm<256, 256, 4, 2, AM, BM, F32, KIND>(g, stream);
+    return run_gemm<128, 128, 2, 2, AM, BM, F32, KIND>(g, stream);
 }
 
 template <bool F32>

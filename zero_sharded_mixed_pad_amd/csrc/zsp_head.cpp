@@ -16,13 +16,6 @@ constexpr int64_t kKeptBytes = int64_t(1) << 31;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-// Parts of a sum of `len` terms so that a product of `tiles` tiles fills the
-// card, each at least 8 stages of 64 long.
-int32_t split_of(int64_t tiles, int64_t len) {
-    const int64_t want = std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), len / 512);
-    return int32_t(std::min<int64_t>(std::max<int64_t>(want, 1), kHeadMaxSplit));
-}
-
 zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
                       int32_t flags, HeadShape* out) {
     if (dtype != ZSP_F32 && dtype != ZSP_BF16) return set_error(ZSP_EINVAL, "bad dtype %d", dtype);
@@ -56,10 +49,6 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.nchunk = std::max<int64_t>((n + chunk - 1) / chunk, 1);
     s.chunk = up((n + s.nchunk - 1) / s.nchunk, kHeadTile);
     if (s.chunk > 0) s.nchunk = std::max<int64_t>((n + s.chunk - 1) / s.chunk, 1);
-    const int64_t da = (s.dp + 127) / 128;
-    if (s.grad_hidden) s.split_hidden = split_of(da * ((s.chunk + 127) / 128), v);
-    if (s.grad_head) s.split_head = split_of(da * ((v + 127) / 128), s.chunk);
-
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = at;
@@ -77,10 +66,7 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.o_part = take(s.chunk * (s.vp / kHeadBlock) * 8);
     if (grads) s.o_p = take(s.chunk * s.vp * (s.f32 ? 4 : 2));
     if (grads && s.f32) s.o_g = take(s.chunk * s.vp * 2 * s.planes);
-    int64_t split = 0;
-    if (s.split_hidden > 1) split = s.split_hidden * s.chunk * s.dp * 4;
-    if (s.split_head > 1) split = std::max(split, s.split_head * v * s.dp * 4);
-    s.o_split = take(split);
+    s.o_split = take(head_split_bytes(s));
     if (s.grad_head && s.nchunk > 1) s.o_acc = take(v * s.dp * 4);
     s.bytes = at;
     *out = s;

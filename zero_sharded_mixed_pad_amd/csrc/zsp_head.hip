@@ -32,7 +32,9 @@ namespace zsp {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -92,9 +94,16 @@ __global__ __launch_bounds__(256) void flag_kernel(const int64_t* index, const f
     if (threadIdx.x % 64 == 0) flag[i] = on;
 }
 
-// rows[0 .. count): the tokens that count, in order. One workgroup; each
-// thread counts a run of tokens, the runs are joined by a scan.
-constexpr int kScanThreads = 1024;
+__device__ __forceinline__ bool counts(const int64_t* target, const float* weight,
+                                       const uint8_t* flag, int64_t i, int64_t v) {
+    if (flag) return flag[i] != 0;
+    const int64_t e = target[i];
+    return e >= 0 && e < v && (!weight || weight[i] != 0.0f);
+}
+
+// rows[0 .. count): the tokens that count, in order. One workgroup, 16 tokens
+// a thread at a time; the waves' counts are joined in LDS.
+constexpr int kScanThreads = 1024, kScanRun = 16;
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* target,
                                                             const float* weight,
                                                             const uint8_t* flag, int64_t n,
@@ -102,25 +111,31 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* targe
                                                             int32_t* count) {
     __shared__ int32_t s_wave[kScanThreads / 64];
     const int t = threadIdx.x, lane = t % 64, wave = t / 64;
-    auto counts = [&](int64_t i) -> bool {
-        if (flag) return flag[i] != 0;
-        const int64_t e = target[i];
-        return e >= 0 && e < v && (!weight || weight[i] != 0.0f);
-    };
     int32_t done = 0;
-    for (int64_t base = 0; base < n; base += kScanThreads) {
-        const int64_t i = base + t;
-        const bool on = i < n && counts(i);
-        const uint64_t m = __ballot(on);
-        if (lane == 0) s_wave[wave] = __popcll(m);
-        __syncthreads();
-        int32_t before = done, all = 0;
-        for (int w = 0; w < kScanThreads / 64; ++w) {
-            if (w < wave) before += s_wave[w];
-            all += s_wave[w];
+    for (int64_t base = 0; base < n; base += kScanThreads * kScanRun) {
+        const int64_t first = base + wave * (64 * kScanRun) + lane;
+        bool on[kScanRun];
+#pragma unroll
+        for (int k = 0; k < kScanRun; ++k) {
+            const int64_t i = first + k * 64;
+            on[k] = i < n && counts(target, weight, flag, i, v);
         }
-        if (on) rows[before + __popcll(m & ((1ull << lane) - 1))] = int32_t(i);
-        done += all;
+        int32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kScanRun; ++k) mine += __popcll(__ballot(on[k]));
+        if (lane == 0) s_wave[wave] = mine;
+        __syncthreads();
+        int32_t at = done;
+        for (int w = 0; w < kScanThreads / 64; ++w) {
+            if (w < wave) at += s_wave[w];
+            done += s_wave[w];
+        }
+#pragma unroll
+        for (int k = 0; k < kScanRun; ++k) {
+            const uint64_t m = __ballot(on[k]);
+            if (on[k]) rows[at + __popcll(m & ((1ull << lane) - 1))] = int32_t(first + k * 64);
+            at += __popcll(m);
+        }
         __syncthreads();
     }
     if (t == 0) *count = done;
@@ -141,59 +156,81 @@ struct PackArgs {
     float* loss;
     float* lse;
     int64_t n, v, d, dp, plane;
-    int32_t top, top_pad;
+    int32_t top, top_pad, parts;
     float scale;
 };
 
-// One element of a row as its planes.
+// Eight elements of a row of d, from column c on, as planes of dp columns;
+// zeros past d, and everywhere if `in` is NULL.
 template <typename T>
-__device__ __forceinline__ void put(uint16_t* out, int64_t plane, const T* in, bool real) {
+__device__ __forceinline__ void put8(uint16_t* out, int64_t plane, const T* in, int64_t c,
+                                     int64_t d) {
     if constexpr (sizeof(T) == 2) {
-        *out = real ? *in : uint16_t(0);
+        u32x4 v = {0, 0, 0, 0};
+        if (in && c + 8 <= d) {
+            v = *reinterpret_cast<const u32x4_a2*>(in + c);
+        } else if (in) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < d) v[k / 2] |= uint32_t(in[c + k]) << (16 * (k % 2));
+        }
+        *reinterpret_cast<u32x4*>(out + c) = v;
     } else {
-        uint16_t h[3] = {0, 0, 0};
-        if (real) split3(*in, h);
-        out[0] = h[0];
-        out[plane] = h[1];
-        out[2 * plane] = h[2];
+        float x[8];
+        if (in && c + 8 <= d) {
+            const f32x4 lo = *reinterpret_cast<const f32x4_a4*>(in + c);
+            const f32x4 hi = *reinterpret_cast<const f32x4_a4*>(in + c + 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = lo[k], x[4 + k] = hi[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = in && c + k < d ? in[c + k] : 0.0f;
+        }
+        u32x4 v[3];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint16_t p[3], q[3];
+            split3(x[2 * k], p);
+            split3(x[2 * k + 1], q);
+#pragma unroll
+            for (int h = 0; h < 3; ++h) v[h][k] = p[h] | uint32_t(q[h]) << 16;
+        }
+#pragma unroll
+        for (int h = 0; h < 3; ++h) *reinterpret_cast<u32x4*>(out + h * plane + c) = v[h];
     }
 }
 
 // Row r of the copied X, its coefficient and entries; the outputs of token r
-// where it does not count.
+// where it does not count. `parts` workgroups a row, eight columns a thread.
 template <typename T>
 __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
-    const int64_t r = blockIdx.x;
-    const int t = threadIdx.x;
+    const int64_t r = blockIdx.x / a.parts;
+    const int32_t part = int32_t(blockIdx.x - r * a.parts);
+    const int64_t c = (int64_t(part) * blockDim.x + threadIdx.x) * 8;
+    const int t = threadIdx.x, threads = blockDim.x;
     const int32_t count = *a.count;
     if (r < count) {
         const int64_t i = a.rows[r];
-        const T* in = static_cast<const T*>(a.hidden) + i * a.d;
-        uint16_t* out = a.x + r * a.dp;
-        for (int64_t c = t; c < a.dp; c += 256) put(out + c, a.plane, in + c, c < a.d);
-        for (int32_t k = t; k < a.top_pad; k += 256) {
-            int64_t e = k < a.top ? a.index[i * a.top + k] : -1;
-            if (a.logit && k < a.top && a.logit[i * a.top + k] == -__builtin_inff()) e = -1;
-            a.entry[r * a.top_pad + k] = e >= 0 && e < a.v ? int32_t(e) : -1;
+        if (c < a.dp)
+            put8(a.x + r * a.dp, a.plane, static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
+        if (part == 0) {
+            for (int32_t k = t; k < a.top_pad; k += threads) {
+                int64_t e = k < a.top ? a.index[i * a.top + k] : -1;
+                if (a.logit && k < a.top && a.logit[i * a.top + k] == -__builtin_inff()) e = -1;
+                a.entry[r * a.top_pad + k] = e >= 0 && e < a.v ? int32_t(e) : -1;
+            }
+            if (t == 0) a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
         }
-        if (t == 0) a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
     } else if (r < (int64_t(count) + kHeadTile - 1) / kHeadTile * kHeadTile) {
-        for (int64_t c = t; c < a.dp; c += 256)
-            put<T>(a.x + r * a.dp + c, a.plane, nullptr, false);
+        if (c < a.dp) put8<T>(a.x + r * a.dp, a.plane, nullptr, c, a.d);
     }
-    if (r < a.n) {
-        bool on;
-        if (a.flag) on = a.flag[r] != 0;
-        else {
-            const int64_t e = a.index[r];
-            on = e >= 0 && e < a.v && (!a.weight || a.weight[r] != 0.0f);
-        }
-        if (on) return;
+    if (r < a.n && !counts(a.index, a.weight, a.flag, r, a.v)) {
         if (a.grad_hidden) {
             T* out = static_cast<T*>(a.grad_hidden) + r * a.d;
-            for (int64_t c = t; c < a.d; c += 256) out[c] = T(0);
+            for (int64_t k = int64_t(part) * threads + t; k < a.d; k += int64_t(a.parts) * threads)
+                out[k] = T(0);
         }
-        if (t == 0) {
+        if (t == 0 && part == 0) {
             a.loss[r] = 0.0f;
             if (a.lse) a.lse[r] = 0.0f;
         }
@@ -203,10 +240,10 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
 // The head's rows in planes of dp columns.
 template <typename T>
 __global__ __launch_bounds__(256) void pack_head_kernel(const T* head, uint16_t* out, int64_t d,
-                                                        int64_t dp, int64_t plane) {
-    const int64_t r = blockIdx.x;
-    for (int64_t c = threadIdx.x; c < dp; c += 256)
-        put(out + r * dp + c, plane, head + r * d + c, c < d);
+                                                        int64_t dp, int64_t plane, int32_t parts) {
+    const int64_t r = blockIdx.x / parts;
+    const int64_t c = ((blockIdx.x - r * parts) * blockDim.x + threadIdx.x) * 8;
+    if (c < dp) put8(out + r * dp, plane, head + r * d, c, d);
 }
 
 // ---- the products --------------------------------------------------------------------
@@ -226,7 +263,7 @@ struct GemmArgs {
     const int32_t* count;      // tokens that count
     int64_t first;             // the chunk's first token
     int32_t tokens_in_b, tokens_in_k;
-    uint32_t nsplit;
+    uint32_t slot_bits;        // log2 of the tiles the card runs at once; 0: sums are not split
     // logits
     float inv_temp;
     float2* part;              // [b][na_blocks]
@@ -242,8 +279,9 @@ struct GemmArgs {
     const int32_t* rows;       // row of b, or NULL: b itself
     int32_t aligned;           // rows of out start on 16 bytes
     const float* acc_in;       // fp32 [b][ldf] to add, or NULL
-    float* acc_out;            // fp32 [split][b][ldf], instead of out
-    int64_t ldf, split_stride;
+    float* acc_out;            // fp32 [b][ldf], instead of out
+    float* split;              // fp32 [part of the sum][b][ldf], if the sums are split
+    int64_t ldf;
 };
 
 enum { kLogits = 0, kOut = 1 };
@@ -253,8 +291,11 @@ enum { kLogits = 0, kOut = 1 };
 // Nothing else here uses m0. The caller waits (wait_stage).
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, ZSP_LDS char* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(uint32_t(uintptr_t(lds)));
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    const uint64_t from = uint64_t(__builtin_amdgcn_readfirstlane(uint32_t(p >> 32))) << 32 |
+                          uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p)));
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off),
-                 "s"(base)
+                 "s"(from)
                  : "memory");
 }
 template <int N>
@@ -267,17 +308,44 @@ __device__ __forceinline__ void wg_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// x[a] of the four 16-lane rows g -> x[g] of row a: what row g holds of four
-// tiles becomes what tile g holds in four rows.
-__device__ __forceinline__ void transpose4(uint32_t x[4]) {
-    auto s = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-    x[0] = s[0]; x[1] = s[1];
-    s = __builtin_amdgcn_permlane16_swap(x[2], x[3], false, false);
-    x[2] = s[0]; x[3] = s[1];
-    s = __builtin_amdgcn_permlane32_swap(x[0], x[2], false, false);
-    x[0] = s[0]; x[2] = s[1];
-    s = __builtin_amdgcn_permlane32_swap(x[1], x[3], false, false);
-    x[1] = s[0]; x[3] = s[1];
+// Two neighbouring 16 x 16 tiles of a wave as bf16, eight columns a lane: the
+// lanes of rows 1 and 3 (16 lanes each) hand their four columns of the first
+// tile to rows 0 and 2 for theirs of the second, so that the four lanes of an
+// output row write 64 bytes of it.
+__device__ __forceinline__ u32x4 pair_of(f32x4 lo, f32x4 hi) {
+    const uint32_t x0 = bf16_pair(lo[0], lo[1]), y0 = bf16_pair(lo[2], lo[3]);
+    const uint32_t x1 = bf16_pair(hi[0], hi[1]), y1 = bf16_pair(hi[2], hi[3]);
+    const auto x = __builtin_amdgcn_permlane16_swap(x0, x1, false, false);
+    const auto y = __builtin_amdgcn_permlane16_swap(y0, y1, false, false);
+    return u32x4{x[0], y[0], x[1], y[1]};
+}
+// The first of a lane's eight columns of the two tiles.
+__device__ __forceinline__ int pair_column(int lane_row) {
+    return (lane_row & 1) * 16 + (lane_row >> 1) * 8;
+}
+
+// Parts of the sums of a product of `tiles` tiles over `stages` steps of k (of
+// `segs` stages each), on a card that runs 2^slot_bits tiles at once: as few
+// turns as the parts, the turns' beginnings and ends (about four stages) and
+// the joining of the parts (a tile's bytes there and back: 1/16 of a stage)
+// allow. Where tokens do not count the device alone knows the tiles, so both
+// sides ask it here. 0 slot_bits: the sums are not split.
+__host__ __device__ inline uint32_t split_of(uint32_t tiles, uint32_t stages, uint32_t segs,
+                                             uint32_t slot_bits) {
+    if (slot_bits == 0 || tiles == 0 || tiles >> slot_bits >= 64) return 1;
+    constexpr uint32_t kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64};
+    uint32_t best = 1, least = ~0u;
+#pragma unroll
+    for (uint32_t s : kParts) {
+        const uint32_t turns = (tiles * s + (1u << slot_bits) - 1) >> slot_bits;
+        const uint32_t cost =
+            turns * ((stages + s - 1) / s * segs + 4) * 16 + (s > 1 ? tiles * s : 0);
+        if ((s == 1 || (s * 8 <= stages * segs && s <= stages && turns <= 64)) && cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
 }
 
 // One operand's share of a stage in LDS: X rows (or columns) of BK k's, in
@@ -365,7 +433,7 @@ struct Operand {
 __device__ __forceinline__ int plane_a_of(int seg) { return (0x201010 >> (4 * seg)) & 0xf; }
 __device__ __forceinline__ int plane_b_of(int seg) { return (0x021100 >> (4 * seg)) & 0xf; }
 
-template <int BA, int BB, int WA, int WB, bool AM, bool BM, bool F32, int KIND>
+template <int BA, int BB, int WA, int WB, int NST, bool AM, bool BM, bool F32, int KIND>
 __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     constexpr int kWaves = WA * WB, BK = kHeadDepth;
     constexpr int EA = BA / WA, EB = BB / WB, TA = EA / 16, TB = EB / 16;
@@ -375,7 +443,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
     constexpr int kPer = OpA::kLoads + OpB::kLoads;
     constexpr int kSegs = F32 ? 6 : 1;
-    __shared__ __attribute__((aligned(1024))) char s_mem[2 * kStage];
+    __shared__ __attribute__((aligned(1024))) char s_mem[NST * kStage];
 
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -384,18 +452,21 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     // XCD (workgroups go to the 8 of them in turn) takes one run of the
     // tiles, four b's at a time along all a's, so that what its L2 holds of
     // both operands is used by its neighbours.
-    int64_t nb = g.nb, klen = g.k;
-    if (g.tokens_in_b || g.tokens_in_k) {
-        int64_t c = int64_t(*g.count) - g.first;
-        c = c < 0 ? 0 : c;
-        if (g.tokens_in_b) nb = c < nb ? c : nb;
-        else klen = c < klen ? c : klen;
-    }
-    const uint32_t ta_n = uint32_t((g.na + BA - 1) / BA), tb_n = uint32_t((nb + BB - 1) / BB);
-    const uint32_t tiles = ta_n * tb_n, per = (tiles + 7) / 8;
-    const uint32_t j = blockIdx.x >> 3, lin = (blockIdx.x & 7) * per + j;
-    if (j >= per || lin >= tiles) return;
+    int32_t nb = int32_t(g.nb), klen = int32_t(g.k);
+    const int32_t tokens = max(*g.count - int32_t(g.first), 0);
+    if (g.tokens_in_b) nb = min(nb, tokens);
+    if (g.tokens_in_k) klen = min(klen, tokens);
+    const uint32_t ta_n = uint32_t(g.na + BA - 1) / BA, tb_n = uint32_t(nb + BB - 1) / BB;
+    const uint32_t kt_all = uint32_t(klen + BK - 1) / BK;
+    const uint32_t tiles = ta_n * tb_n;
+    const uint32_t ns =
+        __builtin_amdgcn_readfirstlane(split_of(tiles, kt_all, kSegs, g.slot_bits));
+    const uint32_t items = tiles * ns, per = (items + 7) / 8;
+    const uint32_t j = blockIdx.x >> 3, item = (blockIdx.x & 7) * per + j;
+    if (j >= per || item >= items) return;
     constexpr uint32_t GB = 4;
+    const uint32_t part = __builtin_amdgcn_readfirstlane(item / tiles);
+    const uint32_t lin = item - part * tiles;
     const uint32_t grp = lin / (GB * ta_n), b_first = grp * GB;
     const uint32_t gb = tb_n - b_first < GB ? tb_n - b_first : GB;
     const uint32_t rem = lin - grp * GB * ta_n, in_b = rem / gb;
@@ -408,8 +479,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 #pragma unroll
         for (int k = 0; k < TB; ++k) acc[i][k] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const uint32_t kt_all = uint32_t((klen + BK - 1) / BK);  // at most 2^18, 64 splits
-    const uint32_t kt0 = kt_all * blockIdx.y / g.nsplit, kt1 = kt_all * (blockIdx.y + 1) / g.nsplit;
+    const uint32_t kt0 = kt_all * part / ns, kt1 = kt_all * (part + 1) / ns;  // below 2^23
     const int nkt = int(kt1 - kt0), steps = nkt * kSegs;
 
     OpA oa;
@@ -435,7 +505,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
             ++i_seg;
         }
     };
-    // Stage s is read from buffer s % 2. Its first half of the k's is read into
+    // Stage s is read from buffer s % NST. Its first half of the k's is read into
     // registers while the matrix cores work on the stage before, its second
     // half while they work on the first, so that they wait for neither.
     bf16x8 fa[2][TA], fb[2][TB];
@@ -446,10 +516,10 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
         else fb[half][i - TA] = OpB::frag(la + OpA::kBytes, wb * EB, (i - TA) * 16, half, lane);
     };
     // Half a stage: the tiles of `half` multiplied, with the reads of the
-    // other half (of buffer `from`) and, where `load`, the loads of the stage
-    // after next between them, a quarter of each at a time.
+    // other half (of buffer `from`) and, where `load`, the loads of a stage to
+    // come between them, a quarter of each at a time.
     constexpr int kParts = 4, kMul = TA * TB / kParts;
-    auto work = [&](auto half_c, int from, auto load_c) {
+    auto work = [&](auto half_c, int from, auto load_c, int into) {
         constexpr int half = decltype(half_c)::value;
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
@@ -457,7 +527,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
             for (int i = (TA + TB) * q / kParts; i < (TA + TB) * (q + 1) / kParts; ++i)
                 read(half ^ 1, from, i);
             if constexpr (decltype(load_c)::value)
-                issue(from ^ 1, kPer * q / kParts, kPer * (q + 1) / kParts);
+                issue(into, kPer * q / kParts, kPer * (q + 1) / kParts);
 #pragma unroll
             for (int i = kMul * q; i < kMul * (q + 1); ++i)
                 acc[i % TA][i / TA] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -467,23 +537,24 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     };
     using std::integral_constant;
     if (steps > 0) {
-        issue(0, 0, kPer);
-        issue(1, 0, kPer);
-        wait_stage<kPer>();
+#pragma unroll
+        for (int i = 0; i < NST; ++i) issue(i, 0, kPer);
+        wait_stage<(NST - 1) * kPer>();
         wg_barrier();
 #pragma unroll
         for (int i = 0; i < TA + TB; ++i) read(0, 0, i);
     }
     for (int it = 0; it < steps; ++it) {
         __builtin_amdgcn_sched_barrier(0);
-        work(integral_constant<int, 0>(), buf, integral_constant<bool, false>());
+        work(integral_constant<int, 0>(), buf, integral_constant<bool, false>(), 0);
         // this wave has read all of this stage, and its part of the next has
         // landed; then that holds for every wave
-        wait_stage<0>();
+        wait_stage<(NST - 2) * kPer>();
         wg_barrier();
-        buf ^= 1;
+        const int old = buf;
+        buf = NST == 2 ? buf ^ 1 : buf + 1 == NST ? 0 : buf + 1;
         // behind the last stage: loaded and read, not used
-        work(integral_constant<int, 1>(), buf, integral_constant<bool, true>());
+        work(integral_constant<int, 1>(), buf, integral_constant<bool, true>(), old);
     }
     wait_stage<0>();  // no load into LDS outlives the workgroup
 
@@ -537,86 +608,65 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
             if (lg == 0 && real) g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m, s);
             if (g.p) {
                 if constexpr (F32) {
-                    float* out = static_cast<float*>(g.p) + row * g.ldp + a_wave + lg * 16;
-                    f32x4 v[TA];
+                    float* out = static_cast<float*>(g.p) + row * g.ldp + a_wave + lg * 4;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) x[a] = __float_as_uint(acc[a][b][k]);
-                        transpose4(x);
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) v[a][k] = __uint_as_float(x[a]);
-                    }
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) *reinterpret_cast<f32x4*>(out + a * 4) = v[a];
+                    for (int a = 0; a < TA; ++a)
+                        *reinterpret_cast<f32x4*>(out + a * 16) = acc[a][b];
                 } else {
-                    uint16_t* out = static_cast<uint16_t*>(g.p) + row * g.ldp + a_wave + lg * 16;
-                    uint32_t x[4], y[4];
+                    uint16_t* out = static_cast<uint16_t*>(g.p) + row * g.ldp + a_wave;
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        x[a] = bf16_pair(acc[a][b][0], acc[a][b][1]);
-                        y[a] = bf16_pair(acc[a][b][2], acc[a][b][3]);
-                    }
-                    transpose4(x);
-                    transpose4(y);
-                    *reinterpret_cast<u32x4*>(out) = u32x4{x[0], y[0], x[1], y[1]};
-                    *reinterpret_cast<u32x4*>(out + 8) = u32x4{x[2], y[2], x[3], y[3]};
+                    for (int a = 0; a < TA; a += 2)
+                        *reinterpret_cast<u32x4*>(out + a * 16 + pair_column(lg)) =
+                            pair_of(acc[a][b], acc[a + 1][b]);
                 }
             }
         }
     } else {
-        const int64_t col = a_wave + lg * 16;
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
             const int64_t row = b0 + wb * EB + b * 16 + lr;
-            f32x4 v[TA];
+            if (row >= nb) continue;  // the same for the lanes of a column of rows
+            if (ns > 1 || g.acc_in || g.acc_out) {
+                float* out = ns > 1 ? g.split + part * (int64_t(nb) * g.ldf) : g.acc_out;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t x[4];
-#pragma unroll
-                for (int a = 0; a < 4; ++a) x[a] = __float_as_uint(acc[a][b][k]);
-                transpose4(x);
-#pragma unroll
-                for (int a = 0; a < 4; ++a) v[a][k] = __uint_as_float(x[a]);
+                for (int a = 0; a < TA; ++a) {
+                    const int64_t col = a_wave + a * 16 + lg * 4;
+                    if (col >= g.na) continue;
+                    const int64_t at = row * g.ldf + col;
+                    if (ns == 1 && g.acc_in)
+                        acc[a][b] += *reinterpret_cast<const f32x4*>(g.acc_in + at);
+                    if (out) *reinterpret_cast<f32x4*>(out + at) = acc[a][b];
+                }
+                if (out) continue;
             }
-            if (row >= nb || col >= g.na) continue;
-            if (g.acc_in) {
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-                    v[a] += *reinterpret_cast<const f32x4*>(g.acc_in + row * g.ldf + col + a * 4);
-            }
-            if (g.acc_out) {
-                float* out = g.acc_out + blockIdx.y * g.split_stride + row * g.ldf + col;
-#pragma unroll
-                for (int a = 0; a < 4; ++a) *reinterpret_cast<f32x4*>(out + a * 4) = v[a];
-                continue;
-            }
-            const int64_t at = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo + col;
+            const int64_t at = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo;
             if constexpr (F32) {
                 float* out = static_cast<float*>(g.out) + at;
-                if (g.aligned && col + 16 <= g.ldo) {
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) *reinterpret_cast<f32x4*>(out + a * 4) = v[a];
-                } else {
+                for (int a = 0; a < TA; ++a) {
+                    const int64_t col = a_wave + a * 16 + lg * 4;
+                    if (g.aligned && col + 4 <= g.ldo) {
+                        *reinterpret_cast<f32x4*>(out + col) = acc[a][b];
+                    } else {
 #pragma unroll
-                    for (int a = 0; a < 16; ++a)
-                        if (col + a < g.ldo) out[a] = v[a / 4][a % 4];
+                        for (int k = 0; k < 4; ++k)
+                            if (col + k < g.ldo) out[col + k] = acc[a][b][k];
+                    }
                 }
             } else {
                 uint16_t* out = static_cast<uint16_t*>(g.out) + at;
-                if (g.aligned && col + 16 <= g.ldo) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<u32x4*>(out + h * 8) =
-                            u32x4{bf16_pair(v[2 * h][0], v[2 * h][1]),
-                                  bf16_pair(v[2 * h][2], v[2 * h][3]),
-                                  bf16_pair(v[2 * h + 1][0], v[2 * h + 1][1]),
-                                  bf16_pair(v[2 * h + 1][2], v[2 * h + 1][3])};
-                } else {
+                for (int a = 0; a < TA; a += 2) {
+                    const u32x4 v = pair_of(acc[a][b], acc[a + 1][b]);
+                    const int64_t col = a_wave + a * 16 + pair_column(lg);
+                    if (g.aligned && col + 8 <= g.ldo) {
+                        *reinterpret_cast<u32x4*>(out + col) = v;
+                    } else {
 #pragma unroll
-                    for (int a = 0; a < 16; ++a)
-                        if (col + a < g.ldo) out[a] = bf16_bits(v[a / 4][a % 4]);
+                        for (int k = 0; k < 8; ++k)
+                            if (col + k < g.ldo)
+                                out[col + k] = uint16_t(v[k / 2] >> (16 * (k % 2)));
+                    }
                 }
             }
         }
@@ -793,59 +843,173 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     }
 }
 
-// A gradient's split sums joined, in order.
+// A gradient's split sums joined, in order: four columns a thread, `parts`
+// workgroups a row. Nothing to do where the product's sums were not split.
 struct SplitArgs {
-    const float* part;
-    uint32_t nsplit;
-    int64_t split_stride, ldf;
-    const float* acc_in;
-    float* acc_out;
-    void* out;
-    int64_t ldo;
-    const int32_t* rows;
-    const int32_t* count;
-    int64_t first, nrow;
-    int32_t tokens;
+    GemmArgs g;
+    uint32_t ba, bb, segs, parts;
 };
 
 template <bool F32>
 __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
-    const int64_t row = blockIdx.x;
-    if (a.tokens && row >= *a.count - a.first) return;
-    const int64_t o = (a.rows ? int64_t(a.rows[row]) : row) * a.ldo;
-    for (int64_t c = threadIdx.x; c < a.ldo; c += 256) {
-        float v = a.acc_in ? a.acc_in[row * a.ldf + c] : 0.0f;
-        for (uint32_t s = 0; s < a.nsplit; ++s) v += a.part[s * a.split_stride + row * a.ldf + c];
-        if (a.acc_out) a.acc_out[row * a.ldf + c] = v;
-        else if constexpr (F32) static_cast<float*>(a.out)[o + c] = v;
-        else static_cast<uint16_t*>(a.out)[o + c] = bf16_bits(v);
+    const GemmArgs& g = a.g;
+    int32_t nb = int32_t(g.nb), klen = int32_t(g.k);
+    const int32_t tokens = max(*g.count - int32_t(g.first), 0);
+    if (g.tokens_in_b) nb = min(nb, tokens);
+    if (g.tokens_in_k) klen = min(klen, tokens);
+    const uint32_t tiles = (uint32_t(g.na) + a.ba - 1) / a.ba * ((uint32_t(nb) + a.bb - 1) / a.bb);
+    const uint32_t ns =
+        split_of(tiles, uint32_t(klen + kHeadDepth - 1) / kHeadDepth, a.segs, g.slot_bits);
+    const int64_t row = blockIdx.x / a.parts;
+    const int64_t col = ((blockIdx.x - row * a.parts) * 256 + threadIdx.x) * 4;
+    if (ns == 1 || row >= nb || col >= g.ldo) return;
+    const int64_t at = row * g.ldf + col;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (g.acc_in) v = *reinterpret_cast<const f32x4*>(g.acc_in + at);
+#pragma unroll 8
+    for (uint32_t s = 0; s < ns; ++s)
+        v += *reinterpret_cast<const f32x4*>(g.split + s * (int64_t(nb) * g.ldf) + at);
+    if (g.acc_out) {
+        *reinterpret_cast<f32x4*>(g.acc_out + at) = v;
+        return;
+    }
+    const int64_t o = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo + col;
+    if constexpr (F32) {
+        float* out = static_cast<float*>(g.out) + o;
+        if (g.aligned && col + 4 <= g.ldo) {
+            *reinterpret_cast<f32x4*>(out) = v;
+        } else {
+            for (int k = 0; k < 4; ++k)
+                if (col + k < g.ldo) out[k] = v[k];
+        }
+    } else {
+        uint16_t* out = static_cast<uint16_t*>(g.out) + o;
+        if (g.aligned && col + 4 <= g.ldo) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+        } else {
+            for (int k = 0; k < 4; ++k)
+                if (col + k < g.ldo) out[k] = bf16_bits(v[k]);
+        }
     }
 }
 
 // ---- launches ------------------------------------------------------------------------
 
-template <int BA, int BB, int WA, int WB, bool AM, bool BM, bool F32, int KIND>
-hipError_t run_gemm(const GemmArgs& g, hipStream_t stream) {
-    const int64_t tiles = (g.na + BA - 1) / BA * ((g.nb + BB - 1) / BB);
-    if (tiles == 0) return hipSuccess;
-    gemm_kernel<BA, BB, WA, WB, AM, BM, F32, KIND>
-        <<<dim3(uint32_t((tiles + 7) / 8 * 8), uint32_t(g.nsplit)), 64 * WA * WB, 0, stream>>>(g);
-    return hipGetLastError();
+// A product's tiles: columns and rows of a tile, and how many the card runs
+// at once (log2).
+struct TileShape {
+    uint32_t ba, bb, slot_bits;
+};
+constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8};
+
+// Largest number of items (tiles times parts) and of partial rows times parts
+// over every number of tokens up to the call's.
+struct Bound {
+    uint64_t items = 0, split_rows = 0;
+};
+Bound bound_of(const GemmArgs& g, TileShape t, uint32_t segs) {
+    Bound m;
+    const uint32_t ta = uint32_t((g.na + t.ba - 1) / t.ba), tb = uint32_t((g.nb + t.bb - 1) / t.bb);
+    const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
+    auto one = [&](uint32_t b, uint32_t k) {
+        const uint32_t s = split_of(ta * b, k, segs, g.slot_bits ? t.slot_bits : 0);
+        m.items = std::max<uint64_t>(m.items, uint64_t(ta) * b * s);
+        if (s > 1)
+            m.split_rows = std::max<uint64_t>(m.split_rows,
+                                              s * std::min<uint64_t>(uint64_t(b) * t.bb, g.nb));
+    };
+    // a split needs turns: past 64 of them there is none
+    if (g.tokens_in_b)
+        for (uint32_t b = tb; b > 0; --b) {
+            one(b, kt);
+            if (!g.slot_bits) break;
+        }
+    else if (g.tokens_in_k)
+        for (uint32_t k = 0; k <= kt; ++k) one(tb, k);
+    else
+        one(tb, kt);
+    return m;
+}
+
+template <int BA, int BB, int WA, int WB, int NST, bool AM, bool BM, bool F32, int KIND>
+hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
+    static_assert(BA <= kHeadTile && BB <= kHeadTile, "");
+    if (g.slot_bits) g.slot_bits = t.slot_bits;
+    const Bound m = bound_of(g, t, F32 ? 6 : 1);
+    if (m.items == 0) return hipSuccess;
+    gemm_kernel<BA, BB, WA, WB, NST, AM, BM, F32, KIND>
+        <<<uint32_t((m.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
+    hipError_t e = hipGetLastError();
+    if constexpr (KIND == kOut) {
+        if (e == hipSuccess && m.split_rows) {
+            SplitArgs q{g, t.ba, t.bb, F32 ? 6u : 1u, uint32_t((g.ldo + 1023) / 1024)};
+            split_kernel<F32><<<uint32_t(g.nb * q.parts), 256, 0, stream>>>(q);
+            e = hipGetLastError();
+        }
+    }
+    return e;
 }
 
 // Tiles of 256 x 256 (eight waves, one workgroup on a CU) reach 1.3 PFLOP/s
 // on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
-// 1.05: the smaller are taken where the larger leave more of the card idle.
+// 1.05: the smaller are taken where the larger leave more of the card idle,
+// and tiles of 128 x 64 with more stages on their way for few tokens, where
+// reading the head is what takes the time.
+TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
+    if (low && g.tokens_in_b && g.nb <= 64) return kLow;
+    auto cost = [&](TileShape t, uint64_t stage) {
+        const uint32_t tiles = uint32_t((g.na + t.ba - 1) / t.ba) * uint32_t((g.nb + t.bb - 1) / t.bb);
+        const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
+        const uint32_t s = split_of(tiles, kt, segs, g.slot_bits ? t.slot_bits : 0);
+        const uint64_t turns = ((uint64_t(tiles) * s - 1) >> t.slot_bits) + 1;
+        return turns * ((kt + s - 1) / s * segs + 4) * stage;
+    };
+    // a turn's stage: 65536 outputs on a CU at 130, or 2 x 16384 at 105
+    return cost(kBig, 2 * 105) <= cost(kMid, 130) ? kBig : kMid;
+}
+
 template <bool AM, bool BM, bool F32, int KIND>
 hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
-    auto turns = [&](int64_t tile, int64_t at_once) {
-        const int64_t t = (g.na + tile - 1) / tile * ((g.nb + tile - 1) / tile) * g.nsplit;
-        return (t + at_once - 1) / at_once;
-    };
-    // a turn is 65536 outputs on a CU at 130, or 32768 at 105
-    if (turns(256, 256) * 2 * 105 <= turns(128, 512) * 130)
-        return run_gemm<256, 256, 4, 2, AM, BM, F32, KIND>(g, stream);
-    return run_gemm<128, 128, 2, 2, AM, BM, F32, KIND>(g, stream);
+    const TileShape t = tile_of(g, F32 ? 6 : 1, !BM);
+    if (t.ba == kBig.ba)
+        return run_gemm<256, 256, 4, 2, 2, AM, BM, F32, KIND>(g, t, stream);
+    if constexpr (!BM)
+        if (t.bb == kLow.bb) return run_gemm<128, 64, 2, 2, 6, AM, BM, F32, KIND>(g, t, stream);
+    return run_gemm<128, 128, 2, 2, 2, AM, BM, F32, KIND>(g, t, stream);
+}
+
+// The gradients' products, without their addresses: what the workspace's
+// size is asked of.
+GemmArgs hidden_product(const HeadShape& s, int64_t len) {
+    GemmArgs h{};
+    h.lda = s.dp;
+    h.ldb = s.vp;
+    h.plane_a = s.v * s.dp;
+    h.plane_b = s.chunk * s.vp;
+    h.na = s.dp;
+    h.nb = len;
+    h.k = s.v;
+    h.k_real = s.v;
+    h.tokens_in_b = 1;
+    h.slot_bits = 1;
+    h.ldo = s.d;
+    h.ldf = s.dp;
+    return h;
+}
+GemmArgs head_product(const HeadShape& s, int64_t len) {
+    GemmArgs h{};
+    h.lda = s.dp;
+    h.ldb = s.vp;
+    h.plane_a = s.rows * s.dp;
+    h.plane_b = s.chunk * s.vp;
+    h.na = s.dp;
+    h.nb = s.v;
+    h.k = len;
+    h.tokens_in_k = 1;
+    h.slot_bits = 1;
+    h.ldo = s.d;
+    h.ldf = s.dp;
+    return h;
 }
 
 template <bool F32>
@@ -872,18 +1036,20 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
                                                 count);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t x_plane = s.rows * s.dp, w_plane = s.v * s.dp;
+    const int pack_threads = s.dp >= 2048 ? 256 : 64;
+    const int32_t pack_parts = int32_t((s.dp / 8 + pack_threads - 1) / pack_threads);
     if (s.rows > 0) {
         PackArgs p{c.hidden, c.index, c.logit, c.token_weight, flag, rows, count, coef, entry, x,
                    c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d, s.dp, x_plane, s.top, s.top_pad,
-                   c.scale};
-        pack_kernel<T><<<uint32_t(s.rows), 256, 0, stream>>>(p);
+                   pack_parts, c.scale};
+        pack_kernel<T><<<uint32_t(s.rows * pack_parts), pack_threads, 0, stream>>>(p);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const uint16_t* w = static_cast<const uint16_t*>(c.head);
     if (s.pack_head) {
         uint16_t* packed = reinterpret_cast<uint16_t*>(ws + s.o_w);
-        pack_head_kernel<T><<<uint32_t(s.v), 256, 0, stream>>>(static_cast<const T*>(c.head),
-                                                               packed, s.d, s.dp, w_plane);
+        pack_head_kernel<T><<<uint32_t(s.v * pack_parts), pack_threads, 0, stream>>>(
+            static_cast<const T*>(c.head), packed, s.d, s.dp, w_plane, pack_parts);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         w = packed;
     }
@@ -911,7 +1077,6 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.count = count;
         l.first = first;
         l.tokens_in_b = 1;
-        l.nsplit = 1;
         l.inv_temp = 1.0f / c.temperature;
         l.part = part;
         l.nblk = s.vp / kHeadBlock;
@@ -933,78 +1098,53 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         }
 
         if (s.grad_hidden && len > 0) {
-            GemmArgs h{};
+            GemmArgs h = hidden_product(s, len);
             h.a = w;
             h.b = gp;
-            h.lda = s.dp;
-            h.ldb = s.vp;
-            h.plane_a = w_plane;
-            h.plane_b = g_plane;
-            h.na = s.dp;
-            h.nb = len;
-            h.k = s.v;
-            h.k_real = s.v;
             h.count = count;
             h.first = first;
-            h.tokens_in_b = 1;
-            h.nsplit = s.split_hidden;
             h.out = c.grad_hidden;
-            h.ldo = s.d;
             h.rows = rows + first;
             h.aligned = aligned(c.grad_hidden, s.d, sizeof(T));
-            h.ldf = s.dp;
-            h.split_stride = s.chunk * s.dp;
-            if (h.nsplit > 1) h.acc_out = split;
+            h.split = split;
             if ((e = pick_gemm<true, false, F32, kOut>(h, stream)) != hipSuccess) return e;
-            if (h.nsplit > 1) {
-                SplitArgs q{split, h.nsplit, h.split_stride, s.dp, nullptr, nullptr, h.out, s.d,
-                            h.rows, count, first, len, 1};
-                split_kernel<F32><<<uint32_t(len), 256, 0, stream>>>(q);
-                if ((e = hipGetLastError()) != hipSuccess) return e;
-            }
         }
         if (s.grad_head) {
-            GemmArgs h{};
+            GemmArgs h = head_product(s, len);
             h.a = x + first * s.dp;
             h.b = gp;
-            h.lda = s.dp;
-            h.ldb = s.vp;
-            h.plane_a = x_plane;
-            h.plane_b = g_plane;
-            h.na = s.dp;
-            h.nb = s.v;
-            h.k = len;
             h.k_real = s.rows - first;
             h.count = count;
             h.first = first;
-            h.tokens_in_k = 1;
-            h.nsplit = s.split_head;
             h.out = c.grad_head;
-            h.ldo = s.d;
             h.aligned = aligned(c.grad_head, s.d, sizeof(T));
-            h.ldf = s.dp;
-            h.split_stride = s.v * s.dp;
-            const float* acc_in = ch > 0 ? acc : nullptr;
-            float* acc_out = ch + 1 < s.nchunk ? acc : nullptr;
-            if (h.nsplit > 1) {
-                h.acc_out = split;
-            } else {
-                h.acc_in = acc_in;
-                h.acc_out = acc_out;
-            }
+            h.split = split;
+            h.acc_in = ch > 0 ? acc : nullptr;
+            h.acc_out = ch + 1 < s.nchunk ? acc : nullptr;
             if ((e = pick_gemm<true, true, F32, kOut>(h, stream)) != hipSuccess) return e;
-            if (h.nsplit > 1) {
-                SplitArgs q{split, h.nsplit, h.split_stride, s.dp, acc_in, acc_out, h.out, s.d,
-                            nullptr, count, first, s.v, 0};
-                split_kernel<F32><<<uint32_t(s.v), 256, 0, stream>>>(q);
-                if ((e = hipGetLastError()) != hipSuccess) return e;
-            }
         }
     }
     return hipSuccess;
 }
 
 }  // namespace
+
+int64_t head_split_bytes(const HeadShape& s) {
+    const uint32_t segs = s.f32 ? 6 : 1;
+    uint64_t rows = 0;
+    for (int64_t ch = 0; ch < s.nchunk; ++ch) {
+        const int64_t len = std::min(s.chunk, s.n - ch * s.chunk);
+        if (s.grad_hidden && len > 0) {
+            const GemmArgs h = hidden_product(s, len);
+            rows = std::max(rows, bound_of(h, tile_of(h, segs, true), segs).split_rows);
+        }
+        if (s.grad_head) {
+            const GemmArgs h = head_product(s, len);
+            rows = std::max(rows, bound_of(h, tile_of(h, segs, false), segs).split_rows);
+        }
+    }
+    return int64_t(rows) * s.dp * 4;
+}
 
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     return s.f32 ? run_head<true>(s, c, stream) : run_head<false>(s, c, stream);

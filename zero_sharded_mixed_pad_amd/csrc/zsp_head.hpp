@@ -30,7 +30,6 @@ struct HeadShape {
     int64_t vp = 0, dp = 0;       // v padded to kHeadTile, d to kHeadDepth
     int64_t chunk = 0;            // tokens whose softmax is kept at a time
     int64_t nchunk = 0;
-    int32_t split_hidden = 1, split_head = 1;  // parts of the gradients' long sums
     // offsets
     int64_t o_count = 0, o_rows = 0, o_coef = 0, o_entry = 0, o_pick = 0, o_flag = 0, o_x = 0,
             o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
@@ -51,6 +50,8 @@ struct HeadCall {
     char* ws;
 };
 
+// Bytes for the parts of the gradients' sums, if those are split.
+int64_t head_split_bytes(const HeadShape& s);
 // Every launch of a call, in order, on `stream`.
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream);
 

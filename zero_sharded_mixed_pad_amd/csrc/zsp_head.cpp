@@ -60,7 +60,11 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.o_coef = take(s.rows * 4);
     s.o_entry = take(s.rows * s.top_pad * 4);
     s.o_pick = take(s.rows * s.top_pad * 4);
-    if (s.teacher) s.o_flag = take(n);
+    if (s.teacher) {
+        s.o_flag = take(n);
+        s.o_teach = take(s.rows * s.top_pad * 4);
+        if (s.top > 1) s.o_start = take(n * ((v + kHeadBlock - 1) / kHeadBlock + 1) * 2);
+    }
     s.o_x = take(s.rows * s.dp * 2 * s.planes);
     if (s.pack_head) s.o_w = take(v * s.dp * 2 * s.planes);
     s.o_part = take(s.chunk * (s.vp / kHeadBlock) * 8);

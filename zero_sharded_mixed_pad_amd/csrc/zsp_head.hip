@@ -98,7 +98,8 @@ __device__ __forceinline__ bool counts(const int64_t* target, const float* weigh
                                        const uint8_t* flag, int64_t i, int64_t v) {
     if (flag) return flag[i] != 0;
     const int64_t e = target[i];
-    return e >= 0 && e < v && (!weight || weight[i] != 0.0f);
+    const float w = weight ? weight[i] : 1.0f;
+    return uint64_t(e) < uint64_t(v) && w != 0.0f;
 }
 
 // rows[0 .. count): the tokens that count, in order. One workgroup, 16 tokens
@@ -114,12 +115,31 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* targe
     int32_t done = 0;
     for (int64_t base = 0; base < n; base += kScanThreads * kScanRun) {
         const int64_t first = base + wave * (64 * kScanRun) + lane;
+        // all loads on their way before the first is looked at
         bool on[kScanRun];
+        const int64_t last = n - 1;
+        if (flag) {
+            uint8_t f[kScanRun];
 #pragma unroll
-        for (int k = 0; k < kScanRun; ++k) {
-            const int64_t i = first + k * 64;
-            on[k] = i < n && counts(target, weight, flag, i, v);
+            for (int k = 0; k < kScanRun; ++k) f[k] = flag[min(first + k * 64, last)];
+#pragma unroll
+            for (int k = 0; k < kScanRun; ++k) on[k] = f[k] != 0;
+        } else {
+            int64_t e[kScanRun];
+#pragma unroll
+            for (int k = 0; k < kScanRun; ++k) e[k] = target[min(first + k * 64, last)];
+#pragma unroll
+            for (int k = 0; k < kScanRun; ++k) on[k] = uint64_t(e[k]) < uint64_t(v);
+            if (weight) {
+                float w[kScanRun];
+#pragma unroll
+                for (int k = 0; k < kScanRun; ++k) w[k] = weight[min(first + k * 64, last)];
+#pragma unroll
+                for (int k = 0; k < kScanRun; ++k) on[k] &= w[k] != 0.0f;
+            }
         }
+#pragma unroll
+        for (int k = 0; k < kScanRun; ++k) on[k] &= first + k * 64 < n;
         int32_t mine = 0;
 #pragma unroll
         for (int k = 0; k < kScanRun; ++k) mine += __popcll(__ballot(on[k]));
@@ -151,12 +171,13 @@ struct PackArgs {
     const int32_t* count;
     float* coef;
     int32_t* entry;
+    float* teach;
     uint16_t* x;
     void* grad_hidden;
     float* loss;
     float* lse;
     int64_t n, v, d, dp, plane;
-    int32_t top, top_pad, parts;
+    int32_t top, parts;
     float scale;
 };
 
@@ -214,10 +235,11 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
         if (c < a.dp)
             put8(a.x + r * a.dp, a.plane, static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
         if (part == 0) {
-            for (int32_t k = t; k < a.top_pad; k += threads) {
-                int64_t e = k < a.top ? a.index[i * a.top + k] : -1;
-                if (a.logit && k < a.top && a.logit[i * a.top + k] == -__builtin_inff()) e = -1;
-                a.entry[r * a.top_pad + k] = e >= 0 && e < a.v ? int32_t(e) : -1;
+            if (t == 0 && a.top == 1) {
+                const int64_t e = a.index[i];
+                const bool out = a.logit && a.logit[i] == -__builtin_inff();
+                a.entry[r] = uint64_t(e) < uint64_t(a.v) && !out ? int32_t(e) : -1;
+                if (a.logit) a.teach[r] = a.logit[i];
             }
             if (t == 0) a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
         }
@@ -234,6 +256,51 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
             a.loss[r] = 0.0f;
             if (a.lse) a.lse[r] = 0.0f;
         }
+    }
+}
+
+// A token's entries in the order of their blocks of the vocabulary (equal ones
+// in the teacher's), with their logits, and where each block's begin: a tile of
+// the logits then looks at its own entries alone. Scanning all 64 entries of
+// every token in every tile took 450 of 1330 us at 4096 x 32000 x 4096.
+struct EntryArgs {
+    const int64_t* index;
+    const float* logit;
+    const int32_t* rows;
+    const int32_t* count;
+    int32_t* entry;
+    float* teach;
+    uint16_t* start;   // [row][blocks + 1]
+    int64_t v;
+    int32_t top, top_pad, blocks;
+};
+
+__global__ __launch_bounds__(256) void entry_kernel(EntryArgs a) {
+    __shared__ int32_t s_block[kHeadMaxTop], s_sorted[kHeadMaxTop];
+    const int64_t r = blockIdx.x;
+    const int t = threadIdx.x;
+    if (r >= *a.count) return;
+    const int64_t from = int64_t(a.rows[r]) * a.top;
+    for (int32_t k = t; k < a.top; k += 256) {
+        const int64_t e = a.index[from + k];
+        const bool on = uint64_t(e) < uint64_t(a.v) && a.logit[from + k] != -__builtin_inff();
+        s_block[k] = on ? int32_t(e) / kHeadBlock : a.blocks;
+    }
+    __syncthreads();
+    for (int32_t k = t; k < a.top; k += 256) {
+        const int32_t b = s_block[k];
+        int32_t at = 0;
+        for (int32_t o = 0; o < a.top; ++o) at += s_block[o] < b || (s_block[o] == b && o < k);
+        s_sorted[at] = b;
+        a.entry[r * a.top_pad + at] = b < a.blocks ? int32_t(a.index[from + k]) : -1;
+        a.teach[r * a.top_pad + at] = a.logit[from + k];
+    }
+    __syncthreads();
+    uint16_t* start = a.start + r * (a.blocks + 1);
+    for (int32_t k = t; k <= a.top; k += 256) {
+        const int32_t lo = k == 0 ? 0 : s_sorted[k - 1] + 1;
+        const int32_t hi = k == a.top ? a.blocks : s_sorted[k];
+        for (int32_t b = lo; b <= hi; ++b) start[b] = uint16_t(k);
     }
 }
 
@@ -271,6 +338,8 @@ struct GemmArgs {
     void* p;                   // [b][ldp] bf16 or fp32, or NULL
     int64_t ldp;
     const int32_t* entry;      // [b][top_pad]
+    const uint16_t* start;     // [b][blocks + 1]: a block's first entry, if top_pad > 1
+    int32_t blocks;
     float* pick;
     int32_t top_pad;
     // outputs
@@ -481,6 +550,12 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 
     const uint32_t kt0 = kt_all * part / ns, kt1 = kt_all * (part + 1) / ns;  // below 2^23
     const int nkt = int(kt1 - kt0), steps = nkt * kSegs;
+    // Few tokens: the head's rows are read from HBM at the pace of the k's, and
+    // columns of the same k of all rows lie in a few of its channels: every
+    // tile starts at another k (262 MB at 4.3 -> 5.5 TB/s). Larger tiles share
+    // rows through the L2 and keep in step (835 us; 850 to 910 out of step).
+    constexpr bool kTurn = KIND == kLogits && NST > 2;
+    const int k_turn = kTurn && nkt > 0 ? int(in_b * 3 % nkt) : 0;
 
     OpA oa;
     OpB ob;
@@ -490,7 +565,9 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     int i_kt = 0, i_seg = 0, i_left = steps;  // the next stage to load
     auto issue = [&](int buf, int from, int to) {
         ZSP_LDS char* lds = (ZSP_LDS char*)s_mem + buf * kStage;
-        const int64_t k0 = int64_t(kt0 + i_kt) * BK;
+        int kt = i_kt;
+        if constexpr (kTurn) kt = kt + k_turn < nkt ? kt + k_turn : kt + k_turn - nkt;
+        const int64_t k0 = int64_t(int(kt0) + kt) * BK;
 #pragma unroll
         for (int i = from; i < to; ++i) {
             if (i < OpA::kLoads)
@@ -536,7 +613,21 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
         }
     };
     using std::integral_constant;
-    if (steps > 0) {
+    if constexpr (NST == 1) {
+        // Short sums, where writing the output is what takes the time: several
+        // workgroups a CU hide each other's loads and stores.
+        for (int it = 0; it < steps; ++it) {
+            if (it > 0) wg_barrier();
+            issue(0, 0, kPer);
+            wait_stage<0>();
+            wg_barrier();
+#pragma unroll
+            for (int i = 0; i < TA + TB; ++i) read(0, 0, i);
+            work(integral_constant<int, 0>(), 0, integral_constant<bool, false>(), 0);
+            work(integral_constant<int, 1>(), 0, integral_constant<bool, false>(), 0);
+            wait_stage<0>();
+        }
+    } else if (steps > 0) {
 #pragma unroll
         for (int i = 0; i < NST; ++i) issue(i, 0, kPer);
         wait_stage<(NST - 1) * kPer>();
@@ -544,12 +635,12 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 #pragma unroll
         for (int i = 0; i < TA + TB; ++i) read(0, 0, i);
     }
-    for (int it = 0; it < steps; ++it) {
+    for (int it = 0; NST > 1 && it < steps; ++it) {
         __builtin_amdgcn_sched_barrier(0);
         work(integral_constant<int, 0>(), buf, integral_constant<bool, false>(), 0);
         // this wave has read all of this stage, and its part of the next has
         // landed; then that holds for every wave
-        wait_stage<(NST - 2) * kPer>();
+        wait_stage<(NST > 2 ? NST - 2 : 0) * kPer>();
         wg_barrier();
         const int old = buf;
         buf = NST == 2 ? buf ^ 1 : buf + 1 == NST ? 0 : buf + 1;
@@ -563,6 +654,28 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     const int lr = lane % 16, lg = lane / 16;
     const int64_t a_wave = a0 + wa * EA;
     if constexpr (KIND == kLogits) {
+        // the first entry of each of this lane's tokens in this block, all
+        // loads at once
+        int32_t one[TB], e_from[TB], e_to[TB];
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+            const int64_t row = b0 + wb * EB + b * 16 + lr;
+            one[b] = -1;
+            e_from[b] = e_to[b] = 0;
+            if (row < nb && g.top_pad == 1) one[b] = g.entry[row];
+            if (row < nb && g.top_pad > 1 && a_wave < g.na) {
+                const uint16_t* s = g.start + row * (g.blocks + 1) + a_wave / kHeadBlock;
+                e_from[b] = s[0];
+                e_to[b] = s[1];
+            }
+        }
+        if (g.top_pad > 1) {
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                const int64_t row = b0 + wb * EB + b * 16 + lr;
+                if (e_from[b] < e_to[b]) one[b] = g.entry[row * g.top_pad + e_from[b]];
+            }
+        }
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
             const int64_t row = b0 + wb * EB + b * 16 + lr;
@@ -579,19 +692,22 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
             const bool real = row < nb;
-            if (real) {
-                const int32_t* e = g.entry + row * g.top_pad;
-                for (int32_t k = 0; k < g.top_pad; ++k) {
-                    const int64_t rel = e[k] - a_wave;
-                    if (e[k] < 0 || uint64_t(rel) >= uint64_t(EA) || ((rel >> 2) & 3) != lg) continue;
-                    float l = 0.0f;
+            auto take = [&](int32_t k, int32_t e) {
+                const int rel = int(e - a_wave);
+                if (unsigned(rel) >= unsigned(EA) || ((rel >> 2) & 3) != lg) return;
+                float l = 0.0f;
 #pragma unroll
-                    for (int a = 0; a < TA; ++a)
+                for (int a = 0; a < TA; ++a)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if ((rel >> 4) == a && (rel & 3) == c) l = acc[a][b][c];
-                    g.pick[row * g.top_pad + k] = l;
-                }
+                    for (int c = 0; c < 4; ++c)
+                        if ((rel >> 4) == a && (rel & 3) == c) l = acc[a][b][c];
+                g.pick[row * g.top_pad + k] = l;
+            };
+            if (real && g.top_pad == 1) take(0, one[b]);
+            if (g.top_pad > 1 && e_from[b] < e_to[b]) {
+                take(e_from[b], one[b]);
+                for (int32_t k = e_from[b] + 1; k < e_to[b]; ++k)
+                    take(k, g.entry[row * g.top_pad + k]);
             }
             // a block without a column of the vocabulary leaves 0
             const float mm = m == -__builtin_inff() ? 0.0f : m;
@@ -685,7 +801,7 @@ struct JoinArgs {
     const float* coef;
     const int32_t* entry;
     const float* pick;
-    const float* logit;       // the teacher's [n, top], or NULL
+    const float* teach;       // the teacher's logits in the entries' order, or NULL
     int32_t top, top_pad;
     float temp, inv_temp;
     float* loss;
@@ -693,6 +809,7 @@ struct JoinArgs {
     void* p;                  // [chunk][ldp], or NULL: no gradients
     uint16_t* g;              // fp32: the planes of G; else P itself
     int64_t ldp, plane;
+    int32_t parts;            // workgroups a token
 };
 
 __device__ __forceinline__ double block_sum(double v, double* s) {
@@ -724,8 +841,8 @@ __device__ __forceinline__ void put_g(const JoinArgs& a, int64_t row, int64_t co
     }
 }
 
-// One workgroup per token that counts: lse, the loss, then the token's row of
-// G. An entry's own G is taken from its logit in 64 bits: c (p - q) from P's
+// A workgroup (several, where tokens are few) per token that counts: lse, the
+// loss, then the token's row of G. An entry's own G is taken from its logit in 64 bits: c (p - q) from P's
 // bf16 would lose all of 1 - p where the model is sure of its target.
 template <bool F32>
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
@@ -733,14 +850,17 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     __shared__ float s_f[4];
     __shared__ float s_q[kHeadMaxTop];
     __shared__ int32_t s_e[kHeadMaxTop];
-    const int64_t r = blockIdx.x, count = *a.count - a.first;
-    const int64_t cols = int64_t(a.blocks) * kHeadBlock;
+    const int64_t r = blockIdx.x / a.parts, count = *a.count - a.first;
+    const int32_t part_no = int32_t(blockIdx.x - r * a.parts);
     const int t = threadIdx.x;
+    // this workgroup's columns
+    const int64_t from = int64_t(a.blocks) * part_no / a.parts * kHeadBlock;
+    const int64_t to = int64_t(a.blocks) * (part_no + 1) / a.parts * kHeadBlock;
     if (r >= count) {
         // zeros behind the last token, as far as a stage of the sum over
         // tokens may read
         if (a.p && r < (count + kHeadDepth - 1) / kHeadDepth * kHeadDepth)
-            for (int64_t c = t * 8; c < cols; c += 2048)
+            for (int64_t c = from + t * 8; c < to; c += 2048)
                 for (int k = 0; k < (F32 ? 3 : 1); ++k)
                     *reinterpret_cast<u32x4*>(a.g + k * a.plane + r * a.ldp + c) = u32x4{0, 0, 0, 0};
         return;
@@ -762,8 +882,8 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     const int32_t* entry = a.entry + r * a.top_pad;
     const float* pick = a.pick + r * a.top_pad;
     double loss = 0.0;
-    if (a.logit) {
-        const float* teach = a.logit + token * a.top;
+    if (a.teach) {
+        const float* teach = a.teach + r * a.top_pad;
         float tm = -__builtin_inff();
         for (int32_t k = t; k < a.top; k += 256)
             if (entry[k] >= 0) tm = nan_max(tm, teach[k]);
@@ -792,7 +912,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         }
         __syncthreads();
     }
-    if (t == 0) {
+    if (t == 0 && part_no == 0) {
         a.loss[token] = float(loss);
         if (a.lse) a.lse[token] = float(lse);
     }
@@ -802,7 +922,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     const float l32 = float(lse);
     if constexpr (F32) {
         const float* p = static_cast<const float*>(a.p) + r * a.ldp;
-        for (int64_t i = t * 4; i < cols; i += 1024) {
+        for (int64_t i = from + t * 4; i < to; i += 1024) {
             const float f = c * fast_exp(part[i / kHeadBlock].x - l32);
             const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
             uint16_t h[4][3];
@@ -818,7 +938,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         }
     } else {
         uint16_t* p = a.g + r * a.ldp;
-        for (int64_t i = t * 8; i < cols; i += 2048) {
+        for (int64_t i = from + t * 8; i < to; i += 2048) {
             const float f = c * fast_exp(part[i / kHeadBlock].x - l32);
             u32x4 v = *reinterpret_cast<const u32x4*>(p + i);
 #pragma unroll
@@ -833,7 +953,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     // equal entries of a row write the same sum of their q
     for (int32_t k = t; k < a.top; k += 256) {
         const int32_t e = s_e[k];
-        if (e < 0) continue;
+        if (e < from || e >= to) continue;
         double q = 0.0;
         for (int32_t o = 0; o < a.top; ++o)
             if (s_e[o] == e) q += double(s_q[o]);
@@ -851,18 +971,11 @@ struct SplitArgs {
 };
 
 template <bool F32>
-__global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
+__device__ __forceinline__ void join_split(const SplitArgs& a, int32_t nb, uint32_t ns, int64_t i) {
     const GemmArgs& g = a.g;
-    int32_t nb = int32_t(g.nb), klen = int32_t(g.k);
-    const int32_t tokens = max(*g.count - int32_t(g.first), 0);
-    if (g.tokens_in_b) nb = min(nb, tokens);
-    if (g.tokens_in_k) klen = min(klen, tokens);
-    const uint32_t tiles = (uint32_t(g.na) + a.ba - 1) / a.ba * ((uint32_t(nb) + a.bb - 1) / a.bb);
-    const uint32_t ns =
-        split_of(tiles, uint32_t(klen + kHeadDepth - 1) / kHeadDepth, a.segs, g.slot_bits);
-    const int64_t row = blockIdx.x / a.parts;
-    const int64_t col = ((blockIdx.x - row * a.parts) * 256 + threadIdx.x) * 4;
-    if (ns == 1 || row >= nb || col >= g.ldo) return;
+    const int64_t row = i / a.parts;
+    const int64_t col = ((i - row * a.parts) * 256 + threadIdx.x) * 4;
+    if (col >= g.ldo) return;
     const int64_t at = row * g.ldf + col;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (g.acc_in) v = *reinterpret_cast<const f32x4*>(g.acc_in + at);
@@ -893,6 +1006,20 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
     }
 }
 
+template <bool F32>
+__global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
+    const GemmArgs& g = a.g;
+    int32_t nb = int32_t(g.nb), klen = int32_t(g.k);
+    const int32_t tokens = max(*g.count - int32_t(g.first), 0);
+    if (g.tokens_in_b) nb = min(nb, tokens);
+    if (g.tokens_in_k) klen = min(klen, tokens);
+    const uint32_t tiles = (uint32_t(g.na) + a.ba - 1) / a.ba * ((uint32_t(nb) + a.bb - 1) / a.bb);
+    const uint32_t ns =
+        split_of(tiles, uint32_t(klen + kHeadDepth - 1) / kHeadDepth, a.segs, g.slot_bits);
+    if (ns == 1) return;
+    for (int64_t i = blockIdx.x; i < int64_t(nb) * a.parts; i += gridDim.x) join_split<F32>(a, nb, ns, i);
+}
+
 // ---- launches ------------------------------------------------------------------------
 
 // A product's tiles: columns and rows of a tile, and how many the card runs
@@ -900,7 +1027,7 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 struct TileShape {
     uint32_t ba, bb, slot_bits;
 };
-constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8};
+constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8}, kLow2{128, 128, 8};
 
 // Largest number of items (tiles times parts) and of partial rows times parts
 // over every number of tokens up to the call's.
@@ -943,7 +1070,8 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
     if constexpr (KIND == kOut) {
         if (e == hipSuccess && m.split_rows) {
             SplitArgs q{g, t.ba, t.bb, F32 ? 6u : 1u, uint32_t((g.ldo + 1023) / 1024)};
-            split_kernel<F32><<<uint32_t(g.nb * q.parts), 256, 0, stream>>>(q);
+            const int64_t rows = g.nb * q.parts;
+            split_kernel<F32><<<uint32_t(std::min<int64_t>(rows, 4096)), 256, 0, stream>>>(q);
             e = hipGetLastError();
         }
     }
@@ -952,11 +1080,12 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
 
 // Tiles of 256 x 256 (eight waves, one workgroup on a CU) reach 1.3 PFLOP/s
 // on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
-// 1.05: the smaller are taken where the larger leave more of the card idle,
-// and tiles of 128 x 64 with more stages on their way for few tokens, where
-// reading the head is what takes the time.
+// 1.05: the smaller are taken where the larger leave more of the card idle.
+// For up to 64 and 128 tokens, where reading the head is what takes the time,
+// tiles of 128 x 64 and 128 x 128 with six and four stages on their way.
 TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (low && g.tokens_in_b && g.nb <= 64) return kLow;
+    if (low && g.part && g.nb <= 128) return kLow2;
     auto cost = [&](TileShape t, uint64_t stage) {
         const uint32_t tiles = uint32_t((g.na + t.ba - 1) / t.ba) * uint32_t((g.nb + t.bb - 1) / t.bb);
         const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
@@ -975,6 +1104,9 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
         return run_gemm<256, 256, 4, 2, 2, AM, BM, F32, KIND>(g, t, stream);
     if constexpr (!BM)
         if (t.bb == kLow.bb) return run_gemm<128, 64, 2, 2, 6, AM, BM, F32, KIND>(g, t, stream);
+    if constexpr (KIND == kLogits)
+        if (t.slot_bits == kLow2.slot_bits)
+            return run_gemm<128, 128, 2, 2, 4, AM, BM, F32, KIND>(g, t, stream);
     return run_gemm<128, 128, 2, 2, 2, AM, BM, F32, KIND>(g, t, stream);
 }
 
@@ -1021,6 +1153,9 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     float* coef = reinterpret_cast<float*>(ws + s.o_coef);
     int32_t* entry = reinterpret_cast<int32_t*>(ws + s.o_entry);
     float* pick = reinterpret_cast<float*>(ws + s.o_pick);
+    float* teach = s.teacher ? reinterpret_cast<float*>(ws + s.o_teach) : nullptr;
+    uint16_t* start = s.top > 1 ? reinterpret_cast<uint16_t*>(ws + s.o_start) : nullptr;
+    const int32_t blocks = int32_t((s.v + kHeadBlock - 1) / kHeadBlock);
     uint8_t* flag = s.teacher ? reinterpret_cast<uint8_t*>(ws + s.o_flag) : nullptr;
     uint16_t* x = reinterpret_cast<uint16_t*>(ws + s.o_x);
     float2* part = reinterpret_cast<float2*>(ws + s.o_part);
@@ -1039,10 +1174,15 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     const int pack_threads = s.dp >= 2048 ? 256 : 64;
     const int32_t pack_parts = int32_t((s.dp / 8 + pack_threads - 1) / pack_threads);
     if (s.rows > 0) {
-        PackArgs p{c.hidden, c.index, c.logit, c.token_weight, flag, rows, count, coef, entry, x,
-                   c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d, s.dp, x_plane, s.top, s.top_pad,
-                   pack_parts, c.scale};
+        PackArgs p{c.hidden, c.index, c.logit, c.token_weight, flag, rows, count, coef, entry, teach, x,
+                   c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d, s.dp, x_plane, s.top, pack_parts, c.scale};
         pack_kernel<T><<<uint32_t(s.rows * pack_parts), pack_threads, 0, stream>>>(p);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (start && s.n > 0) {
+        EntryArgs q{c.index, c.logit, rows, count, entry, teach, start, s.v, s.top, s.top_pad,
+                    blocks};
+        entry_kernel<<<uint32_t(s.n), 256, 0, stream>>>(q);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const uint16_t* w = static_cast<const uint16_t*>(c.head);
@@ -1083,17 +1223,22 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.p = p;
         l.ldp = s.vp;
         l.entry = entry + first * s.top_pad;
+        l.start = start ? start + first * (blocks + 1) : nullptr;
+        l.blocks = blocks;
         l.pick = pick + first * s.top_pad;
         l.top_pad = s.top_pad;
         if (len > 0 && (e = pick_gemm<false, false, F32, kLogits>(l, stream)) != hipSuccess)
             return e;
 
         if (len > 0) {
-            JoinArgs j{part, l.nblk, int32_t((s.v + kHeadBlock - 1) / kHeadBlock), count, first, rows + first, coef + first, l.entry, l.pick,
-                       c.logit, s.top, s.top_pad, c.temperature, l.inv_temp, c.loss, c.lse, p, gp,
-                       s.vp, g_plane};
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
-            join_kernel<F32><<<uint32_t(grads ? pad : len), 256, 0, stream>>>(j);
+            // at least 4096 columns each
+            const int64_t most = std::min<int64_t>((blocks + 63) / 64, 1024 / pad);
+            const int32_t parts = grads ? int32_t(std::max<int64_t>(most, 1)) : 1;
+            JoinArgs j{part, l.nblk, blocks, count, first, rows + first, coef + first, l.entry,
+                       l.pick, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
+                       c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, parts};
+            join_kernel<F32><<<uint32_t(grads ? pad * parts : len), 256, 0, stream>>>(j);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
 

@@ -31,8 +31,8 @@ struct HeadShape {
     int64_t chunk = 0;            // tokens whose softmax is kept at a time
     int64_t nchunk = 0;
     // offsets
-    int64_t o_count = 0, o_rows = 0, o_coef = 0, o_entry = 0, o_pick = 0, o_flag = 0, o_x = 0,
-            o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
+    int64_t o_count = 0, o_rows = 0, o_coef = 0, o_entry = 0, o_pick = 0, o_teach = 0, o_start = 0,
+            o_flag = 0, o_x = 0, o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
     int64_t bytes = 0;
 };
 

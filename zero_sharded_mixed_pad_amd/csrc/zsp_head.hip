@@ -105,11 +105,26 @@ __device__ __forceinline__ bool counts(const int64_t* target, const float* weigh
 // rows[0 .. count): the tokens that count, in order. One workgroup, 16 tokens
 // a thread at a time; the waves' counts are joined in LDS.
 constexpr int kScanThreads = 1024, kScanRun = 16;
+constexpr int64_t kFlagEntries = 65536, kFlagTokens = kScanThreads * kScanRun;
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* target,
-                                                            const float* weight,
-                                                            const uint8_t* flag, int64_t n,
-                                                            int64_t v, int32_t* rows,
+                                                            const float* logit, int32_t top,
+                                                            const float* weight, uint8_t* flag,
+                                                            int64_t n, int64_t v, int32_t* rows,
                                                             int32_t* count) {
+    if (logit) {  // a teacher's few entries: the flags first
+        __shared__ uint8_t s_flag[kFlagTokens];
+        for (int64_t i = threadIdx.x; i < n; i += kScanThreads) s_flag[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int32_t k = threadIdx.x; k < int32_t(n) * top; k += kScanThreads)
+            if (uint64_t(target[k]) < uint64_t(v) && logit[k] != -__builtin_inff())
+                s_flag[k / top] = 1;
+        __syncthreads();
+        for (int64_t i = threadIdx.x; i < n; i += kScanThreads)
+            flag[i] = s_flag[i] && (!weight || weight[i] != 0.0f);
+        __threadfence_block();
+        __syncthreads();
+    }
     __shared__ int32_t s_wave[kScanThreads / 64];
     const int t = threadIdx.x, lane = t % 64, wave = t / 64;
     int32_t done = 0;
@@ -161,26 +176,6 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* targe
     if (t == 0) *count = done;
 }
 
-struct PackArgs {
-    const void* hidden;
-    const int64_t* index;
-    const float* logit;
-    const float* weight;
-    const uint8_t* flag;
-    const int32_t* rows;
-    const int32_t* count;
-    float* coef;
-    int32_t* entry;
-    float* teach;
-    uint16_t* x;
-    void* grad_hidden;
-    float* loss;
-    float* lse;
-    int64_t n, v, d, dp, plane;
-    int32_t top, parts;
-    float scale;
-};
-
 // Eight elements of a row of d, from column c on, as planes of dp columns;
 // zeros past d, and everywhere if `in` is NULL.
 template <typename T>
@@ -221,38 +216,118 @@ __device__ __forceinline__ void put8(uint16_t* out, int64_t plane, const T* in, 
     }
 }
 
-// Row r of the copied X, its coefficient and entries; the outputs of token r
-// where it does not count. `parts` workgroups a row, eight columns a thread.
+struct SetupArgs {
+    const void* hidden;
+    const void* head;
+    const int64_t* index;
+    const float* logit;
+    const float* weight;
+    const uint8_t* flag;
+    int32_t* rows;
+    int32_t* count;
+    float* coef;
+    int32_t* entry;
+    float* teach;
+    uint16_t* start;   // [row][blocks + 1]
+    uint16_t* x;
+    uint16_t* w;
+    void* grad_hidden;
+    float* loss;
+    float* lse;
+    int64_t n, v, d, dp, x_plane, w_plane;
+    int32_t top, top_pad, blocks;
+    int32_t row_threads, parts;               // threads a row, workgroups a row
+    uint32_t x_groups, entry_groups;          // workgroups of each kind; the rest copy the head
+    int32_t scans;                            // each workgroup finds the tokens itself
+    float scale;
+};
+
+constexpr int kSetupThreads = 256, kSetupRun = 8;
+constexpr int64_t kSelfScan = kSetupThreads * kSetupRun;
+
+// Up to kSelfScan tokens: those that count, found by every workgroup for
+// itself (a launch and its wait cost more than reading the targets again).
+// Leaves the tokens of rows [r0, r0 + n) in s_rows.
+__device__ __forceinline__ int32_t scan_here(const SetupArgs& a, int64_t r0, int n, int32_t* s_rows,
+                                             int32_t* s_wave) {
+    const int t = threadIdx.x, lane = t % 64, wave = t / 64;
+    const int64_t first = int64_t(t) * kSetupRun;
+    bool on[kSetupRun];
+    int32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < kSetupRun; ++k) {
+        const int64_t i = min(first + k, a.n - 1);
+        on[k] = counts(a.index, a.weight, nullptr, i, a.v) && first + k < a.n;
+        mine += on[k];
+    }
+    int32_t sum = mine;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int32_t u = __shfl_up(sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 63) s_wave[wave] = sum;
+    __syncthreads();
+    int32_t at = sum - mine, all = 0;
+    for (int w = 0; w < kSetupThreads / 64; ++w) {
+        if (w < wave) at += s_wave[w];
+        all += s_wave[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kSetupRun; ++k) {
+        if (!on[k]) continue;
+        if (at >= r0 && at < r0 + n) s_rows[at - r0] = int32_t(first + k);
+        ++at;
+    }
+    __syncthreads();
+    return all;
+}
+
+// Rows of the copied X, their coefficients and entries; the outputs of tokens
+// that do not count. `row_threads` threads and `parts` workgroups a row, eight
+// columns a thread.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
-    const int64_t r = blockIdx.x / a.parts;
-    const int32_t part = int32_t(blockIdx.x - r * a.parts);
-    const int64_t c = (int64_t(part) * blockDim.x + threadIdx.x) * 8;
-    const int t = threadIdx.x, threads = blockDim.x;
-    const int32_t count = *a.count;
+__device__ __forceinline__ void setup_rows(const SetupArgs& a, uint32_t group) {
+    __shared__ int32_t s_rows[kSetupThreads], s_wave[kSetupThreads / 64];
+    const int per = kSetupThreads / a.row_threads, t = threadIdx.x;
+    const int64_t r0 = int64_t(group / a.parts) * per;
+    const int32_t part = int32_t(group % a.parts);
+    const int mine = t / a.row_threads, lane = t % a.row_threads;
+    const int64_t r = r0 + mine, c = (int64_t(part) * a.row_threads + lane) * 8;
+    int32_t count;
+    int64_t i = 0;
+    if (a.scans) {
+        count = scan_here(a, r0, per, s_rows, s_wave);
+        if (group == 0 && t == 0) *a.count = count;
+        if (r < count) i = s_rows[mine];
+        if (part == 0 && lane == 0 && r < count) a.rows[r] = int32_t(i);
+    } else {
+        count = *a.count;
+        if (r < count) i = a.rows[r];
+    }
     if (r < count) {
-        const int64_t i = a.rows[r];
         if (c < a.dp)
-            put8(a.x + r * a.dp, a.plane, static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
-        if (part == 0) {
-            if (t == 0 && a.top == 1) {
+            put8(a.x + r * a.dp, a.x_plane, static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
+        if (part == 0 && lane == 0) {
+            a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
+            if (a.top == 1) {
                 const int64_t e = a.index[i];
                 const bool out = a.logit && a.logit[i] == -__builtin_inff();
                 a.entry[r] = uint64_t(e) < uint64_t(a.v) && !out ? int32_t(e) : -1;
                 if (a.logit) a.teach[r] = a.logit[i];
             }
-            if (t == 0) a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
         }
-    } else if (r < (int64_t(count) + kHeadTile - 1) / kHeadTile * kHeadTile) {
-        if (c < a.dp) put8<T>(a.x + r * a.dp, a.plane, nullptr, c, a.d);
+    } else if (r < (int64_t(count) + kHeadDepth - 1) / kHeadDepth * kHeadDepth) {
+        // zeros as far as a stage of a sum over tokens may read
+        if (c < a.dp) put8<T>(a.x + r * a.dp, a.x_plane, nullptr, c, a.d);
     }
     if (r < a.n && !counts(a.index, a.weight, a.flag, r, a.v)) {
         if (a.grad_hidden) {
             T* out = static_cast<T*>(a.grad_hidden) + r * a.d;
-            for (int64_t k = int64_t(part) * threads + t; k < a.d; k += int64_t(a.parts) * threads)
+            for (int64_t k = int64_t(part) * a.row_threads + lane; k < a.d;
+                 k += int64_t(a.parts) * a.row_threads)
                 out[k] = T(0);
         }
-        if (t == 0 && part == 0) {
+        if (part == 0 && lane == 0) {
             a.loss[r] = 0.0f;
             if (a.lse) a.lse[r] = 0.0f;
         }
@@ -263,31 +338,18 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
 // in the teacher's), with their logits, and where each block's begin: a tile of
 // the logits then looks at its own entries alone. Scanning all 64 entries of
 // every token in every tile took 450 of 1330 us at 4096 x 32000 x 4096.
-struct EntryArgs {
-    const int64_t* index;
-    const float* logit;
-    const int32_t* rows;
-    const int32_t* count;
-    int32_t* entry;
-    float* teach;
-    uint16_t* start;   // [row][blocks + 1]
-    int64_t v;
-    int32_t top, top_pad, blocks;
-};
-
-__global__ __launch_bounds__(256) void entry_kernel(EntryArgs a) {
+__device__ __forceinline__ void setup_entries(const SetupArgs& a, int64_t r) {
     __shared__ int32_t s_block[kHeadMaxTop], s_sorted[kHeadMaxTop];
-    const int64_t r = blockIdx.x;
     const int t = threadIdx.x;
     if (r >= *a.count) return;
     const int64_t from = int64_t(a.rows[r]) * a.top;
-    for (int32_t k = t; k < a.top; k += 256) {
+    for (int32_t k = t; k < a.top; k += kSetupThreads) {
         const int64_t e = a.index[from + k];
         const bool on = uint64_t(e) < uint64_t(a.v) && a.logit[from + k] != -__builtin_inff();
         s_block[k] = on ? int32_t(e) / kHeadBlock : a.blocks;
     }
     __syncthreads();
-    for (int32_t k = t; k < a.top; k += 256) {
+    for (int32_t k = t; k < a.top; k += kSetupThreads) {
         const int32_t b = s_block[k];
         int32_t at = 0;
         for (int32_t o = 0; o < a.top; ++o) at += s_block[o] < b || (s_block[o] == b && o < k);
@@ -297,20 +359,27 @@ __global__ __launch_bounds__(256) void entry_kernel(EntryArgs a) {
     }
     __syncthreads();
     uint16_t* start = a.start + r * (a.blocks + 1);
-    for (int32_t k = t; k <= a.top; k += 256) {
+    for (int32_t k = t; k <= a.top; k += kSetupThreads) {
         const int32_t lo = k == 0 ? 0 : s_sorted[k - 1] + 1;
         const int32_t hi = k == a.top ? a.blocks : s_sorted[k];
         for (int32_t b = lo; b <= hi; ++b) start[b] = uint16_t(k);
     }
 }
 
-// The head's rows in planes of dp columns.
+// What the products need, in one launch: the rows of X, the tokens' entries
+// and, where it cannot be read in place, the head in planes of dp columns.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_head_kernel(const T* head, uint16_t* out, int64_t d,
-                                                        int64_t dp, int64_t plane, int32_t parts) {
-    const int64_t r = blockIdx.x / parts;
-    const int64_t c = ((blockIdx.x - r * parts) * blockDim.x + threadIdx.x) * 8;
-    if (c < dp) put8(out + r * dp, plane, head + r * d, c, d);
+__global__ __launch_bounds__(kSetupThreads) void setup_kernel(SetupArgs a) {
+    uint32_t group = blockIdx.x;
+    if (group < a.x_groups) return setup_rows<T>(a, group);
+    group -= a.x_groups;
+    if (group < a.entry_groups) return setup_entries(a, group);
+    group -= a.entry_groups;
+    const int per = kSetupThreads / a.row_threads;
+    const int64_t r = int64_t(group / a.parts) * per + threadIdx.x / a.row_threads;
+    const int64_t c = (int64_t(group % a.parts) * a.row_threads + threadIdx.x % a.row_threads) * 8;
+    if (r < a.v && c < a.dp)
+        put8(a.w + r * a.dp, a.w_plane, static_cast<const T*>(a.head) + r * a.d, c, a.d);
 }
 
 // ---- the products --------------------------------------------------------------------
@@ -1094,7 +1163,14 @@ TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
         return turns * ((kt + s - 1) / s * segs + 4) * stage;
     };
     // a turn's stage: 65536 outputs on a CU at 130, or 2 x 16384 at 105
-    return cost(kBig, 2 * 105) <= cost(kMid, 130) ? kBig : kMid;
+    if (cost(kBig, 2 * 105) <= cost(kMid, 130)) return kBig;
+    // less than a workgroup a CU: more stages on their way
+    const uint32_t tiles =
+        uint32_t((g.na + 127) / 128) * uint32_t((g.nb + 127) / 128);
+    return tiles * split_of(tiles, uint32_t((g.k + kHeadDepth - 1) / kHeadDepth), segs,
+                            g.slot_bits ? kLow2.slot_bits : 0) <= 256
+               ? kLow2
+               : kMid;
 }
 
 template <bool AM, bool BM, bool F32, int KIND>
@@ -1104,9 +1180,8 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
         return run_gemm<256, 256, 4, 2, 2, AM, BM, F32, KIND>(g, t, stream);
     if constexpr (!BM)
         if (t.bb == kLow.bb) return run_gemm<128, 64, 2, 2, 6, AM, BM, F32, KIND>(g, t, stream);
-    if constexpr (KIND == kLogits)
-        if (t.slot_bits == kLow2.slot_bits)
-            return run_gemm<128, 128, 2, 2, 4, AM, BM, F32, KIND>(g, t, stream);
+    if (t.slot_bits == kLow2.slot_bits)
+        return run_gemm<128, 128, 2, 2, 4, AM, BM, F32, KIND>(g, t, stream);
     return run_gemm<128, 128, 2, 2, 2, AM, BM, F32, KIND>(g, t, stream);
 }
 
@@ -1162,36 +1237,40 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     const bool grads = s.grad_hidden || s.grad_head;
     hipError_t e;
 
-    if (flag) {
-        flag_kernel<<<uint32_t((s.n + 3) / 4), 256, 0, stream>>>(
-            c.index, c.logit, s.n, s.v, s.top, c.token_weight, flag);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    scan_kernel<<<1, kScanThreads, 0, stream>>>(c.index, c.token_weight, flag, s.n, s.v, rows,
-                                                count);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
     const int64_t x_plane = s.rows * s.dp, w_plane = s.v * s.dp;
-    const int pack_threads = s.dp >= 2048 ? 256 : 64;
-    const int32_t pack_parts = int32_t((s.dp / 8 + pack_threads - 1) / pack_threads);
-    if (s.rows > 0) {
-        PackArgs p{c.hidden, c.index, c.logit, c.token_weight, flag, rows, count, coef, entry, teach, x,
-                   c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d, s.dp, x_plane, s.top, pack_parts, c.scale};
-        pack_kernel<T><<<uint32_t(s.rows * pack_parts), pack_threads, 0, stream>>>(p);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (start && s.n > 0) {
-        EntryArgs q{c.index, c.logit, rows, count, entry, teach, start, s.v, s.top, s.top_pad,
-                    blocks};
-        entry_kernel<<<uint32_t(s.n), 256, 0, stream>>>(q);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
     const uint16_t* w = static_cast<const uint16_t*>(c.head);
-    if (s.pack_head) {
-        uint16_t* packed = reinterpret_cast<uint16_t*>(ws + s.o_w);
-        pack_head_kernel<T><<<uint32_t(s.v * pack_parts), pack_threads, 0, stream>>>(
-            static_cast<const T*>(c.head), packed, s.d, s.dp, w_plane, pack_parts);
+    uint16_t* packed = s.pack_head ? reinterpret_cast<uint16_t*>(ws + s.o_w) : nullptr;
+    if (packed) w = packed;
+    const bool scans = !s.teacher && s.n > 0 && s.n <= kSelfScan;
+    if (!scans) {
+        const bool few = s.teacher && s.n <= kFlagTokens && s.n * s.top <= kFlagEntries;
+        if (flag && !few && s.n > 0) {
+            flag_kernel<<<uint32_t((s.n + 3) / 4), 256, 0, stream>>>(
+                c.index, c.logit, s.n, s.v, s.top, c.token_weight, flag);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        scan_kernel<<<1, kScanThreads, 0, stream>>>(c.index, few ? c.logit : nullptr, s.top,
+                                                    c.token_weight, flag, s.n, s.v, rows, count);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        w = packed;
+    }
+    {
+        int row_threads = 8;
+        while (row_threads < kSetupThreads && row_threads * 8 < s.dp) row_threads *= 2;
+        const int64_t per = kSetupThreads / row_threads;
+        const int32_t parts = int32_t((s.dp / 8 + row_threads - 1) / row_threads);
+        const int64_t x_rows = (s.n + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
+        const int64_t x_groups = (x_rows + per - 1) / per * parts;
+        const int64_t entry_groups = start ? s.n : 0;
+        const int64_t head_groups = packed ? (s.v + per - 1) / per * parts : 0;
+        SetupArgs q{c.hidden, c.head, c.index, c.logit, c.token_weight, flag, rows, count, coef,
+                    entry, teach, start, x, packed, c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d,
+                    s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, row_threads, parts,
+                    uint32_t(x_groups), uint32_t(entry_groups), scans, c.scale};
+        const int64_t groups = x_groups + entry_groups + head_groups;
+        if (groups > 0) {
+            setup_kernel<T><<<uint32_t(groups), kSetupThreads, 0, stream>>>(q);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
     }
 
     void* p = grads ? ws + s.o_p : nullptr;

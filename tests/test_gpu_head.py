@@ -178,7 +178,8 @@ def check(out, r):
 
 SHAPES = [(1, 1, 1), (1, 7, 3), (3, 64, 64), (5, 65, 40), (16, 256, 64), (31, 257, 128),
           (64, 1000, 72), (129, 1000, 1003), (200, 511, 192), (300, 4099, 320), (1, 5000, 512),
-          (700, 130, 256), (2, 3, 1000), (1025, 777, 64)]
+          (700, 130, 256), (2, 3, 1000), (1025, 777, 64), (2500, 130, 72), (40, 9000, 256),
+          (20000, 70, 24), (64, 8192, 1000), (65, 8193, 1000), (1500, 93, 4416)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])

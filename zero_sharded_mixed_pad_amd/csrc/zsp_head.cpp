@@ -49,6 +49,8 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.nchunk = std::max<int64_t>((n + chunk - 1) / chunk, 1);
     s.chunk = up((n + s.nchunk - 1) / s.nchunk, kHeadTile);
     if (s.chunk > 0) s.nchunk = std::max<int64_t>((n + s.chunk - 1) / s.chunk, 1);
+    s.raw = head_is_raw(s);
+
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t o = at;

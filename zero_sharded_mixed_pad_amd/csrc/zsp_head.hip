@@ -34,7 +34,6 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -105,7 +104,7 @@ __device__ __forceinline__ bool counts(const int64_t* target, const float* weigh
 // rows[0 .. count): the tokens that count, in order. One workgroup, 16 tokens
 // a thread at a time; the waves' counts are joined in LDS.
 constexpr int kScanThreads = 1024, kScanRun = 16;
-constexpr int64_t kFlagEntries = 65536, kFlagTokens = kScanThreads * kScanRun;
+constexpr int64_t kFlagEntries = 8192, kFlagTokens = kScanThreads * kScanRun;
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* target,
                                                             const float* logit, int32_t top,
                                                             const float* weight, uint8_t* flag,
@@ -176,45 +175,53 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* targe
     if (t == 0) *count = done;
 }
 
-// Eight elements of a row of d, from column c on, as planes of dp columns;
-// zeros past d, and everywhere if `in` is NULL.
+// Eight elements of a row of d, from column c on; zeros past d.
 template <typename T>
-__device__ __forceinline__ void put8(uint16_t* out, int64_t plane, const T* in, int64_t c,
-                                     int64_t d) {
-    if constexpr (sizeof(T) == 2) {
-        u32x4 v = {0, 0, 0, 0};
-        if (in && c + 8 <= d) {
-            v = *reinterpret_cast<const u32x4_a2*>(in + c);
-        } else if (in) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (c + k < d) v[k / 2] |= uint32_t(in[c + k]) << (16 * (k % 2));
+struct Eight {
+    static constexpr bool kF32 = sizeof(T) == 4;
+    u32x4 v[kF32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const T* in, int64_t c, int64_t d) {
+        if (c + 8 <= d) {
+            if constexpr (kF32) {
+                v[0] = *reinterpret_cast<const u32x4_a2*>(in + c);
+                v[1] = *reinterpret_cast<const u32x4_a2*>(in + c + 4);
+            } else {
+                v[0] = *reinterpret_cast<const u32x4_a2*>(in + c);
+            }
+            return;
         }
-        *reinterpret_cast<u32x4*>(out + c) = v;
-    } else {
-        float x[8];
-        if (in && c + 8 <= d) {
-            const f32x4 lo = *reinterpret_cast<const f32x4_a4*>(in + c);
-            const f32x4 hi = *reinterpret_cast<const f32x4_a4*>(in + c + 4);
+        zero();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = lo[k], x[4 + k] = hi[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = in && c + k < d ? in[c + k] : 0.0f;
-        }
-        u32x4 v[3];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint16_t p[3], q[3];
-            split3(x[2 * k], p);
-            split3(x[2 * k + 1], q);
-#pragma unroll
-            for (int h = 0; h < 3; ++h) v[h][k] = p[h] | uint32_t(q[h]) << 16;
-        }
-#pragma unroll
-        for (int h = 0; h < 3; ++h) *reinterpret_cast<u32x4*>(out + h * plane + c) = v[h];
+        for (int k = 0; k < 8; ++k)
+            if (c + k < d) {
+                if constexpr (kF32) v[k / 4][k % 4] = __float_as_uint(in[c + k]);
+                else v[0][k / 2] |= uint32_t(in[c + k]) << (16 * (k % 2));
+            }
     }
-}
+    __device__ __forceinline__ void zero() {
+        v[0] = u32x4{0, 0, 0, 0};
+        if constexpr (kF32) v[1] = v[0];
+    }
+    // As planes, `plane` elements apart.
+    __device__ __forceinline__ void store(uint16_t* out, int64_t plane) const {
+        if constexpr (kF32) {
+            u32x4 o[3];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint16_t p[3], q[3];
+                split3(__uint_as_float(v[k / 2][k % 2 * 2]), p);
+                split3(__uint_as_float(v[k / 2][k % 2 * 2 + 1]), q);
+#pragma unroll
+                for (int h = 0; h < 3; ++h) o[h][k] = p[h] | uint32_t(q[h]) << 16;
+            }
+#pragma unroll
+            for (int h = 0; h < 3; ++h) *reinterpret_cast<u32x4*>(out + h * plane) = o[h];
+        } else {
+            *reinterpret_cast<u32x4*>(out) = v[0];
+        }
+    }
+};
 
 struct SetupArgs {
     const void* hidden;
@@ -242,11 +249,13 @@ struct SetupArgs {
     float scale;
 };
 
-constexpr int kSetupThreads = 256, kSetupRun = 8;
+constexpr int kSetupThreads = 256, kSetupRun = 2;
+constexpr int kHeadRun = 4;  // rows of the head's copy a thread takes
 constexpr int64_t kSelfScan = kSetupThreads * kSetupRun;
 
 // Up to kSelfScan tokens: those that count, found by every workgroup for
-// itself (a launch and its wait cost more than reading the targets again).
+// itself (a launch and its wait take 5 us; at 1400 tokens the workgroups' own
+// scans took 7).
 // Leaves the tokens of rows [r0, r0 + n) in s_rows.
 __device__ __forceinline__ int32_t scan_here(const SetupArgs& a, int64_t r0, int n, int32_t* s_rows,
                                              int32_t* s_wave) {
@@ -305,8 +314,11 @@ __device__ __forceinline__ void setup_rows(const SetupArgs& a, uint32_t group) {
         if (r < count) i = a.rows[r];
     }
     if (r < count) {
-        if (c < a.dp)
-            put8(a.x + r * a.dp, a.x_plane, static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
+        if (c < a.dp) {
+            Eight<T> v;
+            v.load(static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
+            v.store(a.x + r * a.dp + c, a.x_plane);
+        }
         if (part == 0 && lane == 0) {
             a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
             if (a.top == 1) {
@@ -318,7 +330,11 @@ __device__ __forceinline__ void setup_rows(const SetupArgs& a, uint32_t group) {
         }
     } else if (r < (int64_t(count) + kHeadDepth - 1) / kHeadDepth * kHeadDepth) {
         // zeros as far as a stage of a sum over tokens may read
-        if (c < a.dp) put8<T>(a.x + r * a.dp, a.x_plane, nullptr, c, a.d);
+        if (c < a.dp) {
+            Eight<T> v;
+            v.zero();
+            v.store(a.x + r * a.dp + c, a.x_plane);
+        }
     }
     if (r < a.n && !counts(a.index, a.weight, a.flag, r, a.v)) {
         if (a.grad_hidden) {
@@ -376,10 +392,17 @@ __global__ __launch_bounds__(kSetupThreads) void setup_kernel(SetupArgs a) {
     if (group < a.entry_groups) return setup_entries(a, group);
     group -= a.entry_groups;
     const int per = kSetupThreads / a.row_threads;
-    const int64_t r = int64_t(group / a.parts) * per + threadIdx.x / a.row_threads;
+    const int64_t r0 = int64_t(group / a.parts) * per * kHeadRun + threadIdx.x / a.row_threads;
     const int64_t c = (int64_t(group % a.parts) * a.row_threads + threadIdx.x % a.row_threads) * 8;
-    if (r < a.v && c < a.dp)
-        put8(a.w + r * a.dp, a.w_plane, static_cast<const T*>(a.head) + r * a.d, c, a.d);
+    if (c >= a.dp) return;
+    const T* head = static_cast<const T*>(a.head);
+    Eight<T> v[kHeadRun];  // all loads on their way before the first store
+#pragma unroll
+    for (int k = 0; k < kHeadRun; ++k)
+        v[k].load(head + min(r0 + k * per, a.v - 1) * a.d, c, a.d);
+#pragma unroll
+    for (int k = 0; k < kHeadRun; ++k)
+        if (r0 + k * per < a.v) v[k].store(a.w + (r0 + k * per) * a.dp + c, a.w_plane);
 }
 
 // ---- the products --------------------------------------------------------------------
@@ -419,6 +442,7 @@ struct GemmArgs {
     const float* acc_in;       // fp32 [b][ldf] to add, or NULL
     float* acc_out;            // fp32 [b][ldf], instead of out
     float* split;              // fp32 [part of the sum][b][ldf], if the sums are split
+    int32_t keep_parts;        // the caller joins them
     int64_t ldf;
 };
 
@@ -909,16 +933,88 @@ __device__ __forceinline__ void put_g(const JoinArgs& a, int64_t row, int64_t co
         a.g[row * a.ldp + col] = bf16_bits(v);
     }
 }
+template <bool F32>
+__device__ __forceinline__ void put_g8(const JoinArgs& a, int64_t row, int64_t col,
+                                       const float v[8]) {
+    if constexpr (F32) {
+        Eight<float> e;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e.v[k / 4][k % 4] = __float_as_uint(v[k]);
+        e.store(a.g + row * a.ldp + col, a.plane);
+    } else {
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
+        *reinterpret_cast<u32x4*>(a.g + row * a.ldp + col) = o;
+    }
+}
+
+// The loss of row r from its lse and its entries' logits (logit(k, column));
+// leaves the entries' share of the target distribution in s_q. In 64 bits:
+// the loss is a small difference where the model agrees with its target.
+template <typename F>
+__device__ __forceinline__ double entries_loss(const JoinArgs& a, int64_t r, double lse, float* s_q,
+                                               double* s_d, float* s_f, F logit) {
+    const int t = threadIdx.x;
+    const int32_t* entry = a.entry + r * a.top_pad;
+    if (!a.teach) {
+        if (t == 0) s_q[0] = 1.0f;
+        __syncthreads();
+        return lse - double(logit(0, entry[0]));
+    }
+    const float* teach = a.teach + r * a.top_pad;
+    float tm = -__builtin_inff();
+    for (int32_t k = t; k < a.top; k += 256)
+        if (entry[k] >= 0) tm = nan_max(tm, teach[k]);
+    tm = block_max(tm, s_f);
+    double ts = 0.0;
+    for (int32_t k = t; k < a.top; k += 256)
+        if (entry[k] >= 0) ts += exp((double(teach[k]) - double(tm)) / double(a.temp));
+    ts = block_sum(ts, s_d);
+    const double lq = log(ts);  // from the largest: logits may all be far below 0
+    double loss = 0.0;
+    for (int32_t k = t; k < a.top; k += 256) {
+        double q = 0.0;
+        if (entry[k] >= 0) {
+            const double l = (double(teach[k]) - double(tm)) / double(a.temp) - lq;
+            q = exp(l);
+            if (q != 0.0) loss += q * (l - (double(logit(k, entry[k])) - lse));
+        }
+        s_q[k] = float(q);
+    }
+    return block_sum(loss, s_d) * double(a.temp) * double(a.temp);
+}
+
+// The entries' own G, in columns [from, to): c (p - q) with p - q = (p - 1) +
+// (1 - q) in 64 bits (from P's bf16, all of 1 - p would be lost where the model
+// is sure of its target). Entries of one column write the same sum of their q;
+// they stand in one block of the vocabulary, so beside each other.
+template <bool F32, typename F>
+__device__ __forceinline__ void entries_gradient(const JoinArgs& a, int64_t r, int64_t from,
+                                                 int64_t to, double lse, float c, const float* s_q,
+                                                 F logit) {
+    const int32_t* entry = a.entry + r * a.top_pad;
+    for (int32_t k = threadIdx.x; k < a.top; k += 256) {
+        const int32_t e = entry[k];
+        if (e < from || e >= to) continue;
+        const int32_t block = e / kHeadBlock;
+        int32_t first = k;
+        while (first > 0 && entry[first - 1] / kHeadBlock == block) --first;
+        double q = 0.0;
+        for (int32_t o = first; o < a.top && entry[o] >= 0 && entry[o] / kHeadBlock == block; ++o)
+            if (entry[o] == e) q += double(s_q[o]);
+        const double x = double(logit(k, e)) - lse;
+        put_g<F32>(a, r, e, float(double(c) * (expm1(x) + (1.0 - q))));
+    }
+}
 
 // A workgroup (several, where tokens are few) per token that counts: lse, the
-// loss, then the token's row of G. An entry's own G is taken from its logit in 64 bits: c (p - q) from P's
-// bf16 would lose all of 1 - p where the model is sure of its target.
+// loss, then the token's row of G.
 template <bool F32>
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     __shared__ double s_d[4];
     __shared__ float s_f[4];
     __shared__ float s_q[kHeadMaxTop];
-    __shared__ int32_t s_e[kHeadMaxTop];
     const int64_t r = blockIdx.x / a.parts, count = *a.count - a.first;
     const int32_t part_no = int32_t(blockIdx.x - r * a.parts);
     const int t = threadIdx.x;
@@ -946,41 +1042,10 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     s = block_sum(s, s_d);
     const double lse = double(m) + log(s);
 
-    // the entries' share of the target distribution, and the loss
     const int64_t token = a.rows[r];
-    const int32_t* entry = a.entry + r * a.top_pad;
     const float* pick = a.pick + r * a.top_pad;
-    double loss = 0.0;
-    if (a.teach) {
-        const float* teach = a.teach + r * a.top_pad;
-        float tm = -__builtin_inff();
-        for (int32_t k = t; k < a.top; k += 256)
-            if (entry[k] >= 0) tm = nan_max(tm, teach[k]);
-        tm = block_max(tm, s_f);
-        double ts = 0.0;
-        for (int32_t k = t; k < a.top; k += 256)
-            if (entry[k] >= 0) ts += exp((double(teach[k]) - double(tm)) / double(a.temp));
-        ts = block_sum(ts, s_d);
-        const double lq = log(ts);  // from the largest: logits may all be far below 0
-        for (int32_t k = t; k < a.top; k += 256) {
-            double q = 0.0;
-            if (entry[k] >= 0) {
-                const double l = (double(teach[k]) - double(tm)) / double(a.temp) - lq;
-                q = exp(l);
-                if (q != 0.0) loss += q * (l - (double(pick[k]) - lse));
-            }
-            s_q[k] = float(q);
-            s_e[k] = entry[k];
-        }
-        loss = block_sum(loss, s_d) * double(a.temp) * double(a.temp);
-    } else {
-        loss = lse - double(pick[0]);
-        if (t == 0) {
-            s_q[0] = 1.0f;
-            s_e[0] = entry[0];
-        }
-        __syncthreads();
-    }
+    auto logit = [&](int32_t k, int32_t) { return pick[k]; };
+    const double loss = entries_loss(a, r, lse, s_q, s_d, s_f, logit);
     if (t == 0 && part_no == 0) {
         a.loss[token] = float(loss);
         if (a.lse) a.lse[token] = float(lse);
@@ -1019,17 +1084,72 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     }
     __threadfence_block();
     __syncthreads();
-    // equal entries of a row write the same sum of their q
-    for (int32_t k = t; k < a.top; k += 256) {
-        const int32_t e = s_e[k];
-        if (e < from || e >= to) continue;
-        double q = 0.0;
-        for (int32_t o = 0; o < a.top; ++o)
-            if (s_e[o] == e) q += double(s_q[o]);
-        const double x = double(pick[k]) - lse;
-        // p - q = (p - 1) + (1 - q)
-        put_g<F32>(a, r, e, float(double(c) * (expm1(x) + (1.0 - q))));
+    entries_gradient<F32>(a, r, from, to, lse, c, s_q, logit);
+}
+
+// Few tiles (a small vocabulary, or few tokens): the logits' sums over d are
+// split too, their fp32 parts stand in the workspace, and a workgroup per
+// token joins them in LDS and takes the softmax, the loss and G from there.
+struct RawArgs {
+    JoinArgs j;
+    const float* raw;          // [part][row][ldp]
+    int64_t v, dp;
+    int64_t len;               // tokens of the chunk
+    uint32_t ba, bb, segs, slot_bits;
+};
+
+template <bool F32>
+__global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
+    extern __shared__ float s_l[];
+    __shared__ double s_d[4];
+    __shared__ float s_f[4];
+    __shared__ float s_q[kHeadMaxTop];
+    const JoinArgs& a = q.j;
+    const int64_t r = blockIdx.x;
+    const int32_t count = max(*a.count - int32_t(a.first), 0);
+    const int t = threadIdx.x, cols = a.blocks * kHeadBlock, v = int32_t(q.v);
+    if (r >= count) {
+        if (a.p && r < (count + kHeadDepth - 1) / kHeadDepth * kHeadDepth)
+            for (int c = t * 8; c < cols; c += 2048)
+                for (int k = 0; k < (F32 ? 3 : 1); ++k)
+                    *reinterpret_cast<u32x4*>(a.g + k * a.plane + r * a.ldp + c) = u32x4{0, 0, 0, 0};
+        return;
     }
+    const uint32_t tiles = (uint32_t(v) + q.ba - 1) / q.ba *
+                           ((uint32_t(min(int64_t(count), q.len)) + q.bb - 1) / q.bb);
+    const uint32_t ns = split_of(tiles, uint32_t(q.dp) / kHeadDepth, q.segs, q.slot_bits);
+    const int64_t stride = int64_t(min(int64_t(count), q.len)) * a.ldp;
+    const float* raw = q.raw + r * a.ldp;
+    float m = -__builtin_inff();
+    for (int c = t; c < v; c += 256) {
+        float l = 0.0f;
+#pragma unroll 4
+        for (uint32_t s = 0; s < ns; ++s) l += raw[s * stride + c];
+        l *= a.inv_temp;
+        s_l[c] = l;
+        m = nan_max(m, l);
+    }
+    m = block_max(m, s_f);
+    float part = 0.0f;
+    for (int c = t; c < v; c += 256) part += fast_exp(s_l[c] - m);
+    const double lse = double(m) + log(block_sum(double(part), s_d));
+    const int64_t token = a.rows[r];
+    const double loss = entries_loss(a, r, lse, s_q, s_d, s_f, [&](int32_t, int32_t e) { return s_l[e]; });
+    if (t == 0) {
+        a.loss[token] = float(loss);
+        if (a.lse) a.lse[token] = float(lse);
+    }
+    if (!a.p) return;
+    const float c = a.coef[r] * a.temp, l32 = float(lse);
+    for (int i = t * 8; i < cols; i += 2048) {
+        float g[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * fast_exp(s_l[i + k] - l32) : 0.0f;
+        put_g8<F32>(a, r, i, g);
+    }
+    __threadfence_block();
+    __syncthreads();
+    entries_gradient<F32>(a, r, 0, cols, lse, c, s_q, [&](int32_t, int32_t e) { return s_l[e]; });
 }
 
 // A gradient's split sums joined, in order: four columns a thread, `parts`
@@ -1137,7 +1257,7 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
         <<<uint32_t((m.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
     hipError_t e = hipGetLastError();
     if constexpr (KIND == kOut) {
-        if (e == hipSuccess && m.split_rows) {
+        if (e == hipSuccess && m.split_rows && !g.keep_parts) {
             SplitArgs q{g, t.ba, t.bb, F32 ? 6u : 1u, uint32_t((g.ldo + 1023) / 1024)};
             const int64_t rows = g.nb * q.parts;
             split_kernel<F32><<<uint32_t(std::min<int64_t>(rows, 4096)), 256, 0, stream>>>(q);
@@ -1164,13 +1284,12 @@ TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     };
     // a turn's stage: 65536 outputs on a CU at 130, or 2 x 16384 at 105
     if (cost(kBig, 2 * 105) <= cost(kMid, 130)) return kBig;
-    // less than a workgroup a CU: more stages on their way
-    const uint32_t tiles =
-        uint32_t((g.na + 127) / 128) * uint32_t((g.nb + 127) / 128);
-    return tiles * split_of(tiles, uint32_t((g.k + kHeadDepth - 1) / kHeadDepth), segs,
-                            g.slot_bits ? kLow2.slot_bits : 0) <= 256
-               ? kLow2
-               : kMid;
+    // at most a workgroup a CU (half of one if the sums are split: more parts
+    // serve better than more stages): more stages on their way
+    const uint32_t tiles = uint32_t((g.na + 127) / 128) * uint32_t((g.nb + 127) / 128);
+    const uint32_t parts = split_of(tiles, uint32_t((g.k + kHeadDepth - 1) / kHeadDepth), segs,
+                                    g.slot_bits ? kMid.slot_bits : 0);
+    return tiles * parts <= (g.slot_bits ? 128u : 256u) ? kLow2 : kMid;
 }
 
 template <bool AM, bool BM, bool F32, int KIND>
@@ -1201,6 +1320,20 @@ GemmArgs hidden_product(const HeadShape& s, int64_t len) {
     h.slot_bits = 1;
     h.ldo = s.d;
     h.ldf = s.dp;
+    return h;
+}
+GemmArgs raw_product(const HeadShape& s, int64_t len) {
+    GemmArgs h{};
+    h.lda = h.ldb = s.dp;
+    h.plane_a = s.v * s.dp;
+    h.plane_b = s.rows * s.dp;
+    h.na = s.v;
+    h.nb = len;
+    h.k = s.dp;
+    h.tokens_in_b = 1;
+    h.slot_bits = 1;
+    h.ldo = s.v;
+    h.ldf = s.vp;
     return h;
 }
 GemmArgs head_product(const HeadShape& s, int64_t len) {
@@ -1254,14 +1387,18 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     {
-        int row_threads = 8;
-        while (row_threads < kSetupThreads && row_threads * 8 < s.dp) row_threads *= 2;
+        // the most threads a row that leave at most a sixth of them idle
+        int row_threads = kSetupThreads;
+        const int64_t eights = s.dp / 8;
+        while (row_threads > 8 && ((eights + row_threads - 1) / row_threads * row_threads - eights) * 6 > eights)
+            row_threads /= 2;
         const int64_t per = kSetupThreads / row_threads;
         const int32_t parts = int32_t((s.dp / 8 + row_threads - 1) / row_threads);
         const int64_t x_rows = (s.n + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
         const int64_t x_groups = (x_rows + per - 1) / per * parts;
         const int64_t entry_groups = start ? s.n : 0;
-        const int64_t head_groups = packed ? (s.v + per - 1) / per * parts : 0;
+        const int64_t head_groups =
+            packed ? (s.v + per * kHeadRun - 1) / (per * kHeadRun) * parts : 0;
         SetupArgs q{c.hidden, c.head, c.index, c.logit, c.token_weight, flag, rows, count, coef,
                     entry, teach, start, x, packed, c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d,
                     s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, row_threads, parts,
@@ -1306,10 +1443,29 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.blocks = blocks;
         l.pick = pick + first * s.top_pad;
         l.top_pad = s.top_pad;
-        if (len > 0 && (e = pick_gemm<false, false, F32, kLogits>(l, stream)) != hipSuccess)
+        if (s.raw && len > 0) {
+            GemmArgs h = raw_product(s, len);
+            h.a = w;
+            h.b = l.b;
+            h.count = count;
+            h.first = first;
+            h.split = h.acc_out = split;
+            h.keep_parts = 1;
+            const TileShape t = tile_of(h, F32 ? 6 : 1, true);
+            if ((e = pick_gemm<false, false, F32, kOut>(h, stream)) != hipSuccess) return e;
+            JoinArgs j{nullptr, 0, blocks, count, first, rows + first, coef + first, l.entry,
+                       nullptr, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
+                       c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
+            RawArgs q{j, split, s.v, s.dp, len, t.ba, t.bb, F32 ? 6u : 1u, t.slot_bits};
+            const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
+            raw_join_kernel<F32><<<uint32_t(grads ? pad : len), 256, s.v * 4, stream>>>(q);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        } else if (len > 0 &&
+                   (e = pick_gemm<false, false, F32, kLogits>(l, stream)) != hipSuccess) {
             return e;
+        }
 
-        if (len > 0) {
+        if (!s.raw && len > 0) {
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
             // at least 4096 columns each
             const int64_t most = std::min<int64_t>((blocks + 63) / 64, 1024 / pad);
@@ -1353,21 +1509,31 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
 
 }  // namespace
 
+// Whether the logits' sums are worth splitting: a row of them has to fit LDS
+// beside others, and the whole product to leave most of the card idle.
+bool head_is_raw(const HeadShape& s) {
+    if (s.n == 0 || s.v > kHeadRawColumns || s.nchunk > 1) return false;
+    const GemmArgs h = raw_product(s, s.n);
+    const uint32_t segs = s.f32 ? 6 : 1;
+    const TileShape t = tile_of(h, segs, true);
+    const uint32_t tiles = uint32_t((h.na + t.ba - 1) / t.ba) * uint32_t((h.nb + t.bb - 1) / t.bb);
+    return split_of(tiles, uint32_t(h.k) / kHeadDepth, segs, t.slot_bits) > 1;
+}
+
 int64_t head_split_bytes(const HeadShape& s) {
     const uint32_t segs = s.f32 ? 6 : 1;
-    uint64_t rows = 0;
+    int64_t bytes = 0;
     for (int64_t ch = 0; ch < s.nchunk; ++ch) {
         const int64_t len = std::min(s.chunk, s.n - ch * s.chunk);
-        if (s.grad_hidden && len > 0) {
-            const GemmArgs h = hidden_product(s, len);
-            rows = std::max(rows, bound_of(h, tile_of(h, segs, true), segs).split_rows);
-        }
-        if (s.grad_head) {
-            const GemmArgs h = head_product(s, len);
-            rows = std::max(rows, bound_of(h, tile_of(h, segs, false), segs).split_rows);
-        }
+        auto add = [&](const GemmArgs& h, bool low, int64_t rows) {
+            const Bound m = bound_of(h, tile_of(h, segs, low), segs);
+            bytes = std::max(bytes, std::max(int64_t(m.split_rows), rows) * h.ldf * 4);
+        };
+        if (s.raw && len > 0) add(raw_product(s, len), true, len);
+        if (s.grad_hidden && len > 0) add(hidden_product(s, len), true, 0);
+        if (s.grad_head) add(head_product(s, len), false, 0);
     }
-    return int64_t(rows) * s.dp * 4;
+    return bytes;
 }
 
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {

@@ -15,7 +15,7 @@ constexpr int32_t kHeadTile = 256;       // rows and columns of P are padded to 
 constexpr int32_t kHeadBlock = 64;       // vocabulary columns per partial of a softmax
 constexpr int32_t kHeadDepth = 64;       // d is padded to it
 constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
-constexpr int32_t kHeadMaxSplit = 64;
+constexpr int32_t kHeadRawColumns = 8192;  // logits of a token that a workgroup keeps in LDS
 
 // Sizes of a call, and the byte offsets of its parts of the workspace.
 struct HeadShape {
@@ -24,6 +24,7 @@ struct HeadShape {
     bool f32 = false, teacher = false;
     bool grad_hidden = false, grad_head = false;
     bool pack_head = false;       // the head is copied: fp32, d or its address not aligned
+    bool raw = false;             // logits summed in parts, in the workspace
     int32_t planes = 1;           // bf16 planes of an operand: 3 hold an fp32 value
     int32_t top_pad = 1;          // entries per row in the workspace
     int64_t rows = 0;             // n padded to kHeadTile
@@ -50,7 +51,9 @@ struct HeadCall {
     char* ws;
 };
 
-// Bytes for the parts of the gradients' sums, if those are split.
+// Whether a call's logits are summed in parts.
+bool head_is_raw(const HeadShape& s);
+// Bytes for the parts of the sums that are split.
 int64_t head_split_bytes(const HeadShape& s);
 // Every launch of a call, in order, on `stream`.
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream);

@@ -408,8 +408,8 @@ def test_on_another_stream_and_replayed():
 
 
 def test_more_tokens_than_are_kept_at_a_time():
-    """Two chunks: 2^20 columns by 1100 tokens are more than 2 GiB of P."""
-    n, v, d = 1100, 1 << 20, 64
+    """Two chunks: 2^20 columns by 2200 tokens are more than 4 GiB of P."""
+    n, v, d = 2200, 1 << 20, 64
     x, w, t, _ = make(n, v, d, BF)
     t[::5] = -100
     loss, lse, gx, gw = call(x, w, t)

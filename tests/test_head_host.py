@@ -105,7 +105,8 @@ def test_workspace_is_bounded():
     """The softmax kept at a time does not grow with the tokens."""
     size = lambda n: binding.zsp_head_workspace(n, 131072, 4096, torch.bfloat16)  # noqa: E731
     per_token = 4096 * 2 + 16                       # the copy of hidden, and a few words
-    assert size(1 << 20) < (1 << 31) + 131072 * 4096 * 4 + (1 << 20) * (per_token + 8) + (1 << 30)
+    kept, acc, parts = (1 << 32) * 17 // 16, 131072 * 4096 * 4, 5 << 28
+    assert size(1 << 20) < kept + acc + parts + (1 << 20) * (per_token + 8)
     assert size(1 << 20) - size(1 << 19) < (1 << 19) * (per_token + 8) + (1 << 29)
     none = binding.zsp_head_workspace(4096, 32000, 4096, torch.bfloat16, grad_hidden=False,
                                       grad_head=False)

@@ -12,7 +12,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 22, kMaxDepth = 65536;
 // The softmax of at most so many bytes is kept at a time.
-constexpr int64_t kKeptBytes = int64_t(1) << 31;
+constexpr int64_t kKeptBytes = int64_t(1) << 32;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 

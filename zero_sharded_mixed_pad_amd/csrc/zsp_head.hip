@@ -33,7 +33,9 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -103,7 +105,7 @@ __device__ __forceinline__ bool counts(const int64_t* target, const float* weigh
 
 // rows[0 .. count): the tokens that count, in order. One workgroup, 16 tokens
 // a thread at a time; the waves' counts are joined in LDS.
-constexpr int kScanThreads = 1024, kScanRun = 16;
+constexpr int kScanThreads = 1024, kScanRun = 8;
 constexpr int64_t kFlagEntries = 8192, kFlagTokens = kScanThreads * kScanRun;
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* target,
                                                             const float* logit, int32_t top,
@@ -438,7 +440,6 @@ struct GemmArgs {
     void* out;                 // final: [row][ldo] of the output's type, or NULL
     int64_t ldo;
     const int32_t* rows;       // row of b, or NULL: b itself
-    int32_t aligned;           // rows of out start on 16 bytes
     const float* acc_in;       // fp32 [b][ldf] to add, or NULL
     float* acc_out;            // fp32 [b][ldf], instead of out
     float* split;              // fp32 [part of the sum][b][ldf], if the sums are split
@@ -854,8 +855,8 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 #pragma unroll
                 for (int a = 0; a < TA; ++a) {
                     const int64_t col = a_wave + a * 16 + lg * 4;
-                    if (g.aligned && col + 4 <= g.ldo) {
-                        *reinterpret_cast<f32x4*>(out + col) = acc[a][b];
+                    if (col + 4 <= g.ldo) {
+                        *reinterpret_cast<f32x4_a4*>(out + col) = acc[a][b];
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -868,8 +869,8 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
                 for (int a = 0; a < TA; a += 2) {
                     const u32x4 v = pair_of(acc[a][b], acc[a + 1][b]);
                     const int64_t col = a_wave + a * 16 + pair_column(lg);
-                    if (g.aligned && col + 8 <= g.ldo) {
-                        *reinterpret_cast<u32x4*>(out + col) = v;
+                    if (col + 8 <= g.ldo) {
+                        *reinterpret_cast<u32x4_a2*>(out + col) = v;
                     } else {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -1168,9 +1169,17 @@ __device__ __forceinline__ void join_split(const SplitArgs& a, int32_t nb, uint3
     const int64_t at = row * g.ldf + col;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (g.acc_in) v = *reinterpret_cast<const f32x4*>(g.acc_in + at);
-#pragma unroll 8
-    for (uint32_t s = 0; s < ns; ++s)
-        v += *reinterpret_cast<const f32x4*>(g.split + s * (int64_t(nb) * g.ldf) + at);
+    const float* part = g.split + at;
+    const int64_t stride = int64_t(nb) * g.ldf;
+    for (uint32_t s = 0; s < ns; s += 4) {
+        f32x4 q[4];  // all on their way before the first is added
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            q[k] = *reinterpret_cast<const f32x4*>(part + min(s + k, ns - 1) * stride);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (s + k < ns) v += q[k];
+    }
     if (g.acc_out) {
         *reinterpret_cast<f32x4*>(g.acc_out + at) = v;
         return;
@@ -1178,16 +1187,16 @@ __device__ __forceinline__ void join_split(const SplitArgs& a, int32_t nb, uint3
     const int64_t o = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo + col;
     if constexpr (F32) {
         float* out = static_cast<float*>(g.out) + o;
-        if (g.aligned && col + 4 <= g.ldo) {
-            *reinterpret_cast<f32x4*>(out) = v;
+        if (col + 4 <= g.ldo) {
+            *reinterpret_cast<f32x4_a4*>(out) = v;
         } else {
             for (int k = 0; k < 4; ++k)
                 if (col + k < g.ldo) out[k] = v[k];
         }
     } else {
         uint16_t* out = static_cast<uint16_t*>(g.out) + o;
-        if (g.aligned && col + 4 <= g.ldo) {
-            *reinterpret_cast<uint2*>(out) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+        if (col + 4 <= g.ldo) {
+            *reinterpret_cast<u32x2_a2*>(out) = u32x2_a2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         } else {
             for (int k = 0; k < 4; ++k)
                 if (col + k < g.ldo) out[k] = bf16_bits(v[k]);
@@ -1216,7 +1225,8 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 struct TileShape {
     uint32_t ba, bb, slot_bits;
 };
-constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8}, kLow2{128, 128, 8};
+constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8}, kLow2{128, 128, 8},
+    kShort{128, 128, 10};
 
 // Largest number of items (tiles times parts) and of partial rows times parts
 // over every number of tokens up to the call's.
@@ -1271,7 +1281,9 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
 // on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
 // 1.05: the smaller are taken where the larger leave more of the card idle.
 // For up to 64 and 128 tokens, where reading the head is what takes the time,
-// tiles of 128 x 64 and 128 x 128 with six and four stages on their way.
+// tiles of 128 x 64 and 128 x 128 with six and four stages on their way; for
+// the head's gradient of so few, where writing it does, three workgroups a CU
+// with one stage each.
 TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (low && g.tokens_in_b && g.nb <= 64) return kLow;
     if (low && g.part && g.nb <= 128) return kLow2;
@@ -1283,6 +1295,7 @@ TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
         return turns * ((kt + s - 1) / s * segs + 4) * stage;
     };
     // a turn's stage: 65536 outputs on a CU at 130, or 2 x 16384 at 105
+    if (g.tokens_in_k && g.nb * g.na >= (1 << 24) && g.k <= 2 * kHeadDepth) return kShort;
     if (cost(kBig, 2 * 105) <= cost(kMid, 130)) return kBig;
     // at most a workgroup a CU (half of one if the sums are split: more parts
     // serve better than more stages): more stages on their way
@@ -1299,6 +1312,9 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
         return run_gemm<256, 256, 4, 2, 2, AM, BM, F32, KIND>(g, t, stream);
     if constexpr (!BM)
         if (t.bb == kLow.bb) return run_gemm<128, 64, 2, 2, 6, AM, BM, F32, KIND>(g, t, stream);
+    if constexpr (BM)
+        if (t.slot_bits == kShort.slot_bits)
+            return run_gemm<128, 128, 2, 2, 1, AM, BM, F32, KIND>(g, t, stream);
     if (t.slot_bits == kLow2.slot_bits)
         return run_gemm<128, 128, 2, 2, 4, AM, BM, F32, KIND>(g, t, stream);
     return run_gemm<128, 128, 2, 2, 2, AM, BM, F32, KIND>(g, t, stream);
@@ -1415,10 +1431,6 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     const int64_t g_plane = s.chunk * s.vp;
     float* split = reinterpret_cast<float*>(ws + s.o_split);
     float* acc = reinterpret_cast<float*>(ws + s.o_acc);
-    auto aligned = [](const void* q, int64_t ld, size_t size) {
-        return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * int64_t(size) % 16 == 0;
-    };
-
     for (int64_t ch = 0; ch < s.nchunk; ++ch) {
         const int64_t first = ch * s.chunk, len = std::min(s.chunk, s.n - first);
         GemmArgs l{};
@@ -1485,7 +1497,6 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.first = first;
             h.out = c.grad_hidden;
             h.rows = rows + first;
-            h.aligned = aligned(c.grad_hidden, s.d, sizeof(T));
             h.split = split;
             if ((e = pick_gemm<true, false, F32, kOut>(h, stream)) != hipSuccess) return e;
         }
@@ -1497,7 +1508,6 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.count = count;
             h.first = first;
             h.out = c.grad_head;
-            h.aligned = aligned(c.grad_head, s.d, sizeof(T));
             h.split = split;
             h.acc_in = ch > 0 ? acc : nullptr;
             h.acc_out = ch + 1 < s.nchunk ? acc : nullptr;

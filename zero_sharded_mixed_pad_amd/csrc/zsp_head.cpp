@@ -68,6 +68,7 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
         if (s.top > 1) s.o_start = take(n * ((v + kHeadBlock - 1) / kHeadBlock + 1) * 2);
     }
     s.o_x = take(s.rows * s.dp * 2 * s.planes);
+    if (s.grad_head && !s.f32 && n <= kHeadFew) s.o_xt = take(up(n, 32) * s.dp * 2);
     if (s.pack_head) s.o_w = take(v * s.dp * 2 * s.planes);
     s.o_part = take(s.chunk * (s.vp / kHeadBlock) * 8);
     if (grads) s.o_p = take(s.chunk * s.vp * (s.f32 ? 4 : 2));

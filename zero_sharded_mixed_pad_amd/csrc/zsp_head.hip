@@ -205,6 +205,13 @@ struct Eight {
         v[0] = u32x4{0, 0, 0, 0};
         if constexpr (kF32) v[1] = v[0];
     }
+    // bf16: one element in each of eight rows.
+    __device__ __forceinline__ void turn(uint16_t* out, int64_t ld) const {
+        if constexpr (!kF32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[k * ld] = uint16_t(v[0][k / 2] >> (16 * (k % 2)));
+        }
+    }
     // As planes, `plane` elements apart.
     __device__ __forceinline__ void store(uint16_t* out, int64_t plane) const {
         if constexpr (kF32) {
@@ -239,6 +246,7 @@ struct SetupArgs {
     float* teach;
     uint16_t* start;   // [row][blocks + 1]
     uint16_t* x;
+    uint16_t* xt;      // [dp][few_pad], bf16 and few tokens only, or NULL
     uint16_t* w;
     void* grad_hidden;
     float* loss;
@@ -246,6 +254,7 @@ struct SetupArgs {
     int64_t n, v, d, dp, x_plane, w_plane;
     int32_t top, top_pad, blocks;
     int32_t row_threads, parts;               // threads a row, workgroups a row
+    int32_t few_pad;
     uint32_t x_groups, entry_groups;          // workgroups of each kind; the rest copy the head
     int32_t scans;                            // each workgroup finds the tokens itself
     float scale;
@@ -320,6 +329,7 @@ __device__ __forceinline__ void setup_rows(const SetupArgs& a, uint32_t group) {
             Eight<T> v;
             v.load(static_cast<const T*>(a.hidden) + i * a.d, c, a.d);
             v.store(a.x + r * a.dp + c, a.x_plane);
+            if (a.xt) v.turn(a.xt + c * a.few_pad + r, a.few_pad);
         }
         if (part == 0 && lane == 0) {
             a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
@@ -337,6 +347,11 @@ __device__ __forceinline__ void setup_rows(const SetupArgs& a, uint32_t group) {
             v.zero();
             v.store(a.x + r * a.dp + c, a.x_plane);
         }
+    }
+    if (a.xt && r >= count && r < a.few_pad && c < a.dp) {
+        Eight<T> v;
+        v.zero();
+        v.turn(a.xt + c * a.few_pad + r, a.few_pad);
     }
     if (r < a.n && !counts(a.index, a.weight, a.flag, r, a.v)) {
         if (a.grad_hidden) {
@@ -707,21 +722,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
         }
     };
     using std::integral_constant;
-    if constexpr (NST == 1) {
-        // Short sums, where writing the output is what takes the time: several
-        // workgroups a CU hide each other's loads and stores.
-        for (int it = 0; it < steps; ++it) {
-            if (it > 0) wg_barrier();
-            issue(0, 0, kPer);
-            wait_stage<0>();
-            wg_barrier();
-#pragma unroll
-            for (int i = 0; i < TA + TB; ++i) read(0, 0, i);
-            work(integral_constant<int, 0>(), 0, integral_constant<bool, false>(), 0);
-            work(integral_constant<int, 1>(), 0, integral_constant<bool, false>(), 0);
-            wait_stage<0>();
-        }
-    } else if (steps > 0) {
+    if (steps > 0) {
 #pragma unroll
         for (int i = 0; i < NST; ++i) issue(i, 0, kPer);
         wait_stage<(NST - 1) * kPer>();
@@ -729,12 +730,12 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 #pragma unroll
         for (int i = 0; i < TA + TB; ++i) read(0, 0, i);
     }
-    for (int it = 0; NST > 1 && it < steps; ++it) {
+    for (int it = 0; it < steps; ++it) {
         __builtin_amdgcn_sched_barrier(0);
         work(integral_constant<int, 0>(), buf, integral_constant<bool, false>(), 0);
         // this wave has read all of this stage, and its part of the next has
         // landed; then that holds for every wave
-        wait_stage<(NST > 2 ? NST - 2 : 0) * kPer>();
+        wait_stage<(NST - 2) * kPer>();
         wg_barrier();
         const int old = buf;
         buf = NST == 2 ? buf ^ 1 : buf + 1 == NST ? 0 : buf + 1;
@@ -1153,6 +1154,111 @@ __global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
     entries_gradient<F32>(a, r, 0, cols, lse, c, s_q, [&](int32_t, int32_t e) { return s_l[e]; });
 }
 
+// The head's gradient of few tokens (bf16): rows of d for every column of the
+// vocabulary, of sums over at most 32 KS tokens, so that writing them is what
+// takes the time. A workgroup holds 64 columns of G (through LDS, transposed,
+// in registers); its waves go along the rows of X^T, which the L2 holds, and
+// write: no stage waits for another, nothing for a barrier. 32000 x 4096 of 96
+// tokens: 90 us by tiles, 73 this way; of 17: 69 and 45.
+struct OuterArgs {
+    const uint16_t* xt;        // [dp][32 KS]
+    const uint16_t* g;         // [token][ldp]
+    uint16_t* out;             // [v][d]
+    const int32_t* count;
+    int64_t v, d, dp, ldp;
+    int32_t parts, steps;      // workgroups for 64 columns, 64-column steps a wave
+};
+
+template <int KS>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
+    __shared__ __attribute__((aligned(16))) char s_g[32 * KS * 128];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, lr = lane % 16, lg = lane / 16;
+    const int64_t v0 = int64_t(blockIdx.x / a.parts) * 64;
+    const int32_t count = *a.count;
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        const int k = i * 32 + threadIdx.x / 8, c = threadIdx.x % 8;
+        u32x4 q = {0, 0, 0, 0};
+        if (k < count) q = *reinterpret_cast<const u32x4*>(a.g + k * a.ldp + v0 + c * 8);
+        *reinterpret_cast<u32x4*>(s_g + k * 128 + c * 16) = q;
+    }
+    __syncthreads();
+    bf16x8 fb[4][KS];
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const int row = k * 32 + lg * 8 + lr / 4;
+            ZSP_LDS char* at = (ZSP_LDS char*)s_g + row * 128 + b * 32 + (lr % 4) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZSP_LDS s16x4*)at);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZSP_LDS s16x4*)(at + 512));
+            fb[b][k] = __builtin_bit_cast(
+                bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    const int64_t first = (int64_t(blockIdx.x % a.parts) * 4 + wave) * a.steps * 64;
+    const int64_t last = min(first + a.steps * 64, a.dp);
+    // the next step's rows on their way while this one's are multiplied
+    bf16x8 fa[4][KS], next[4][KS];
+    auto load = [&](int64_t c0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                next[i][k] = *reinterpret_cast<const bf16x8*>(
+                    a.xt + (c0 + i * 16 + lr) * (32 * KS) + k * 32 + lg * 8);
+    };
+    if (first < last) load(first);
+    for (int64_t c0 = first; c0 < last; c0 += 64) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) fa[i][k] = next[i][k];
+        if (c0 + 64 < last) load(c0 + 64);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            f32x4 acc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i][k], fb[b][k], acc[i], 0,
+                                                                     0, 0);
+            }
+            const int64_t row = v0 + b * 16 + lr;
+            uint16_t* out = a.out + row * a.d;
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const u32x4 v = pair_of(acc[i], acc[i + 1]);
+                const int64_t col = c0 + i * 16 + pair_column(lg);
+                if (row >= a.v) continue;
+                if (col + 8 <= a.d) {
+                    *reinterpret_cast<u32x4_a2*>(out + col) = v;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (col + k < a.d) out[col + k] = uint16_t(v[k / 2] >> (16 * (k % 2)));
+                }
+            }
+        }
+    }
+}
+
+hipError_t run_outer(OuterArgs a, int64_t n, hipStream_t stream) {
+    const int64_t blocks = (a.v + 63) / 64, columns = a.dp / 64;
+    // eight waves a CU at least, where there are columns enough
+    a.parts = int32_t(std::min<int64_t>((511 + blocks) / blocks, (columns + 3) / 4));
+    a.steps = int32_t((columns + a.parts * 4 - 1) / (a.parts * 4));
+    const uint32_t grid = uint32_t(blocks * a.parts);
+    switch ((n + 31) / 32) {
+        case 1: outer_kernel<1><<<grid, 256, 0, stream>>>(a); break;
+        case 2: outer_kernel<2><<<grid, 256, 0, stream>>>(a); break;
+        case 3: outer_kernel<3><<<grid, 256, 0, stream>>>(a); break;
+        default: outer_kernel<4><<<grid, 256, 0, stream>>>(a); break;
+    }
+    return hipGetLastError();
+}
+
 // A gradient's split sums joined, in order: four columns a thread, `parts`
 // workgroups a row. Nothing to do where the product's sums were not split.
 struct SplitArgs {
@@ -1225,8 +1331,7 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 struct TileShape {
     uint32_t ba, bb, slot_bits;
 };
-constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8}, kLow2{128, 128, 8},
-    kShort{128, 128, 10};
+constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8}, kLow2{128, 128, 8};
 
 // Largest number of items (tiles times parts) and of partial rows times parts
 // over every number of tokens up to the call's.
@@ -1281,9 +1386,7 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
 // on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
 // 1.05: the smaller are taken where the larger leave more of the card idle.
 // For up to 64 and 128 tokens, where reading the head is what takes the time,
-// tiles of 128 x 64 and 128 x 128 with six and four stages on their way; for
-// the head's gradient of so few, where writing it does, three workgroups a CU
-// with one stage each.
+// tiles of 128 x 64 and 128 x 128 with six and four stages on their way.
 TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (low && g.tokens_in_b && g.nb <= 64) return kLow;
     if (low && g.part && g.nb <= 128) return kLow2;
@@ -1295,7 +1398,6 @@ TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
         return turns * ((kt + s - 1) / s * segs + 4) * stage;
     };
     // a turn's stage: 65536 outputs on a CU at 130, or 2 x 16384 at 105
-    if (g.tokens_in_k && g.nb * g.na >= (1 << 24) && g.k <= 2 * kHeadDepth) return kShort;
     if (cost(kBig, 2 * 105) <= cost(kMid, 130)) return kBig;
     // at most a workgroup a CU (half of one if the sums are split: more parts
     // serve better than more stages): more stages on their way
@@ -1312,9 +1414,6 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
         return run_gemm<256, 256, 4, 2, 2, AM, BM, F32, KIND>(g, t, stream);
     if constexpr (!BM)
         if (t.bb == kLow.bb) return run_gemm<128, 64, 2, 2, 6, AM, BM, F32, KIND>(g, t, stream);
-    if constexpr (BM)
-        if (t.slot_bits == kShort.slot_bits)
-            return run_gemm<128, 128, 2, 2, 1, AM, BM, F32, KIND>(g, t, stream);
     if (t.slot_bits == kLow2.slot_bits)
         return run_gemm<128, 128, 2, 2, 4, AM, BM, F32, KIND>(g, t, stream);
     return run_gemm<128, 128, 2, 2, 2, AM, BM, F32, KIND>(g, t, stream);
@@ -1390,6 +1489,10 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     const uint16_t* w = static_cast<const uint16_t*>(c.head);
     uint16_t* packed = s.pack_head ? reinterpret_cast<uint16_t*>(ws + s.o_w) : nullptr;
     if (packed) w = packed;
+    // few tokens' gradient of the head goes by its own way
+    const bool few_tokens = !F32 && s.grad_head && s.n > 0 && s.n <= kHeadFew;
+    const int32_t few_pad = int32_t((s.n + 31) / 32 * 32);
+    uint16_t* xt = few_tokens ? reinterpret_cast<uint16_t*>(ws + s.o_xt) : nullptr;
     const bool scans = !s.teacher && s.n > 0 && s.n <= kSelfScan;
     if (!scans) {
         const bool few = s.teacher && s.n <= kFlagTokens && s.n * s.top <= kFlagEntries;
@@ -1416,8 +1519,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         const int64_t head_groups =
             packed ? (s.v + per * kHeadRun - 1) / (per * kHeadRun) * parts : 0;
         SetupArgs q{c.hidden, c.head, c.index, c.logit, c.token_weight, flag, rows, count, coef,
-                    entry, teach, start, x, packed, c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d,
-                    s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, row_threads, parts,
+                    entry, teach, start, x, xt, packed, c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d,
+                    s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, row_threads, parts, few_pad,
                     uint32_t(x_groups), uint32_t(entry_groups), scans, c.scale};
         const int64_t groups = x_groups + entry_groups + head_groups;
         if (groups > 0) {
@@ -1500,7 +1603,11 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.split = split;
             if ((e = pick_gemm<true, false, F32, kOut>(h, stream)) != hipSuccess) return e;
         }
-        if (s.grad_head) {
+        if (few_tokens) {
+            const OuterArgs o{xt, gp, static_cast<uint16_t*>(c.grad_head), count, s.v, s.d, s.dp,
+                              s.vp, 0, 0};
+            if ((e = run_outer(o, s.n, stream)) != hipSuccess) return e;
+        } else if (s.grad_head) {
             GemmArgs h = head_product(s, len);
             h.a = x + first * s.dp;
             h.b = gp;

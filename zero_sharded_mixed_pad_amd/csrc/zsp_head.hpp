@@ -15,6 +15,7 @@ constexpr int32_t kHeadTile = 256;       // rows and columns of P are padded to 
 constexpr int32_t kHeadBlock = 64;       // vocabulary columns per partial of a softmax
 constexpr int32_t kHeadDepth = 64;       // d is padded to it
 constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
+constexpr int32_t kHeadFew = 128;        // tokens whose gradient of the head has a way of its own
 constexpr int32_t kHeadRawColumns = 8192;  // logits of a token that a workgroup keeps in LDS
 
 // Sizes of a call, and the byte offsets of its parts of the workspace.
@@ -33,7 +34,7 @@ struct HeadShape {
     int64_t nchunk = 0;
     // offsets
     int64_t o_count = 0, o_rows = 0, o_coef = 0, o_entry = 0, o_pick = 0, o_teach = 0, o_start = 0,
-            o_flag = 0, o_x = 0, o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
+            o_flag = 0, o_x = 0, o_xt = 0, o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
     int64_t bytes = 0;
 };
 

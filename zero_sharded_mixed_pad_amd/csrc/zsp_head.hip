@@ -3,7 +3,8 @@
 //
 //   l_iv = (x_i . w_v) / T          lse_i = log sum_v exp l_iv
 //   p_iv = exp(l_iv - lse_i)        q_i: the target, or the teacher's softmax
-//   G_iv = c_i (p_iv - q_iv)        dX = G W        dW = G^T X
+//   G_iv = c_i (p_iv - q_iv)        dX = s G W      dW = s G^T X
+//   c_i: the token's weight         s = scale * T
 //
 // The logits are never kept: the first product's tiles leave, per token and
 // block of 64 columns, the block's largest logit m and the sum of
@@ -257,7 +258,6 @@ struct SetupArgs {
     int32_t few_pad;
     uint32_t x_groups, entry_groups;          // workgroups of each kind; the rest copy the head
     int32_t scans;                            // each workgroup finds the tokens itself
-    float scale;
 };
 
 constexpr int kSetupThreads = 256, kSetupRun = 2;
@@ -332,7 +332,7 @@ __device__ __forceinline__ void setup_rows(const SetupArgs& a, uint32_t group) {
             if (a.xt) v.turn(a.xt + c * a.few_pad + r, a.few_pad);
         }
         if (part == 0 && lane == 0) {
-            a.coef[r] = a.weight ? a.scale * a.weight[i] : a.scale;
+            a.coef[r] = a.weight ? a.weight[i] : 1.0f;
             if (a.top == 1) {
                 const int64_t e = a.index[i];
                 const bool out = a.logit && a.logit[i] == -__builtin_inff();
@@ -454,6 +454,7 @@ struct GemmArgs {
     // outputs
     void* out;                 // final: [row][ldo] of the output's type, or NULL
     int64_t ldo;
+    float factor;              // of what goes to out
     const int32_t* rows;       // row of b, or NULL: b itself
     const float* acc_in;       // fp32 [b][ldf] to add, or NULL
     float* acc_out;            // fp32 [b][ldf], instead of out
@@ -851,6 +852,8 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
                 if (out) continue;
             }
             const int64_t at = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo;
+#pragma unroll
+            for (int a = 0; a < TA; ++a) acc[a][b] *= g.factor;
             if constexpr (F32) {
                 float* out = static_cast<float*>(g.out) + at;
 #pragma unroll
@@ -1054,7 +1057,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     }
     if (!a.p) return;
 
-    const float c = a.coef[r] * a.temp;
+    const float c = a.coef[r];
     const float l32 = float(lse);
     if constexpr (F32) {
         const float* p = static_cast<const float*>(a.p) + r * a.ldp;
@@ -1142,7 +1145,7 @@ __global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
         if (a.lse) a.lse[token] = float(lse);
     }
     if (!a.p) return;
-    const float c = a.coef[r] * a.temp, l32 = float(lse);
+    const float c = a.coef[r], l32 = float(lse);
     for (int i = t * 8; i < cols; i += 2048) {
         float g[8];
 #pragma unroll
@@ -1166,6 +1169,7 @@ struct OuterArgs {
     uint16_t* out;             // [v][d]
     const int32_t* count;
     int64_t v, d, dp, ldp;
+    float factor;
     int32_t parts, steps;      // workgroups for 64 columns, 64-column steps a wave
 };
 
@@ -1229,7 +1233,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
             uint16_t* out = a.out + row * a.d;
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                const u32x4 v = pair_of(acc[i], acc[i + 1]);
+                const u32x4 v = pair_of(acc[i] * a.factor, acc[i + 1] * a.factor);
                 const int64_t col = c0 + i * 16 + pair_column(lg);
                 if (row >= a.v) continue;
                 if (col + 8 <= a.d) {
@@ -1290,6 +1294,7 @@ __device__ __forceinline__ void join_split(const SplitArgs& a, int32_t nb, uint3
         *reinterpret_cast<f32x4*>(g.acc_out + at) = v;
         return;
     }
+    v *= g.factor;
     const int64_t o = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo + col;
     if constexpr (F32) {
         float* out = static_cast<float*>(g.out) + o;
@@ -1521,7 +1526,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         SetupArgs q{c.hidden, c.head, c.index, c.logit, c.token_weight, flag, rows, count, coef,
                     entry, teach, start, x, xt, packed, c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d,
                     s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, row_threads, parts, few_pad,
-                    uint32_t(x_groups), uint32_t(entry_groups), scans, c.scale};
+                    uint32_t(x_groups), uint32_t(entry_groups), scans};
         const int64_t groups = x_groups + entry_groups + head_groups;
         if (groups > 0) {
             setup_kernel<T><<<uint32_t(groups), kSetupThreads, 0, stream>>>(q);
@@ -1529,6 +1534,9 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         }
     }
 
+    // What all tokens have in common comes to the gradients in fp32: a factor
+    // of 1/96 within G would give every target's -1 the same error in bf16.
+    const float factor = c.scale * c.temperature;
     void* p = grads ? ws + s.o_p : nullptr;
     uint16_t* gp = reinterpret_cast<uint16_t*>(ws + (F32 ? s.o_g : s.o_p));
     const int64_t g_plane = s.chunk * s.vp;
@@ -1599,13 +1607,14 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.count = count;
             h.first = first;
             h.out = c.grad_hidden;
+            h.factor = factor;
             h.rows = rows + first;
             h.split = split;
             if ((e = pick_gemm<true, false, F32, kOut>(h, stream)) != hipSuccess) return e;
         }
         if (few_tokens) {
             const OuterArgs o{xt, gp, static_cast<uint16_t*>(c.grad_head), count, s.v, s.d, s.dp,
-                              s.vp, 0, 0};
+                              s.vp, factor, 0, 0};
             if ((e = run_outer(o, s.n, stream)) != hipSuccess) return e;
         } else if (s.grad_head) {
             GemmArgs h = head_product(s, len);
@@ -1615,6 +1624,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.count = count;
             h.first = first;
             h.out = c.grad_head;
+            h.factor = factor;
             h.split = split;
             h.acc_in = ch > 0 ? acc : nullptr;
             h.acc_out = ch + 1 < s.nchunk ? acc : nullptr;

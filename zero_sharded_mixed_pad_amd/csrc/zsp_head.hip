@@ -468,14 +468,20 @@ enum { kLogits = 0, kOut = 1 };
 // 16 bytes a lane from base + off to lds + 16 * lane. In assembly: the
 // compiler would wait for every such load before each transposing LDS read.
 // Nothing else here uses m0. The caller waits (wait_stage).
+template <bool NT>
 __device__ __forceinline__ void load_to_lds(const char* base, uint32_t off, ZSP_LDS char* lds) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(uint32_t(uintptr_t(lds)));
     const uint64_t p = reinterpret_cast<uint64_t>(base);
     const uint64_t from = uint64_t(__builtin_amdgcn_readfirstlane(uint32_t(p >> 32))) << 32 |
                           uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(p)));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off),
-                 "s"(from)
-                 : "memory");
+    if constexpr (NT)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(at),
+                     "v"(off), "s"(from)
+                     : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at),
+                     "v"(off), "s"(from)
+                     : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_stage() {
@@ -532,7 +538,7 @@ __host__ __device__ inline uint32_t split_of(uint32_t tiles, uint32_t stages, ui
 // the groups in a row is changed on the reading side of the load: group c of
 // a row is kept at c ^ s(row), which spreads the lanes of one LDS read over
 // the banks.
-template <int X, int BK, int WAVES, bool MMAJ, bool CLAMP>
+template <int X, int BK, int WAVES, bool MMAJ, bool CLAMP, bool NT>
 struct Operand {
     static constexpr int kGroups = X * BK / 8;
     static constexpr int kLoads = kGroups / 64 / WAVES;
@@ -584,7 +590,7 @@ struct Operand {
             const int32_t k = k_last - k0 < BK ? int32_t(k_last - k0) : BK;
             o += uint32_t(krow[i] < k ? krow[i] : k) * uint32_t(ld);
         }
-        load_to_lds(src, o, lds + (wave * kLoads + i) * 1024);
+        load_to_lds<NT>(src, o, lds + (wave * kLoads + i) * 1024);
     }
     // The operand's 16 x 32 values for tile `x` (a multiple of 16, of the
     // wave's share at x_wave) and k's [32 kk, 32 kk + 32).
@@ -612,13 +618,13 @@ struct Operand {
 __device__ __forceinline__ int plane_a_of(int seg) { return (0x201010 >> (4 * seg)) & 0xf; }
 __device__ __forceinline__ int plane_b_of(int seg) { return (0x021100 >> (4 * seg)) & 0xf; }
 
-template <int BA, int BB, int WA, int WB, int NST, bool AM, bool BM, bool F32, int KIND>
+template <int BA, int BB, int WA, int WB, int NST, bool NT, bool AM, bool BM, bool F32, int KIND>
 __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     constexpr int kWaves = WA * WB, BK = kHeadDepth;
     constexpr int EA = BA / WA, EB = BB / WB, TA = EA / 16, TB = EB / 16;
     static_assert(EA == kHeadBlock && TA == 4, "a wave's columns are one block");
-    using OpA = Operand<BA, BK, kWaves, AM, AM && !BM>;  // the head's rows end at v
-    using OpB = Operand<BB, BK, kWaves, BM, false>;
+    using OpA = Operand<BA, BK, kWaves, AM, AM && !BM, NT>;  // the head's rows end at v
+    using OpB = Operand<BB, BK, kWaves, BM, false, false>;
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
     constexpr int kPer = OpA::kLoads + OpB::kLoads;
     constexpr int kSegs = F32 ? 6 : 1;
@@ -1331,12 +1337,16 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 
 // ---- launches ------------------------------------------------------------------------
 
-// A product's tiles: columns and rows of a tile, and how many the card runs
-// at once (log2).
+// A product's tiles: columns and rows of a tile, how many the card runs at once
+// (log2), and which form.
+enum Form { kFormBig, kFormMid, kFormMidOnce, kFormLow, kFormLow2 };
 struct TileShape {
     uint32_t ba, bb, slot_bits;
+    Form form;
 };
-constexpr TileShape kBig{256, 256, 8}, kMid{128, 128, 9}, kLow{128, 64, 8}, kLow2{128, 128, 8};
+constexpr TileShape kBig{256, 256, 8, kFormBig}, kMid{128, 128, 9, kFormMid},
+    kMidOnce{128, 128, 9, kFormMidOnce}, kLow{128, 64, 8, kFormLow},
+    kLow2{128, 128, 8, kFormLow2};
 
 // Largest number of items (tiles times parts) and of partial rows times parts
 // over every number of tokens up to the call's.
@@ -1367,13 +1377,13 @@ Bound bound_of(const GemmArgs& g, TileShape t, uint32_t segs) {
     return m;
 }
 
-template <int BA, int BB, int WA, int WB, int NST, bool AM, bool BM, bool F32, int KIND>
+template <int BA, int BB, int WA, int WB, int NST, bool NT, bool AM, bool BM, bool F32, int KIND>
 hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
     static_assert(BA <= kHeadTile && BB <= kHeadTile, "");
     if (g.slot_bits) g.slot_bits = t.slot_bits;
     const Bound m = bound_of(g, t, F32 ? 6 : 1);
     if (m.items == 0) return hipSuccess;
-    gemm_kernel<BA, BB, WA, WB, NST, AM, BM, F32, KIND>
+    gemm_kernel<BA, BB, WA, WB, NST, NT, AM, BM, F32, KIND>
         <<<uint32_t((m.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
     hipError_t e = hipGetLastError();
     if constexpr (KIND == kOut) {
@@ -1391,10 +1401,15 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
 // on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
 // 1.05: the smaller are taken where the larger leave more of the card idle.
 // For up to 64 and 128 tokens, where reading the head is what takes the time,
-// tiles of 128 x 64 and 128 x 128 with six and four stages on their way.
+// tiles of 128 x 64 and 128 x 128 with six and four stages on their way. They
+// read it non-temporally: kept in the caches, it would only be driven out by
+// the head's gradient, which they can hold instead until it is written
+// (32000 x 4096 of 5 tokens 46.8 -> 42.3 us alone; 17 tokens with gradients
+// 198 -> 175).
 TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (low && g.tokens_in_b && g.nb <= 64) return kLow;
-    if (low && g.part && g.nb <= 128) return kLow2;
+    const bool few = low && g.tokens_in_b && g.nb <= 128;
+    if (few && !g.slot_bits) return kLow2;
     auto cost = [&](TileShape t, uint64_t stage) {
         const uint32_t tiles = uint32_t((g.na + t.ba - 1) / t.ba) * uint32_t((g.nb + t.bb - 1) / t.bb);
         const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
@@ -1409,19 +1424,26 @@ TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     const uint32_t tiles = uint32_t((g.na + 127) / 128) * uint32_t((g.nb + 127) / 128);
     const uint32_t parts = split_of(tiles, uint32_t((g.k + kHeadDepth - 1) / kHeadDepth), segs,
                                     g.slot_bits ? kMid.slot_bits : 0);
-    return tiles * parts <= (g.slot_bits ? 128u : 256u) ? kLow2 : kMid;
+    if (tiles * parts <= (g.slot_bits ? 128u : 256u)) return kLow2;
+    return few ? kMidOnce : kMid;
 }
 
 template <bool AM, bool BM, bool F32, int KIND>
 hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
     const TileShape t = tile_of(g, F32 ? 6 : 1, !BM);
-    if (t.ba == kBig.ba)
-        return run_gemm<256, 256, 4, 2, 2, AM, BM, F32, KIND>(g, t, stream);
-    if constexpr (!BM)
-        if (t.bb == kLow.bb) return run_gemm<128, 64, 2, 2, 6, AM, BM, F32, KIND>(g, t, stream);
-    if (t.slot_bits == kLow2.slot_bits)
-        return run_gemm<128, 128, 2, 2, 4, AM, BM, F32, KIND>(g, t, stream);
-    return run_gemm<128, 128, 2, 2, 2, AM, BM, F32, KIND>(g, t, stream);
+    if (t.form == kFormBig)
+        return run_gemm<256, 256, 4, 2, 2, false, AM, BM, F32, KIND>(g, t, stream);
+    if constexpr (!BM) {
+        if (t.form == kFormLow)
+            return run_gemm<128, 64, 2, 2, 6, !F32, AM, BM, F32, KIND>(g, t, stream);
+        if (t.form == kFormLow2)
+            return run_gemm<128, 128, 2, 2, 4, !F32, AM, BM, F32, KIND>(g, t, stream);
+        if (t.form == kFormMidOnce)  // fp32: the copied planes are read several times
+            return run_gemm<128, 128, 2, 2, 2, !F32, AM, BM, F32, KIND>(g, t, stream);
+    } else if (t.form == kFormLow2) {
+        return run_gemm<128, 128, 2, 2, 4, false, AM, BM, F32, KIND>(g, t, stream);
+    }
+    return run_gemm<128, 128, 2, 2, 2, false, AM, BM, F32, KIND>(g, t, stream);
 }
 
 // The gradients' products, without their addresses: what the workspace's

@@ -432,6 +432,8 @@ struct GemmArgs {
     const uint16_t* b;
     int64_t lda, ldb;          // elements
     int64_t plane_a, plane_b;  // elements between planes
+    int64_t a_width;           // fp32 head read in place: its columns
+    int32_t thin;              // an fp32 head read in place
     int64_t na;                // extent of a: further rows or columns are read as the last ones
     int64_t nb;                // extent of b; a product over tokens: bounded by *count - first
     int64_t k;                 // the sum's length, and for M-major A with na_k its real rows
@@ -442,6 +444,7 @@ struct GemmArgs {
     uint32_t slot_bits;        // log2 of the tiles the card runs at once; 0: sums are not split
     // logits
     float inv_temp;
+    float factor;              // of what goes to out
     float2* part;              // [b][na_blocks]
     int64_t nblk;
     void* p;                   // [b][ldp] bf16 or fp32, or NULL
@@ -454,7 +457,6 @@ struct GemmArgs {
     // outputs
     void* out;                 // final: [row][ldo] of the output's type, or NULL
     int64_t ldo;
-    float factor;              // of what goes to out
     const int32_t* rows;       // row of b, or NULL: b itself
     const float* acc_in;       // fp32 [b][ldf] to add, or NULL
     float* acc_out;            // fp32 [b][ldf], instead of out
@@ -491,6 +493,32 @@ __device__ __forceinline__ void wg_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// Columns [col, col + 4) or [col, col + 8) of a row of `end`, which may start
+// on any element. (Element by element without a loop: one that is not unrolled
+// would put the vector into LDS.)
+__device__ __forceinline__ void store_part(float* row, int64_t col, int64_t end, f32x4 v) {
+    if (col + 4 <= end) {
+        *reinterpret_cast<f32x4_a4*>(row + col) = v;
+        return;
+    }
+    if (col < end) row[col] = v[0];
+    if (col + 1 < end) row[col + 1] = v[1];
+    if (col + 2 < end) row[col + 2] = v[2];
+}
+__device__ __forceinline__ void store_part(uint16_t* row, int64_t col, int64_t end, u32x4 v) {
+    if (col + 8 <= end) {
+        *reinterpret_cast<u32x4_a2*>(row + col) = v;
+        return;
+    }
+    if (col < end) row[col] = uint16_t(v[0]);
+    if (col + 1 < end) row[col + 1] = uint16_t(v[0] >> 16);
+    if (col + 2 < end) row[col + 2] = uint16_t(v[1]);
+    if (col + 3 < end) row[col + 3] = uint16_t(v[1] >> 16);
+    if (col + 4 < end) row[col + 4] = uint16_t(v[2]);
+    if (col + 5 < end) row[col + 5] = uint16_t(v[2] >> 16);
+    if (col + 6 < end) row[col + 6] = uint16_t(v[3]);
 }
 
 // Two neighbouring 16 x 16 tiles of a wave as bf16, eight columns a lane: the
@@ -614,9 +642,146 @@ struct Operand {
     }
 };
 
+// What a product's kernel does with a wave's sums, columns from a_wave and rows
+// from b_wave on.
+template <int KIND, bool F32, int TA, int TB>
+__device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], int64_t a_wave,
+                                       int64_t b_wave, int32_t nb, uint32_t part, uint32_t ns,
+                                       int lane) {
+    static_assert(TA * 16 == kHeadBlock, "a wave's columns are one block");
+    // A lane holds, of each 16 x 16 tile, column lane % 16 (a row of the
+    // output) at rows 4 (lane / 16) + 0..3 (its columns).
+    const int lr = lane % 16, lg = lane / 16;
+    if constexpr (KIND == kLogits) {
+        // the first entry of each of this lane's tokens in this block, all
+        // loads at once
+        int32_t one[TB], e_from[TB], e_to[TB];
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+            const int64_t row = b_wave + b * 16 + lr;
+            one[b] = -1;
+            e_from[b] = e_to[b] = 0;
+            if (row < nb && g.top_pad == 1) one[b] = g.entry[row];
+            if (row < nb && g.top_pad > 1 && a_wave < g.na) {
+                const uint16_t* s = g.start + row * (g.blocks + 1) + a_wave / kHeadBlock;
+                e_from[b] = s[0];
+                e_to[b] = s[1];
+            }
+        }
+        if (g.top_pad > 1) {
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                const int64_t row = b_wave + b * 16 + lr;
+                if (e_from[b] < e_to[b]) one[b] = g.entry[row * g.top_pad + e_from[b]];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+            const int64_t row = b_wave + b * 16 + lr;
+            float m = -__builtin_inff();
+#pragma unroll
+            for (int a = 0; a < TA; ++a)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float l = acc[a][b][k] * g.inv_temp;
+                    if (a_wave + a * 16 + lg * 4 + k >= g.na) l = -__builtin_inff();
+                    acc[a][b][k] = l;
+                    m = fmaxf(m, l);
+                }
+            m = fmaxf(m, __shfl_xor(m, 16));
+            m = fmaxf(m, __shfl_xor(m, 32));
+            const bool real = row < nb;
+            auto take = [&](int32_t k, int32_t e) {
+                const int rel = int(e - a_wave);
+                if (unsigned(rel) >= unsigned(kHeadBlock) || ((rel >> 2) & 3) != lg) return;
+                float l = 0.0f;
+#pragma unroll
+                for (int a = 0; a < TA; ++a)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if ((rel >> 4) == a && (rel & 3) == c) l = acc[a][b][c];
+                g.pick[row * g.top_pad + k] = l;
+            };
+            if (real && g.top_pad == 1) take(0, one[b]);
+            if (g.top_pad > 1 && e_from[b] < e_to[b]) {
+                take(e_from[b], one[b]);
+                for (int32_t k = e_from[b] + 1; k < e_to[b]; ++k)
+                    take(k, g.entry[row * g.top_pad + k]);
+            }
+            // a block without a column of the vocabulary leaves 0
+            const float mm = m == -__builtin_inff() ? 0.0f : m;
+            float s = 0.0f;
+#pragma unroll
+            for (int a = 0; a < TA; ++a)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[a][b][k] = fast_exp(acc[a][b][k] - mm);
+                    s += acc[a][b][k];
+                }
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (lg == 0 && real) g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m, s);
+            if (g.p) {
+                if constexpr (F32) {
+                    float* out = static_cast<float*>(g.p) + row * g.ldp + a_wave + lg * 4;
+#pragma unroll
+                    for (int a = 0; a < TA; ++a)
+                        *reinterpret_cast<f32x4*>(out + a * 16) = acc[a][b];
+                } else {
+                    uint16_t* out = static_cast<uint16_t*>(g.p) + row * g.ldp + a_wave;
+#pragma unroll
+                    for (int a = 0; a < TA; a += 2)
+                        *reinterpret_cast<u32x4*>(out + a * 16 + pair_column(lg)) =
+                            pair_of(acc[a][b], acc[a + 1][b]);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+            const int64_t row = b_wave + b * 16 + lr;
+            if (row >= nb) continue;  // the same for the lanes of a column of rows
+            if (ns > 1 || g.acc_in || g.acc_out) {
+                float* out = ns > 1 ? g.split + part * (int64_t(nb) * g.ldf) : g.acc_out;
+#pragma unroll
+                for (int a = 0; a < TA; ++a) {
+                    const int64_t col = a_wave + a * 16 + lg * 4;
+                    if (col >= g.na) continue;
+                    const int64_t at = row * g.ldf + col;
+                    if (ns == 1 && g.acc_in)
+                        acc[a][b] += *reinterpret_cast<const f32x4*>(g.acc_in + at);
+                    if (out) *reinterpret_cast<f32x4*>(out + at) = acc[a][b];
+                }
+                if (out) continue;
+            }
+            const int64_t at = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo;
+#pragma unroll
+            for (int a = 0; a < TA; ++a) acc[a][b] *= g.factor;
+            if constexpr (F32) {
+                float* out = static_cast<float*>(g.out) + at;
+#pragma unroll
+                for (int a = 0; a < TA; ++a) {
+                    const int64_t col = a_wave + a * 16 + lg * 4;
+                    store_part(out, col, g.ldo, acc[a][b]);
+                }
+            } else {
+                uint16_t* out = static_cast<uint16_t*>(g.out) + at;
+#pragma unroll
+                for (int a = 0; a < TA; a += 2) {
+                    const u32x4 v = pair_of(acc[a][b], acc[a + 1][b]);
+                    const int64_t col = a_wave + a * 16 + pair_column(lg);
+                    store_part(out, col, g.ldo, v);
+                }
+            }
+        }
+    }
+}
+
 // The products of fp32 planes, the largest first.
 __device__ __forceinline__ int plane_a_of(int seg) { return (0x201010 >> (4 * seg)) & 0xf; }
 __device__ __forceinline__ int plane_b_of(int seg) { return (0x021100 >> (4 * seg)) & 0xf; }
+
+constexpr uint32_t kThinSegs = 2;  // stages of 32 in a step of 64 k's
 
 template <int BA, int BB, int WA, int WB, int NST, bool NT, bool AM, bool BM, bool F32, int KIND>
 __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
@@ -693,9 +858,9 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
                          F32 ? plane_b_of(i_seg) * g.plane_b : 0, k0, 0, wave);
         }
         // past the last stage it is loaded again: nothing reads it
-        if (to == kPer && --i_left > 0 && ++i_kt == nkt) {
-            i_kt = 0;
-            ++i_seg;
+        if (to == kPer && --i_left > 0 && ++i_seg == kSegs) {
+            i_seg = 0;
+            ++i_kt;
         }
     };
     // Stage s is read from buffer s % NST. Its first half of the k's is read into
@@ -751,146 +916,152 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     }
     wait_stage<0>();  // no load into LDS outlives the workgroup
 
-    // A lane holds, of each 16 x 16 tile, column lane % 16 (a row of the
-    // output) at rows 4 (lane / 16) + 0..3 (its columns).
-    const int lr = lane % 16, lg = lane / 16;
-    const int64_t a_wave = a0 + wa * EA;
-    if constexpr (KIND == kLogits) {
-        // the first entry of each of this lane's tokens in this block, all
-        // loads at once
-        int32_t one[TB], e_from[TB], e_to[TB];
+    finish<KIND, F32, TA, TB>(g, acc, a0 + wa * EA, b0 + wb * EB, nb, part, ns, lane);
+}
+
+// Few tokens and an fp32 head: the head is read in place, once for each
+// product, and split into planes on its way from LDS to the matrix cores (4
+// bytes an element; copied as planes first it would be 10, and 12 more for
+// each product). A workgroup takes 256 rows (columns) of the head, four waves
+// of 64; 16 TB tokens; stages of 32 k's. An infinity in the head comes out as
+// NaN. 24 tokens x 66306 x 4224 with the gradient of hidden: 1570 us with the
+// planes copied, 590 this way.
+template <int TB, bool AM, int KIND>
+__global__ __launch_bounds__(256) void thin_kernel(GemmArgs g) {
+    constexpr int BA = 256, BB = 16 * TB, TA = 4, BK = 32, NST = TB == 4 ? 3 : 4;
+    constexpr int kABytes = BA * BK * 4, kStage = kABytes + 3 * BB * BK * 2;
+    constexpr int kALoads = kABytes / 1024 / 4, kBLoads = (3 * TB + 3) / 4;
+    constexpr int kPer = kALoads + kBLoads;
+    __shared__ __attribute__((aligned(1024))) char s_mem[NST * kStage];
+    const int lane = threadIdx.x % 64, lr = lane % 16, lg = lane / 16;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+
+    const int32_t nb = min(int32_t(g.nb), max(*g.count - int32_t(g.first), 0));
+    const uint32_t tiles = nb > 0 ? uint32_t(g.na + BA - 1) / BA : 0;
+    const uint32_t kt_all = uint32_t(g.k + kHeadDepth - 1) / kHeadDepth;
+    const uint32_t ns =
+        __builtin_amdgcn_readfirstlane(split_of(tiles, kt_all, kThinSegs, g.slot_bits));
+    const uint32_t items = tiles * ns, per = (items + 7) / 8;
+    const uint32_t j = blockIdx.x >> 3, item = (blockIdx.x & 7) * per + j;
+    if (j >= per || item >= items) return;
+    const uint32_t part = __builtin_amdgcn_readfirstlane(item / tiles), tile = item - part * tiles;
+    const int64_t a0 = int64_t(tile) * BA;
+    const uint32_t kt0 = kt_all * part / ns, kt1 = kt_all * (part + 1) / ns;
+    const int nkt = int(kt1 - kt0), steps = nkt * kThinSegs;
+    const int k_turn = !AM && nkt > 0 ? int(tile * 3 % nkt) : 0;  // as in gemm_kernel
+
+    const float* head = reinterpret_cast<const float*>(g.a);
+    const int32_t width = int32_t(g.a_width);
+    uint32_t a_off[kALoads];
+    int32_t a_k[kALoads];
 #pragma unroll
-        for (int b = 0; b < TB; ++b) {
-            const int64_t row = b0 + wb * EB + b * 16 + lr;
-            one[b] = -1;
-            e_from[b] = e_to[b] = 0;
-            if (row < nb && g.top_pad == 1) one[b] = g.entry[row];
-            if (row < nb && g.top_pad > 1 && a_wave < g.na) {
-                const uint16_t* s = g.start + row * (g.blocks + 1) + a_wave / kHeadBlock;
-                e_from[b] = s[0];
-                e_to[b] = s[1];
-            }
-        }
-        if (g.top_pad > 1) {
-#pragma unroll
-            for (int b = 0; b < TB; ++b) {
-                const int64_t row = b0 + wb * EB + b * 16 + lr;
-                if (e_from[b] < e_to[b]) one[b] = g.entry[row * g.top_pad + e_from[b]];
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < TB; ++b) {
-            const int64_t row = b0 + wb * EB + b * 16 + lr;
-            float m = -__builtin_inff();
-#pragma unroll
-            for (int a = 0; a < TA; ++a)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float l = acc[a][b][k] * g.inv_temp;
-                    if (a_wave + a * 16 + lg * 4 + k >= g.na) l = -__builtin_inff();
-                    acc[a][b][k] = l;
-                    m = fmaxf(m, l);
-                }
-            m = fmaxf(m, __shfl_xor(m, 16));
-            m = fmaxf(m, __shfl_xor(m, 32));
-            const bool real = row < nb;
-            auto take = [&](int32_t k, int32_t e) {
-                const int rel = int(e - a_wave);
-                if (unsigned(rel) >= unsigned(EA) || ((rel >> 2) & 3) != lg) return;
-                float l = 0.0f;
-#pragma unroll
-                for (int a = 0; a < TA; ++a)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if ((rel >> 4) == a && (rel & 3) == c) l = acc[a][b][c];
-                g.pick[row * g.top_pad + k] = l;
-            };
-            if (real && g.top_pad == 1) take(0, one[b]);
-            if (g.top_pad > 1 && e_from[b] < e_to[b]) {
-                take(e_from[b], one[b]);
-                for (int32_t k = e_from[b] + 1; k < e_to[b]; ++k)
-                    take(k, g.entry[row * g.top_pad + k]);
-            }
-            // a block without a column of the vocabulary leaves 0
-            const float mm = m == -__builtin_inff() ? 0.0f : m;
-            float s = 0.0f;
-#pragma unroll
-            for (int a = 0; a < TA; ++a)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[a][b][k] = fast_exp(acc[a][b][k] - mm);
-                    s += acc[a][b][k];
-                }
-            s += __shfl_xor(s, 16);
-            s += __shfl_xor(s, 32);
-            if (lg == 0 && real) g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m, s);
-            if (g.p) {
-                if constexpr (F32) {
-                    float* out = static_cast<float*>(g.p) + row * g.ldp + a_wave + lg * 4;
-#pragma unroll
-                    for (int a = 0; a < TA; ++a)
-                        *reinterpret_cast<f32x4*>(out + a * 16) = acc[a][b];
-                } else {
-                    uint16_t* out = static_cast<uint16_t*>(g.p) + row * g.ldp + a_wave;
-#pragma unroll
-                    for (int a = 0; a < TA; a += 2)
-                        *reinterpret_cast<u32x4*>(out + a * 16 + pair_column(lg)) =
-                            pair_of(acc[a][b], acc[a + 1][b]);
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int b = 0; b < TB; ++b) {
-            const int64_t row = b0 + wb * EB + b * 16 + lr;
-            if (row >= nb) continue;  // the same for the lanes of a column of rows
-            if (ns > 1 || g.acc_in || g.acc_out) {
-                float* out = ns > 1 ? g.split + part * (int64_t(nb) * g.ldf) : g.acc_out;
-#pragma unroll
-                for (int a = 0; a < TA; ++a) {
-                    const int64_t col = a_wave + a * 16 + lg * 4;
-                    if (col >= g.na) continue;
-                    const int64_t at = row * g.ldf + col;
-                    if (ns == 1 && g.acc_in)
-                        acc[a][b] += *reinterpret_cast<const f32x4*>(g.acc_in + at);
-                    if (out) *reinterpret_cast<f32x4*>(out + at) = acc[a][b];
-                }
-                if (out) continue;
-            }
-            const int64_t at = (g.rows ? int64_t(g.rows[row]) : row) * g.ldo;
-#pragma unroll
-            for (int a = 0; a < TA; ++a) acc[a][b] *= g.factor;
-            if constexpr (F32) {
-                float* out = static_cast<float*>(g.out) + at;
-#pragma unroll
-                for (int a = 0; a < TA; ++a) {
-                    const int64_t col = a_wave + a * 16 + lg * 4;
-                    if (col + 4 <= g.ldo) {
-                        *reinterpret_cast<f32x4_a4*>(out + col) = acc[a][b];
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (col + k < g.ldo) out[col + k] = acc[a][b][k];
-                    }
-                }
-            } else {
-                uint16_t* out = static_cast<uint16_t*>(g.out) + at;
-#pragma unroll
-                for (int a = 0; a < TA; a += 2) {
-                    const u32x4 v = pair_of(acc[a][b], acc[a + 1][b]);
-                    const int64_t col = a_wave + a * 16 + pair_column(lg);
-                    if (col + 8 <= g.ldo) {
-                        *reinterpret_cast<u32x4_a2*>(out + col) = v;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (col + k < g.ldo)
-                                out[col + k] = uint16_t(v[k / 2] >> (16 * (k % 2)));
-                    }
-                }
-            }
+    for (int i = 0; i < kALoads; ++i) {
+        const int q = (wave * kALoads + i) * 64 + lane;
+        if constexpr (AM) {  // rows of 256 columns, 64 groups of 4
+            const int k = q / 64, c = (q % 64) ^ (((k >> 3) & 3) * 4);
+            a_k[i] = k;
+            a_off[i] = uint32_t(min(int32_t(a0) + c * 4, width - 4) - int32_t(a0)) * 4;
+        } else {             // rows of 32 k's, 8 groups of 4
+            const int r = q / 8, c = (q % 8) ^ ((r >> 1) & 7);
+            a_k[i] = c * 4;
+            a_off[i] = uint32_t(min(a0 + r, g.na - 1) - a0) * uint32_t(g.lda) * 4;
         }
     }
+    int next = 0;  // the stage to load
+    auto issue = [&](int buf) {
+        ZSP_LDS char* lds = (ZSP_LDS char*)s_mem + buf * kStage;
+        int kt = next / kThinSegs;
+        kt = kt + k_turn < nkt ? kt + k_turn : kt + k_turn - nkt;
+        const int64_t k0 = int64_t(int(kt0) + kt) * kHeadDepth + next % kThinSegs * BK;
+        // half a step may lie behind the head's last row
+        const int64_t k_last = g.k_real - 1, k_base = k0 < k_last ? k0 : k_last;
+        const char* base = reinterpret_cast<const char*>(AM ? head + k_base * g.lda + a0
+                                                            : head + a0 * g.lda);
+#pragma unroll
+        for (int i = 0; i < kALoads; ++i) {
+            uint32_t o = a_off[i];
+            if constexpr (AM)  // rows past the head's last are read as that one
+                o += uint32_t(min(k0 + a_k[i], k_last) - k_base) * uint32_t(g.lda) * 4;
+            else               // columns past a row's last four as those
+                o += uint32_t(min(int32_t(k0) + a_k[i], width - 4)) * 4;
+            load_to_lds<true>(base, o, lds + (wave * kALoads + i) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < kBLoads; ++i) {
+            const int load = min(wave * kBLoads + i, 3 * TB - 1);
+            const int r = lane / 4, c = (lane % 4) ^ ((r >> 2) & 3);
+            const uint16_t* b = g.b + load / TB * g.plane_b + load % TB * 16 * g.ldb + k0;
+            load_to_lds<false>(reinterpret_cast<const char*>(b),
+                               uint32_t(r) * uint32_t(g.ldb) * 2 + c * 16,
+                               lds + kABytes + load * 1024);
+        }
+        if (next + 1 < steps) ++next;  // past the last stage it is loaded again: nothing reads it
+    };
+    f32x4 acc[TA][TB];
+#pragma unroll
+    for (int i = 0; i < TA; ++i)
+#pragma unroll
+        for (int k = 0; k < TB; ++k) acc[i][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (steps > 0)
+        for (int i = 0; i < NST - 1; ++i) issue(i);
+    int buf = 0, into = NST - 1;
+    for (int it = 0; it < steps; ++it) {
+        wait_stage<(NST - 2) * kPer>();
+        wg_barrier();
+        issue(into);
+        into = into + 1 == NST ? 0 : into + 1;
+        ZSP_LDS const char* la = (ZSP_LDS const char*)s_mem + buf * kStage;
+        ZSP_LDS const char* lb = la + kABytes;
+        buf = buf + 1 == NST ? 0 : buf + 1;
+        bf16x8 fb[3][TB];
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int b = 0; b < TB; ++b)
+                fb[p][b] = *(ZSP_LDS const bf16x8*)(lb + (p * TB + b) * 1024 + lr * 64 +
+                                                    (lg ^ ((lr >> 2) & 3)) * 16);
+#pragma unroll
+        for (int i = 0; i < TA; ++i) {
+            float x[8];
+            if constexpr (AM) {
+                const int a = wave * 64 + i * 16 + lr;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x[k] = *(ZSP_LDS const float*)(la + (lg * 8 + k) * 1024 +
+                                                   ((a >> 2) ^ (lg * 4)) * 16 + (a & 3) * 4);
+            } else {
+                const int row = wave * 64 + i * 16 + lr;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 v = *(ZSP_LDS const f32x4*)(la + row * 128 +
+                                                            ((2 * lg + h) ^ (lr >> 1)) * 16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[h * 4 + k] = v[k];
+                }
+            }
+            u32x4 plane[3];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float lo = x[2 * k], hi = x[2 * k + 1];
+#pragma unroll
+                for (int p = 0; p < 3; ++p) {
+                    const uint32_t u = bf16_pair(lo, hi);
+                    plane[p][k] = u;
+                    lo -= __uint_as_float(u << 16);
+                    hi -= __uint_as_float(u & 0xffff0000u);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 6; ++q)
+#pragma unroll
+                for (int b = 0; b < TB; ++b)
+                    acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, plane[plane_a_of(q)]), fb[plane_b_of(q)][b],
+                        acc[i][b], 0, 0, 0);
+        }
+    }
+    wait_stage<0>();  // no load into LDS outlives the workgroup
+    finish<KIND, true, TA, TB>(g, acc, a0 + wave * 64, 0, nb, part, ns, lane);
 }
 
 // ---- the softmax joined, the losses, G ------------------------------------------------
@@ -1242,13 +1413,7 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a) {
                 const u32x4 v = pair_of(acc[i] * a.factor, acc[i + 1] * a.factor);
                 const int64_t col = c0 + i * 16 + pair_column(lg);
                 if (row >= a.v) continue;
-                if (col + 8 <= a.d) {
-                    *reinterpret_cast<u32x4_a2*>(out + col) = v;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (col + k < a.d) out[col + k] = uint16_t(v[k / 2] >> (16 * (k % 2)));
-                }
+                store_part(out, col, a.d, v);
             }
         }
     }
@@ -1339,10 +1504,11 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 
 // A product's tiles: columns and rows of a tile, how many the card runs at once
 // (log2), and which form.
-enum Form { kFormBig, kFormMid, kFormMidOnce, kFormLow, kFormLow2 };
+enum Form { kFormBig, kFormMid, kFormMidOnce, kFormLow, kFormLow2, kFormThin };
 struct TileShape {
     uint32_t ba, bb, slot_bits;
     Form form;
+    uint32_t segs = 1;  // stages of a step of 64 k's
 };
 constexpr TileShape kBig{256, 256, 8, kFormBig}, kMid{128, 128, 9, kFormMid},
     kMidOnce{128, 128, 9, kFormMidOnce}, kLow{128, 64, 8, kFormLow},
@@ -1353,12 +1519,12 @@ constexpr TileShape kBig{256, 256, 8, kFormBig}, kMid{128, 128, 9, kFormMid},
 struct Bound {
     uint64_t items = 0, split_rows = 0;
 };
-Bound bound_of(const GemmArgs& g, TileShape t, uint32_t segs) {
+Bound bound_of(const GemmArgs& g, TileShape t) {
     Bound m;
     const uint32_t ta = uint32_t((g.na + t.ba - 1) / t.ba), tb = uint32_t((g.nb + t.bb - 1) / t.bb);
     const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
     auto one = [&](uint32_t b, uint32_t k) {
-        const uint32_t s = split_of(ta * b, k, segs, g.slot_bits ? t.slot_bits : 0);
+        const uint32_t s = split_of(ta * b, k, t.segs, g.slot_bits ? t.slot_bits : 0);
         m.items = std::max<uint64_t>(m.items, uint64_t(ta) * b * s);
         if (s > 1)
             m.split_rows = std::max<uint64_t>(m.split_rows,
@@ -1377,24 +1543,42 @@ Bound bound_of(const GemmArgs& g, TileShape t, uint32_t segs) {
     return m;
 }
 
-template <int BA, int BB, int WA, int WB, int NST, bool NT, bool AM, bool BM, bool F32, int KIND>
-hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
-    static_assert(BA <= kHeadTile && BB <= kHeadTile, "");
-    if (g.slot_bits) g.slot_bits = t.slot_bits;
-    const Bound m = bound_of(g, t, F32 ? 6 : 1);
-    if (m.items == 0) return hipSuccess;
-    gemm_kernel<BA, BB, WA, WB, NST, NT, AM, BM, F32, KIND>
-        <<<uint32_t((m.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
-    hipError_t e = hipGetLastError();
+// The parts of a split product joined, unless the caller does it.
+template <bool F32, int KIND>
+hipError_t join_parts(const GemmArgs& g, TileShape t, const Bound& m, hipError_t e,
+                      hipStream_t stream) {
     if constexpr (KIND == kOut) {
         if (e == hipSuccess && m.split_rows && !g.keep_parts) {
-            SplitArgs q{g, t.ba, t.bb, F32 ? 6u : 1u, uint32_t((g.ldo + 1023) / 1024)};
+            SplitArgs q{g, t.ba, t.bb, t.segs, uint32_t((g.ldo + 1023) / 1024)};
             const int64_t rows = g.nb * q.parts;
             split_kernel<F32><<<uint32_t(std::min<int64_t>(rows, 4096)), 256, 0, stream>>>(q);
             e = hipGetLastError();
         }
     }
     return e;
+}
+
+template <int BA, int BB, int WA, int WB, int NST, bool NT, bool AM, bool BM, bool F32, int KIND>
+hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
+    static_assert(BA <= kHeadTile && BB <= kHeadTile, "");
+    if (g.slot_bits) g.slot_bits = t.slot_bits;
+    const Bound m = bound_of(g, t);
+    if (m.items == 0) return hipSuccess;
+    gemm_kernel<BA, BB, WA, WB, NST, NT, AM, BM, F32, KIND>
+        <<<uint32_t((m.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
+    return join_parts<F32, KIND>(g, t, m, hipGetLastError(), stream);
+}
+
+template <bool AM, int KIND>
+hipError_t run_thin(GemmArgs g, TileShape t, hipStream_t stream) {
+    if (g.slot_bits) g.slot_bits = t.slot_bits;
+    const Bound m = bound_of(g, t);
+    if (m.items == 0) return hipSuccess;
+    const uint32_t grid = uint32_t((m.items + 7) / 8 * 8);
+    if (t.bb == 16) thin_kernel<1, AM, KIND><<<grid, 256, 0, stream>>>(g);
+    else if (t.bb == 32) thin_kernel<2, AM, KIND><<<grid, 256, 0, stream>>>(g);
+    else thin_kernel<4, AM, KIND><<<grid, 256, 0, stream>>>(g);
+    return join_parts<true, KIND>(g, t, m, hipGetLastError(), stream);
 }
 
 // Tiles of 256 x 256 (eight waves, one workgroup on a CU) reach 1.3 PFLOP/s
@@ -1406,7 +1590,11 @@ hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
 // the head's gradient, which they can hold instead until it is written
 // (32000 x 4096 of 5 tokens 46.8 -> 42.3 us alone; 17 tokens with gradients
 // 198 -> 175).
-TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
+TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
+    if (g.thin) {
+        const uint32_t bb = g.nb <= 16 ? 16 : g.nb <= 32 ? 32 : 64;
+        return {256, bb, 8, kFormThin, kThinSegs};
+    }
     if (low && g.tokens_in_b && g.nb <= 64) return kLow;
     const bool few = low && g.tokens_in_b && g.nb <= 128;
     if (few && !g.slot_bits) return kLow2;
@@ -1428,9 +1616,17 @@ TileShape tile_of(const GemmArgs& g, uint32_t segs, bool low) {
     return few ? kMidOnce : kMid;
 }
 
+TileShape tile_of(const GemmArgs& g, bool f32, bool low) {
+    TileShape t = shape_of(g, f32 ? 6 : 1, low);
+    if (t.form != kFormThin) t.segs = f32 ? 6 : 1;
+    return t;
+}
+
 template <bool AM, bool BM, bool F32, int KIND>
 hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
-    const TileShape t = tile_of(g, F32 ? 6 : 1, !BM);
+    const TileShape t = tile_of(g, F32, !BM);
+    if constexpr (F32 && !BM)
+        if (t.form == kFormThin) return run_thin<AM, KIND>(g, t, stream);
     if (t.form == kFormBig)
         return run_gemm<256, 256, 4, 2, 2, false, AM, BM, F32, KIND>(g, t, stream);
     if constexpr (!BM) {
@@ -1450,7 +1646,9 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
 // size is asked of.
 GemmArgs hidden_product(const HeadShape& s, int64_t len) {
     GemmArgs h{};
-    h.lda = s.dp;
+    h.thin = s.thin;
+    h.a_width = s.d;
+    h.lda = s.thin ? s.d : s.dp;
     h.ldb = s.vp;
     h.plane_a = s.v * s.dp;
     h.plane_b = s.chunk * s.vp;
@@ -1466,7 +1664,10 @@ GemmArgs hidden_product(const HeadShape& s, int64_t len) {
 }
 GemmArgs raw_product(const HeadShape& s, int64_t len) {
     GemmArgs h{};
-    h.lda = h.ldb = s.dp;
+    h.thin = s.thin;
+    h.a_width = s.d;
+    h.lda = s.thin ? s.d : s.dp;
+    h.ldb = s.dp;
     h.plane_a = s.v * s.dp;
     h.plane_b = s.rows * s.dp;
     h.na = s.v;
@@ -1569,7 +1770,10 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         GemmArgs l{};
         l.a = w;
         l.b = x + first * s.dp;
-        l.lda = l.ldb = s.dp;
+        l.thin = s.thin;
+        l.a_width = s.d;
+        l.lda = s.thin ? s.d : s.dp;
+        l.ldb = s.dp;
         l.plane_a = w_plane;
         l.plane_b = x_plane;
         l.na = s.v;
@@ -1596,12 +1800,12 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.first = first;
             h.split = h.acc_out = split;
             h.keep_parts = 1;
-            const TileShape t = tile_of(h, F32 ? 6 : 1, true);
+            const TileShape t = tile_of(h, F32, true);
             if ((e = pick_gemm<false, false, F32, kOut>(h, stream)) != hipSuccess) return e;
             JoinArgs j{nullptr, 0, blocks, count, first, rows + first, coef + first, l.entry,
                        nullptr, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
                        c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
-            RawArgs q{j, split, s.v, s.dp, len, t.ba, t.bb, F32 ? 6u : 1u, t.slot_bits};
+            RawArgs q{j, split, s.v, s.dp, len, t.ba, t.bb, t.segs, t.slot_bits};
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
             raw_join_kernel<F32><<<uint32_t(grads ? pad : len), 256, s.v * 4, stream>>>(q);
             if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1663,19 +1867,17 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
 bool head_is_raw(const HeadShape& s) {
     if (s.n == 0 || s.v > kHeadRawColumns || s.nchunk > 1) return false;
     const GemmArgs h = raw_product(s, s.n);
-    const uint32_t segs = s.f32 ? 6 : 1;
-    const TileShape t = tile_of(h, segs, true);
+    const TileShape t = tile_of(h, s.f32, true);
     const uint32_t tiles = uint32_t((h.na + t.ba - 1) / t.ba) * uint32_t((h.nb + t.bb - 1) / t.bb);
-    return split_of(tiles, uint32_t(h.k) / kHeadDepth, segs, t.slot_bits) > 1;
+    return split_of(tiles, uint32_t(h.k) / kHeadDepth, t.segs, t.slot_bits) > 1;
 }
 
 int64_t head_split_bytes(const HeadShape& s) {
-    const uint32_t segs = s.f32 ? 6 : 1;
     int64_t bytes = 0;
     for (int64_t ch = 0; ch < s.nchunk; ++ch) {
         const int64_t len = std::min(s.chunk, s.n - ch * s.chunk);
         auto add = [&](const GemmArgs& h, bool low, int64_t rows) {
-            const Bound m = bound_of(h, tile_of(h, segs, low), segs);
+            const Bound m = bound_of(h, tile_of(h, s.f32, low));
             bytes = std::max(bytes, std::max(int64_t(m.split_rows), rows) * h.ldf * 4);
         };
         if (s.raw && len > 0) add(raw_product(s, len), true, len);

@@ -16,6 +16,7 @@ constexpr int32_t kHeadBlock = 64;       // vocabulary columns per partial of a 
 constexpr int32_t kHeadDepth = 64;       // d is padded to it
 constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
 constexpr int32_t kHeadFew = 128;        // tokens whose gradient of the head has a way of its own
+constexpr int32_t kHeadThin = 64;        // tokens that read an fp32 head in place
 constexpr int32_t kHeadRawColumns = 8192;  // logits of a token that a workgroup keeps in LDS
 
 // Sizes of a call, and the byte offsets of its parts of the workspace.
@@ -24,6 +25,7 @@ struct HeadShape {
     int32_t top = 1;              // entries per token (a target is one)
     bool f32 = false, teacher = false;
     bool grad_hidden = false, grad_head = false;
+    bool thin = false;            // an fp32 head is read in place by few tokens
     bool pack_head = false;       // the head is copied: fp32, d or its address not aligned
     bool raw = false;             // logits summed in parts, in the workspace
     int32_t planes = 1;           // bf16 planes of an operand: 3 hold an fp32 value

@@ -514,8 +514,8 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * that make the gradients; scale * T comes to their sums in fp32. Equal inputs give equal bits.
  *   0 <= n <= 2^24 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024.
  * Pointers need the alignment of their element type only, ws 16 bytes; a head
- * on 16 bytes whose d is a multiple of 64 is read in place (bf16), any other is
- * copied into the workspace first. No plan is involved: all tensors are on
+ * on 16 bytes whose d is a multiple of 8 is read in place (fp32: of 4, by up to
+ * 64 tokens), any other is copied into the workspace first. No plan is involved: all tensors are on
  * the current device. Nothing is waited for, copied by the host or allocated,
  * so calls can be captured into a HIP graph. A workspace's contents mean
  * nothing between calls; calls that may run at the same time, replays of

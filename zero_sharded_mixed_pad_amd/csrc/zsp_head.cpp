@@ -43,7 +43,7 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.dp = up(d, kHeadDepth);
     const bool aligned = !(flags & ZSP_HEAD_UNALIGNED);
     s.thin = s.f32 && n <= kHeadThin && d % 4 == 0 && aligned;
-    s.pack_head = s.f32 ? !s.thin : d % kHeadDepth != 0 || !aligned;
+    s.pack_head = s.f32 ? !s.thin : d % 8 != 0 || !aligned;
     const bool grads = s.grad_hidden || s.grad_head;
     // per token: P (and its planes), or the partials alone
     const int64_t per = grads ? s.vp * (s.f32 ? 4 + 2 * s.planes : 2) : s.vp / kHeadBlock * 8;

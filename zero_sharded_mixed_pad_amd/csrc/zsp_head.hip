@@ -432,12 +432,12 @@ struct GemmArgs {
     const uint16_t* b;
     int64_t lda, ldb;          // elements
     int64_t plane_a, plane_b;  // elements between planes
-    int64_t a_width;           // fp32 head read in place: its columns
+    int64_t a_width;           // columns of A's rows as they lie in memory
     int32_t thin;              // an fp32 head read in place
     int64_t na;                // extent of a: further rows or columns are read as the last ones
     int64_t nb;                // extent of b; a product over tokens: bounded by *count - first
     int64_t k;                 // the sum's length, and for M-major A with na_k its real rows
-    int64_t k_real;            // rows of an M-major A that exist (later ones read as the last)
+    int64_t k_real;            // k's of the head that exist (later ones are read as the last)
     const int32_t* count;      // tokens that count
     int64_t first;             // the chunk's first token
     int32_t tokens_in_b, tokens_in_k;
@@ -585,7 +585,7 @@ struct Operand {
     const char* base;         // of the tile's first row (M-major: column)
     int64_t ld;               // bytes
     uint32_t off[kLoads];     // bytes from base; M-major: of the first row
-    int32_t krow[kLoads];     // M-major
+    int32_t krow[kLoads];     // the row, K-major: the group's first k
 
     __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int64_t x0, int64_t nx,
                                          int wave, int lane) {
@@ -603,20 +603,22 @@ struct Operand {
             } else {
                 const int r = q / (BK / 8), c = (q % (BK / 8)) ^ k_swizzle(r);
                 const int64_t x = x0 + r < nx ? r : nx - 1 - x0;
-                off[i] = uint32_t(x * ld + c * 16);
-                krow[i] = 0;
+                off[i] = uint32_t(x * ld + (CLAMP ? 0 : c * 16));
+                krow[i] = c * 8;
             }
         }
     }
-    // Load i of the stage whose first k is k0 into `lds`. CLAMP: rows past
-    // k_last are read as that one.
+    // Load i of the stage whose first k is k0 into `lds`. CLAMP: rows (K-major:
+    // groups of 8 k's) past k_last are read as that one.
     __device__ __forceinline__ void issue(int i, ZSP_LDS char* lds, int64_t plane, int64_t k0,
                                           int64_t k_last, int wave) {
-        const char* src = base + 2 * plane + (MMAJ ? k0 * ld : k0 * 2);
+        const char* src = base + 2 * plane + (MMAJ ? k0 * ld : CLAMP ? 0 : k0 * 2);
         uint32_t o = off[i];
-        if constexpr (CLAMP) {
+        if constexpr (CLAMP && MMAJ) {
             const int32_t k = k_last - k0 < BK ? int32_t(k_last - k0) : BK;
             o += uint32_t(krow[i] < k ? krow[i] : k) * uint32_t(ld);
+        } else if constexpr (CLAMP) {
+            o += uint32_t(min(int32_t(k0) + krow[i], int32_t(k_last) - 7)) * 2;
         }
         load_to_lds<NT>(src, o, lds + (wave * kLoads + i) * 1024);
     }
@@ -788,7 +790,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
     constexpr int kWaves = WA * WB, BK = kHeadDepth;
     constexpr int EA = BA / WA, EB = BB / WB, TA = EA / 16, TB = EB / 16;
     static_assert(EA == kHeadBlock && TA == 4, "a wave's columns are one block");
-    using OpA = Operand<BA, BK, kWaves, AM, AM && !BM, NT>;  // the head's rows end at v
+    using OpA = Operand<BA, BK, kWaves, AM, !BM, NT>;  // the head ends at v and d
     using OpB = Operand<BB, BK, kWaves, BM, false, false>;
     constexpr int kStage = OpA::kBytes + OpB::kBytes;
     constexpr int kPer = OpA::kLoads + OpB::kLoads;
@@ -840,7 +842,7 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 
     OpA oa;
     OpB ob;
-    oa.init(g.a, g.lda, a0, g.na, wave, lane);
+    oa.init(g.a, g.lda, a0, AM ? g.a_width : g.na, wave, lane);
     ob.init(g.b, g.ldb, b0, BM ? g.ldb : (b0 + BB), wave, lane);
 
     int i_kt = 0, i_seg = 0, i_left = steps;  // the next stage to load
@@ -925,10 +927,10 @@ __global__ __launch_bounds__(64 * WA * WB) void gemm_kernel(GemmArgs g) {
 // each product). A workgroup takes 256 rows (columns) of the head, four waves
 // of 64; 16 TB tokens; stages of 32 k's. An infinity in the head comes out as
 // NaN. 24 tokens x 66306 x 4224 with the gradient of hidden: 1570 us with the
-// planes copied, 590 this way.
+// planes copied, 510 this way.
 template <int TB, bool AM, int KIND>
 __global__ __launch_bounds__(256) void thin_kernel(GemmArgs g) {
-    constexpr int BA = 256, BB = 16 * TB, TA = 4, BK = 32, NST = TB == 4 ? 3 : 4;
+    constexpr int BA = 256, BB = 16 * TB, TA = 4, BK = 32, NST = TB == 4 ? 3 : 2;
     constexpr int kABytes = BA * BK * 4, kStage = kABytes + 3 * BB * BK * 2;
     constexpr int kALoads = kABytes / 1024 / 4, kBLoads = (3 * TB + 3) / 4;
     constexpr int kPer = kALoads + kBLoads;
@@ -1303,13 +1305,29 @@ __global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
     const int64_t stride = int64_t(min(int64_t(count), q.len)) * a.ldp;
     const float* raw = q.raw + r * a.ldp;
     float m = -__builtin_inff();
-    for (int c = t; c < v; c += 256) {
-        float l = 0.0f;
-#pragma unroll 4
-        for (uint32_t s = 0; s < ns; ++s) l += raw[s * stride + c];
-        l *= a.inv_temp;
-        s_l[c] = l;
-        m = nan_max(m, l);
+    for (int c0 = t; c0 < v; c0 += 1024) {
+        float l[4] = {0.f, 0.f, 0.f, 0.f};
+        for (uint32_t s = 0; s < ns; s += 4) {
+            float q[4][4];  // all on their way before the first is added
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[k][i] = raw[min(s + k, ns - 1) * stride + min(c0 + i * 256, v - 1)];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (s + k < ns) l[i] += q[k][i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * 256;
+            if (c >= v) break;
+            l[i] *= a.inv_temp;
+            s_l[c] = l[i];
+            m = nan_max(m, l[i]);
+        }
     }
     m = block_max(m, s_f);
     float part = 0.0f;
@@ -1593,7 +1611,8 @@ hipError_t run_thin(GemmArgs g, TileShape t, hipStream_t stream) {
 TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (g.thin) {
         const uint32_t bb = g.nb <= 16 ? 16 : g.nb <= 32 ? 32 : 64;
-        return {256, bb, 8, kFormThin, kThinSegs};
+        // two workgroups a CU, or one where 64 tokens leave no room for them
+        return {256, bb, bb == 64 ? 8u : 9u, kFormThin, kThinSegs};
     }
     if (low && g.tokens_in_b && g.nb <= 64) return kLow;
     const bool few = low && g.tokens_in_b && g.nb <= 128;
@@ -1647,8 +1666,7 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
 GemmArgs hidden_product(const HeadShape& s, int64_t len) {
     GemmArgs h{};
     h.thin = s.thin;
-    h.a_width = s.d;
-    h.lda = s.thin ? s.d : s.dp;
+    h.a_width = h.lda = s.pack_head ? s.dp : s.d;
     h.ldb = s.vp;
     h.plane_a = s.v * s.dp;
     h.plane_b = s.chunk * s.vp;
@@ -1665,14 +1683,14 @@ GemmArgs hidden_product(const HeadShape& s, int64_t len) {
 GemmArgs raw_product(const HeadShape& s, int64_t len) {
     GemmArgs h{};
     h.thin = s.thin;
-    h.a_width = s.d;
-    h.lda = s.thin ? s.d : s.dp;
+    h.a_width = h.lda = s.pack_head ? s.dp : s.d;
     h.ldb = s.dp;
     h.plane_a = s.v * s.dp;
     h.plane_b = s.rows * s.dp;
     h.na = s.v;
     h.nb = len;
     h.k = s.dp;
+    h.k_real = h.a_width;
     h.tokens_in_b = 1;
     h.slot_bits = 1;
     h.ldo = s.v;
@@ -1681,7 +1699,7 @@ GemmArgs raw_product(const HeadShape& s, int64_t len) {
 }
 GemmArgs head_product(const HeadShape& s, int64_t len) {
     GemmArgs h{};
-    h.lda = s.dp;
+    h.a_width = h.lda = s.dp;
     h.ldb = s.vp;
     h.plane_a = s.rows * s.dp;
     h.plane_b = s.chunk * s.vp;
@@ -1771,8 +1789,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.a = w;
         l.b = x + first * s.dp;
         l.thin = s.thin;
-        l.a_width = s.d;
-        l.lda = s.thin ? s.d : s.dp;
+        l.a_width = l.lda = l.k_real = s.pack_head ? s.dp : s.d;
         l.ldb = s.dp;
         l.plane_a = w_plane;
         l.plane_b = x_plane;

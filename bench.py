@@ -29,14 +29,18 @@ Other modes, each printing its own JSON line:
   --split       reduce into the accumulator, then Adam (unfused update)
   --prefetch    forward + backward over a Llama-7B stack through the
                 per-layer gather schedule; hidden fraction of gather time
+                (--head-loss: with the 32000 x 4096 head gathered where the
+                pass turns, and its loss and gradients)
   --checkpoint DIR   sharded checkpoint save / load / reshard-load timings
   --operators CASES  cases of perf/operators.py (gradient norm, clipping and
-                clipped steps) through the library
+                clipped steps) and perf/more_operators.py (losses over the
+                head) through the library
   --rocprof-summary DIR, --traffic-from F W   turn rocprofv3 output into the
                 text and JSON summaries kept under profiles/
 """
 import argparse
 import csv
+import dataclasses
 import glob
 import hashlib
 import json
@@ -124,8 +128,12 @@ def parse():
                          "print the hidden fraction of gather time as one JSON line")
     ap.add_argument("--operators", metavar="CASE[,CASE...]", default=None,
                     help="instead of the step: time --steps passes of cases of "
-                         "perf/operators.py ('all': every one) through the library, over "
-                         "three sets of inputs in turn, and print one JSON line")
+                         "perf/operators.py ('all': every one) or perf/more_operators.py "
+                         "('head': every one) through the library, over three sets of "
+                         "inputs in turn, and print one JSON line")
+    ap.add_argument("--head-loss", action="store_true",
+                    help="with --prefetch: the head as a last group of the schedule, gathered "
+                         "between forward and backward, and zsp_head_loss with both gradients")
     ap.add_argument("--layers", type=int, default=32)
     ap.add_argument("--tokens", type=int, nargs="+", default=[512, 1024, 4096])
     ap.add_argument("--depths", type=int, nargs="+", default=[1, 2])
@@ -488,7 +496,9 @@ def prefetch_bench(args, device):
       gathers  = passes of gathers alone (depth 0, no compute)
       depth D  = gathers through the schedule with compute
       hidden(D) = (compute + gathers - depth D) / gathers
-    each for the gather kernel and for the copy engines (copy_*).
+    each for the gather kernel and for the copy engines (copy_*). With
+    --head-loss the head is one more group, at the turn from forward to
+    backward, and its compute is zsp_head_loss with both gradients.
     """
     import statistics
     import torch
@@ -496,6 +506,9 @@ def prefetch_bench(args, device):
     from zero_sharded_mixed_pad_amd import synth
 
     w = synth.llama_stack(args.layers, 8)
+    head = (32000, 4096) if args.head_loss else None
+    if head:
+        w = dataclasses.replace(w, numel=w.numel + [head[0] * head[1]])
     plan = zsp.partition(w.numel, w.n_d)
     n = w.n_d * plan.S
     state = [torch.empty(n, dtype=torch.float32, device=device) for _ in range(3)]
@@ -506,8 +519,8 @@ def prefetch_bench(args, device):
     torch.cuda.synchronize()
     del flat
     L = args.layers
-    groups = [(9 * l, 9) for l in range(L)]
-    order = list(range(L)) + list(range(L - 1, -1, -1))
+    groups = [(9 * l, 9) for l in range(L)] + ([(9 * L, 1)] if head else [])
+    order = list(range(L)) + ([L] if head else []) + list(range(L - 1, -1, -1))
     shapes = [(4096, 4096)] * 4 + [(11008, 4096)] * 2 + [(4096, 11008)]  # (out, in)
     layer_elems = sum(w.numel[:9])
     cs, gs = torch.cuda.Stream(), torch.cuda.Stream()
@@ -517,6 +530,13 @@ def prefetch_bench(args, device):
     for t in range(9):
         fixed_views.append(fixed[k:k + w.numel[t]])
         k += w.numel[t]
+    pass_elems = 2 * L * layer_elems
+    if head:
+        pass_elems += head[0] * head[1]
+        fixed_head = torch.empty(head[0] * head[1], dtype=torch.bfloat16, device=device)
+        plan.gather(9 * L, fixed_head, "work")
+        # rank 0's gradient of the head, as the reduce reads it
+        head_grad = torch.empty(head, dtype=torch.bfloat16, device=device)
     scheds = {}
     for engine in ("kernel", "copy"):
         for D in [0] + list(args.depths):
@@ -529,6 +549,7 @@ def prefetch_bench(args, device):
 
     results = {"layers": L, "n_d": w.n_d, "positions": len(order),
                "gather_bytes_per_layer": 4 * layer_elems,
+               "head": list(head) if head else None,
                "arena_bytes": {str(D): s.arena_bytes for (e, D), (s, _a) in scheds.items()
                                if e == "kernel"},
                "runs": []}
@@ -537,7 +558,18 @@ def prefetch_bench(args, device):
              for d in (4096, 11008)}
         dw = {sh: torch.empty(sh, device=device, dtype=torch.bfloat16) for sh in set(shapes)}
 
-        def compute(views, backward):
+        if head:
+            target = torch.randint(0, head[0], (T,), device=device)
+            loss = torch.empty(T, device=device)
+            head_ws = zsp.head_workspace(T, *head, torch.bfloat16, device=device)
+            hidden_grad = torch.empty_like(x[head[1]])
+
+        def compute(views, p):
+            if head and p == L:          # the turn: the loss and its gradients
+                zsp.head_loss(x[head[1]], views[0].view(head), target, loss, head_ws,
+                              scale=1.0 / T, grad_hidden=hidden_grad, grad_head=head_grad)
+                return
+            backward = p >= L
             for v, (o, i) in zip(views[:7], shapes):
                 W = v.view(o, i)
                 if not backward:
@@ -553,11 +585,11 @@ def prefetch_bench(args, device):
                 a.record(cs)
                 for p in range(len(order)):
                     if sched is None:
-                        compute(fixed_views, p >= L)
+                        compute([fixed_head] if head and p == L else fixed_views, p)
                         continue
                     views = sched.acquire(p, cs)
                     if with_compute:
-                        compute(views, p >= L)
+                        compute(views, p)
                     sched.release(p, cs)
                 b.record(cs)
             return a, b
@@ -579,9 +611,9 @@ def prefetch_bench(args, device):
         ms = {name: statistics.median(a.elapsed_time(b) for a, b in e) for name, e in evs.items()}
         c, g, gc = ms["compute"], ms["gathers"], ms["gathers_copy"]
         row = {"tokens": T, "compute_ms": round(c, 3), "gathers_ms": round(g, 3),
-               "gather_GBps": round(4 * layer_elems * len(order) / g / 1e6, 1),
+               "gather_GBps": round(4 * pass_elems / g / 1e6, 1),
                "copy_gathers_ms": round(gc, 3),
-               "copy_gather_GBps": round(4 * layer_elems * len(order) / gc / 1e6, 1),
+               "copy_gather_GBps": round(4 * pass_elems / gc / 1e6, 1),
                "depth": {}, "copy_depth": {}}
         for D in [0] + list(args.depths):
             t = ms[f"depth{D}"]
@@ -758,6 +790,34 @@ _OPS = {0: "copy_in", 1: "reduce_set", 2: "reduce_acc", 3: "fused_reduce_adam_ca
         10: "fused_clip", 11: "fused_acc_clip", 12: "adam_clip"}
 
 
+def _short_head(name):
+    """The name of a kernel of the head's losses, or None."""
+    import re
+    m = re.search(r"zsp.*?(gemm|thin|outer|setup|scan|flag|split|raw_join|join)_kernel", name)
+    if not m:
+        return None
+    kind = m.group(1)
+    args = [int(v) for v in re.findall(r"L[ib](\d+)E", name)]
+    if "<" in name:
+        inner = re.search(r"_kernel<(.*?)>\(", name)
+        args = [{"false": 0, "true": 1}.get(v.strip(), v.strip()) for v in
+                inner.group(1).split(",")] if inner else []
+        args = [int(v) if str(v).lstrip("-").isdigit() else v for v in args]
+    if kind == "gemm" and len(args) == 10:
+        ba, bb, a_rows, b_rows, f32, out = args[0], args[1], *args[6:]
+        what = "logits" if not out else "logit_parts" if not a_rows else \
+            "grad_head" if b_rows else "grad_hidden"
+        return f"head_{what}_{ba}x{bb}[{'f32' if f32 else 'bf16'}]"
+    if kind == "thin" and len(args) == 3:
+        what = "logits" if not args[2] else "grad_hidden" if args[1] else "logit_parts"
+        return f"head_{what}_in_place_{16 * args[0]}[f32]"
+    if kind == "outer" and args:
+        return f"head_grad_head_{32 * args[0]}_tokens[bf16]"
+    if kind in ("split", "join", "raw_join") and args:
+        return f"head_{kind}[{'f32' if args[0] else 'bf16'}]"
+    return f"head_{kind}"
+
+
 def _short(name):
     """Readable kernel name from a mangled or demangled rocprofv3 name."""
     import re
@@ -778,6 +838,9 @@ def _short(name):
         return f"gather_list_{m.group(1)}[{dt}]"
     if "list_expand_kernel" in name:
         return "gather_list_expand"
+    head = _short_head(name)
+    if head:
+        return head
     name = re.sub(r"^void ", "", name)
     return name[:48]
 
@@ -877,25 +940,30 @@ def load_traffic(workload, kernel):
 # ---------------------------------------------------------------------------
 
 def operators_bench(args, say):
-    """Passes of the named cases of perf/operators.py through the library, one
-    after another over three sets of inputs: us per pass (median of five
-    blocks, the device waited for at the end of each) and the host's share."""
+    """Passes of the named cases of perf/operators.py and
+    perf/more_operators.py through the library, one after another over three
+    sets of inputs: us per pass (median of five blocks, the device waited for
+    at the end of each) and the host's share."""
     import importlib.util
     import statistics
     import torch
-    spec = importlib.util.spec_from_file_location(
-        "_zsp_operators", os.path.join(ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
-    ops.own = True
-    cases = {c["name"]: c for c in ops.listed()}
-    names = list(cases) if args.operators == "all" else args.operators.split(",")
+    cases, groups = {}, {}
+    for group, file in (("all", "operators"), ("head", "more_operators")):
+        spec = importlib.util.spec_from_file_location(
+            f"_zsp_{file}", os.path.join(ROOT, "perf", f"{file}.py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.own = True
+        groups[group] = [c["name"] for c in ops.listed()]
+        cases.update({c["name"]: (ops, c) for c in ops.listed()})
+    names = groups.get(args.operators) or args.operators.split(",")
     unknown = [n for n in names if n not in cases]
     if unknown:
         raise SystemExit(f"unknown case {unknown[0]}; choose from {', '.join(cases)}")
     res = {}
     for name in names:
-        states = [ops.prepare(cases[name], seed) for seed in range(3)]
+        ops, case = cases[name]
+        states = [ops.prepare(case, seed) for seed in range(3)]
         for i in range(max(3, args.warmup)):
             ops.run(states[i % 3])
         torch.cuda.synchronize()
@@ -908,10 +976,13 @@ def operators_bench(args, say):
             torch.cuda.synchronize()
             blocks.append((time.perf_counter() - t0, t1 - t0))
         us, host = (statistics.median(b[k] for b in blocks) * 1e6 / args.steps for k in (0, 1))
-        size = ops.work(cases[name])["bytes"]
+        work = ops.work(case)
+        size = work["bytes"]
         res[name] = {"us_per_pass": round(us, 2), "host_us": round(host, 2), "bytes": size,
                      "GBps": round(size / us / 1e3, 1)}
         say(f"[bench] {name}: {us:.1f} us a pass, {size / us / 1e3:.0f} GB/s")
+        if name in groups["head"]:
+            res[name]["TFLOPs"] = round(work["flops"] / us / 1e6, 1)
         del states
         torch.cuda.empty_cache()
     return res

@@ -372,6 +372,95 @@ def test_differences():
         assert abs(got - want) <= tol, (what, got, want, tol)
 
 
+@pytest.mark.parametrize("n,v,d,dtype,top", [
+    (5, 9000, 256, BF, 0),        # few tokens
+    (100, 9000, 256, BF, 6),
+    (9, 9000, 256, F32, 0),       # an fp32 head read in place
+    (50, 700, 1000, F32, 4),      # the same, logits in parts
+    (40, 500, 333, BF, 0),        # the head copied, logits in parts
+    (600, 3000, 128, F32, 0),
+])
+def test_forms_replayed(n, v, d, dtype, top):
+    """Each form captured on a side stream and replayed over other inputs, a
+    workspace full of NaN each time, eager work of its own between."""
+    sets = [make(n, v, d, dtype, top, seed) for seed in range(2)]
+    T = 1.5 if top else 1.0
+    live = [None if s is None else s.clone() for s in sets[0]]
+    want = [[o.clone() for o in call(*s, T)] for s in sets]
+    out = [torch.zeros_like(o) for o in want[0]]
+    ws = zsp.head_workspace(n, v, d, dtype, top=top)
+    st = torch.cuda.Stream()
+
+    def run():
+        more = dict(lse=out[1], grad_hidden=out[2], grad_head=out[3], stream=st)
+        if top:
+            zsp.head_distill(*live, out[0], ws, temperature=T, **more)
+        else:
+            zsp.head_loss(*live[:3], out[0], ws, **more)
+
+    torch.cuda.synchronize()
+    run()
+    st.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        run()
+    for k in (1, 0, 1):
+        for a, b in zip(live, sets[k]):
+            if a is not None:
+                a.copy_(b)
+        for o in out:
+            o.fill_(float("nan"))
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[k]):
+            assert torch.equal(a, b)
+        call(*sets[0], T)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight together, each with a workspace of its own."""
+    sets = [make(700, 5000, 256, BF, 0, s) for s in range(2)]
+    want = [call(*s) for s in sets]
+    ws = [zsp.head_workspace(700, 5000, 256, BF) for _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call(*s, ws=ws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+def test_binding_refuses():
+    x, w, t, _ = make(10, 70, 64, BF)
+    loss, ws = torch.empty(10, device=dev()), zsp.head_workspace(10, 70, 64, BF)
+    ok = lambda **k: zsp.head_loss(**{**dict(hidden=x, head=w, target=t, loss=loss, ws=ws), **k})  # noqa: E731
+    ok()
+    wide = torch.empty(10, 128, device=dev(), dtype=BF)
+    for bad, error, text in (
+            (dict(hidden=wide[:, ::2]), ValueError, "hidden must be contiguous"),
+            (dict(target=t.int()), TypeError, "target must be torch.int64"),
+            (dict(target=t[:9]), ValueError, "target must have shape"),
+            (dict(loss=loss.double()), TypeError, "loss must be torch.float32"),
+            (dict(lse=loss[:9]), ValueError, "lse must have shape"),
+            (dict(head=w.float()), TypeError, "head must be torch.bfloat16"),
+            (dict(grad_hidden=x.float()), TypeError, "grad_hidden must be torch.bfloat16"),
+            (dict(grad_head=w[:69].clone()), ValueError, "grad_head must have shape"),
+            (dict(token_weight=loss.to(BF)), TypeError, "token_weight must be torch.float32"),
+            (dict(ws=ws.float()), TypeError, "ws must be torch.uint8")):
+        with pytest.raises(error, match=text):
+            ok(**bad)
+    for bad in (dict(ws=ws[:256]), dict(lse=loss), dict(grad_hidden=x), dict(scale=float("nan"))):
+        with pytest.raises(zsp.ZspError):
+            ok(**bad)
+
+
 def test_on_another_stream_and_replayed():
     """A captured call, replayed over new inputs with eager work between."""
     n, v, d = 260, 1100, 192
@@ -407,23 +496,49 @@ def test_on_another_stream_and_replayed():
         call(*sets[0], 2.0)
 
 
-def test_more_tokens_than_are_kept_at_a_time():
-    """Two chunks: 2^20 columns by 2200 tokens are more than 4 GiB of P."""
-    n, v, d = 2200, 1 << 20, 64
-    x, w, t, _ = make(n, v, d, BF)
+@pytest.mark.parametrize("n,dtype,top", [(2200, BF, 0), (2200, BF, 3), (900, F32, 0)])
+def test_more_tokens_than_are_kept_at_a_time(n, dtype, top):
+    """2^20 columns by so many tokens are more than 4 GiB of P: chunks, the
+    head's gradient summed over them in fp32."""
+    v, d = 1 << 20, 64
+    x, w, t, lg = make(n, v, d, dtype, top)
     t[::5] = -100
-    loss, lse, gx, gw = call(x, w, t)
-    on = t >= 0
+    loss, lse, gx, gw = call(x, w, t, lg)
+    idx = t if top else t[:, None]
+    ok = idx >= 0
+    on = ok.any(1)
     l = x.double() @ w.double().t()
     ref = torch.logsumexp(l, 1)
     assert float(((lse.double() - ref) * on).abs().max()) < 2.0 ** -16
+    at = idx.clamp_min(0)
+    q = torch.softmax(torch.where(ok & on[:, None], lg.double(), -1e300), 1) if top else ok.double()
+    q = torch.where(ok, q, 0.0)
+    terms = torch.where(q > 0, q * (q.clamp_min(1e-300).log() - l.gather(1, at) + ref[:, None]), 0)
+    assert float((loss.double() - terms.sum(1) * on).abs().max()) < 2.0 ** -15
     l.sub_(ref[:, None]).exp_()
-    l.scatter_add_(1, t.clamp_min(0)[:, None], torch.full((n, 1), -1.0, device=dev(),
-                                                        dtype=torch.float64))
+    l.scatter_add_(1, at, -q)
     l[~on] = 0
+    far = 3 * B if dtype == BF else 2.0 ** -15
     for got, want in ((gx, l @ w.double()), (gw, l.t() @ x.double())):
-        far = torch.linalg.norm(got.double() - want) / torch.linalg.norm(want)
-        assert float(far) < 3 * B, float(far)
+        e = torch.linalg.norm(got.double() - want) / torch.linalg.norm(want)
+        assert float(e) < far, float(e)
+
+
+def test_rows_of_the_softmax_past_31_bits():
+    """A tile's last row of P starts more than 2^31 bytes behind its first."""
+    n, v, d = 300, (1 << 22), 16
+    x, w, t, _ = make(n, v, d, BF)
+    t[7] = v - 1
+    loss, lse, gx, gw = call(x, w, t)
+    l = x.double() @ w.double().t()
+    ref = torch.logsumexp(l, 1)
+    assert float((lse.double() - ref).abs().max()) < 2.0 ** -16
+    assert float((loss.double() - ref + l.gather(1, t[:, None])[:, 0]).abs().max()) < 2.0 ** -15
+    l.sub_(ref[:, None]).exp_()
+    l[torch.arange(n), t] -= 1
+    for got, want in ((gx, l @ w.double()), (gw, l.t() @ x.double())):
+        e = torch.linalg.norm(got.double() - want) / torch.linalg.norm(want)
+        assert float(e) < 3 * B, float(e)
 
 
 def test_offsets_past_32_bits():

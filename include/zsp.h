@@ -511,7 +511,8 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * products below 2^-23 of a term left out); the softmax is taken in fp32, its
  * sums, the losses and a target's own g in 64 bits. For bf16, p and
  * token_weight_i * g_iv / T are each rounded to bf16 before the two products
- * that make the gradients; scale * T comes to their sums in fp32. Equal inputs give equal bits.
+ * that make the gradients; scale * T comes to their sums in fp32. Equal inputs
+ * give equal bits.
  *   0 <= n <= 2^24 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024.
  * Pointers need the alignment of their element type only, ws 16 bytes; a head
  * on 16 bytes whose d is a multiple of 8 is read in place (fp32: of 4, by up to

@@ -1089,21 +1089,50 @@ struct JoinArgs {
     int32_t parts;            // workgroups a token
 };
 
-__device__ __forceinline__ double block_sum(double v, double* s) {
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = v;
-    __syncthreads();
-    return s[0] + s[1] + s[2] + s[3];
-}
 // NaN wins, as in a sum
 __device__ __forceinline__ float nan_max(float a, float b) { return a != a || a > b ? a : b; }
-__device__ __forceinline__ float block_max(float v, float* s) {
-    for (int o = 32; o; o >>= 1) v = nan_max(v, __shfl_xor(v, o));
+
+// Two largest values, and two sums, over the T threads of a workgroup, in a
+// fixed order; s holds two for each wave.
+template <int T>
+__device__ __forceinline__ void block_max2(float& a, float& b, float* s) {
+    for (int o = 32; o; o >>= 1) {
+        a = nan_max(a, __shfl_xor(a, o));
+        b = nan_max(b, __shfl_xor(b, o));
+    }
     __syncthreads();
-    if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = v;
+    if (threadIdx.x % 64 == 0) {
+        s[threadIdx.x / 64] = a;
+        s[T / 64 + threadIdx.x / 64] = b;
+    }
     __syncthreads();
-    return nan_max(nan_max(s[0], s[1]), nan_max(s[2], s[3]));
+    a = s[0];
+    b = s[T / 64];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) {
+        a = nan_max(a, s[w]);
+        b = nan_max(b, s[T / 64 + w]);
+    }
+}
+template <int T>
+__device__ __forceinline__ void block_sum2(double& a, double& b, double* s) {
+    for (int o = 32; o; o >>= 1) {
+        a += __shfl_xor(a, o);
+        b += __shfl_xor(b, o);
+    }
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) {
+        s[threadIdx.x / 64] = a;
+        s[T / 64 + threadIdx.x / 64] = b;
+    }
+    __syncthreads();
+    a = s[0];
+    b = s[T / 64];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) {
+        a += s[w];
+        b += s[T / 64 + w];
+    }
 }
 
 template <bool F32>
@@ -1133,52 +1162,83 @@ __device__ __forceinline__ void put_g8(const JoinArgs& a, int64_t row, int64_t c
     }
 }
 
-// The loss of row r from its lse and its entries' logits (logit(k, column));
-// leaves the entries' share of the target distribution in s_q. In 64 bits:
-// the loss is a small difference where the model agrees with its target.
-template <typename F>
-__device__ __forceinline__ double entries_loss(const JoinArgs& a, int64_t r, double lse, float* s_q,
-                                               double* s_d, float* s_f, F logit) {
-    const int t = threadIdx.x;
-    const int32_t* entry = a.entry + r * a.top_pad;
-    if (!a.teach) {
-        if (t == 0) s_q[0] = 1.0f;
-        __syncthreads();
-        return lse - double(logit(0, entry[0]));
-    }
-    const float* teach = a.teach + r * a.top_pad;
-    float tm = -__builtin_inff();
-    for (int32_t k = t; k < a.top; k += 256)
-        if (entry[k] >= 0) tm = nan_max(tm, teach[k]);
-    tm = block_max(tm, s_f);
-    double ts = 0.0;
-    for (int32_t k = t; k < a.top; k += 256)
-        if (entry[k] >= 0) ts += exp((double(teach[k]) - double(tm)) / double(a.temp));
-    ts = block_sum(ts, s_d);
-    const double lq = log(ts);  // from the largest: logits may all be far below 0
-    double loss = 0.0;
-    for (int32_t k = t; k < a.top; k += 256) {
-        double q = 0.0;
-        if (entry[k] >= 0) {
-            const double l = (double(teach[k]) - double(tm)) / double(a.temp) - lq;
-            q = exp(l);
-            if (q != 0.0) loss += q * (l - (double(logit(k, entry[k])) - lse));
+// A thread's entries of row r, read before anything waits for them: the
+// teacher's softmax goes through the same joins over the workgroup as the
+// model's. In 64 bits, exponentials too: the loss and p - q are small
+// differences where the model agrees with its target, and with fp32
+// exponentials (32 us in place of 36 for 6354 tokens x 716 x 14 entries) a
+// gradient of 1.5e-6 was 4e-9 off.
+template <int T>
+struct Entries {
+    static constexpr int N = kHeadMaxTop / T;
+    int32_t e[N];
+    float t[N];
+
+    __device__ __forceinline__ void load(const JoinArgs& a, int64_t r) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int32_t k = i * T + threadIdx.x;
+            e[i] = -1;
+            t[i] = 0.0f;
+            if (i * T >= a.top || k >= a.top) continue;
+            e[i] = a.entry[r * a.top_pad + k];
+            if (a.teach) t[i] = a.teach[r * a.top_pad + k];
         }
-        s_q[k] = float(q);
     }
-    return block_sum(loss, s_d) * double(a.temp) * double(a.temp);
-}
+    __device__ __forceinline__ float largest(const JoinArgs& a) const {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i * T < a.top && e[i] >= 0) m = nan_max(m, t[i]);
+        return m;
+    }
+    // Against the largest: logits may all be far below 0.
+    __device__ __forceinline__ double total(const JoinArgs& a, float m) const {
+        double s = 0.0;
+        if (!a.teach) return s;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i * T < a.top && e[i] >= 0)
+                s += exp((double(t[i]) - double(m)) / double(a.temp));
+        return s;
+    }
+    // The row's loss; leaves the entries' share of the target in s_q.
+    template <typename F>
+    __device__ __forceinline__ double loss(const JoinArgs& a, double lse, float m, double total,
+                                           float* s_q, double* s_d, F logit) const {
+        if (!a.teach) {
+            if (threadIdx.x == 0) s_q[0] = 1.0f;
+            return threadIdx.x == 0 ? lse - double(logit(0, e[0])) : 0.0;
+        }
+        const double lq = log(total);
+        double sum = 0.0, none = 0.0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int32_t k = i * T + threadIdx.x;
+            if (i * T >= a.top || k >= a.top) continue;
+            double q = 0.0;
+            if (e[i] >= 0) {
+                const double l = (double(t[i]) - double(m)) / double(a.temp) - lq;
+                q = exp(l);
+                if (q != 0.0) sum += q * (l - (double(logit(k, e[i])) - lse));
+            }
+            s_q[k] = float(q);
+        }
+        block_sum2<T>(sum, none, s_d);
+        return sum * double(a.temp) * double(a.temp);
+    }
+};
 
 // The entries' own G, in columns [from, to): c (p - q) with p - q = (p - 1) +
 // (1 - q) in 64 bits (from P's bf16, all of 1 - p would be lost where the model
 // is sure of its target). Entries of one column write the same sum of their q;
 // they stand in one block of the vocabulary, so beside each other.
-template <bool F32, typename F>
+template <bool F32, int T, typename F>
 __device__ __forceinline__ void entries_gradient(const JoinArgs& a, int64_t r, int64_t from,
                                                  int64_t to, double lse, float c, const float* s_q,
                                                  F logit) {
     const int32_t* entry = a.entry + r * a.top_pad;
-    for (int32_t k = threadIdx.x; k < a.top; k += 256) {
+    for (int32_t k = threadIdx.x; k < a.top; k += T) {
         const int32_t e = entry[k];
         if (e < from || e >= to) continue;
         const int32_t block = e / kHeadBlock;
@@ -1196,8 +1256,8 @@ __device__ __forceinline__ void entries_gradient(const JoinArgs& a, int64_t r, i
 // loss, then the token's row of G.
 template <bool F32>
 __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
-    __shared__ double s_d[4];
-    __shared__ float s_f[4];
+    __shared__ double s_d[8];
+    __shared__ float s_f[8];
     __shared__ float s_q[kHeadMaxTop];
     const int64_t r = blockIdx.x / a.parts, count = *a.count - a.first;
     const int32_t part_no = int32_t(blockIdx.x - r * a.parts);
@@ -1214,29 +1274,32 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
                     *reinterpret_cast<u32x4*>(a.g + k * a.plane + r * a.ldp + c) = u32x4{0, 0, 0, 0};
         return;
     }
+    Entries<256> entries;
+    entries.load(a, r);
+    const int64_t token = a.rows[r];
+    const float c = a.coef[r];
     const float2* part = a.part + r * a.nblk;
     float m = -__builtin_inff();
-    for (int64_t b = t; b < a.blocks; b += 256) m = nan_max(m, part[b].x);
-    m = block_max(m, s_f);
+    for (int32_t b = t; b < a.blocks; b += 256) m = nan_max(m, part[b].x);
+    float tm = entries.largest(a);
+    block_max2<256>(m, tm, s_f);
     double s = 0.0;
-    for (int64_t b = t; b < a.blocks; b += 256) {
+    for (int32_t b = t; b < a.blocks; b += 256) {
         const float2 q = part[b];
         s += double(q.y) * double(q.x == m ? 1.0f : fast_exp(q.x - m));
     }
-    s = block_sum(s, s_d);
+    double ts = entries.total(a, tm);
+    block_sum2<256>(s, ts, s_d);
     const double lse = double(m) + log(s);
-
-    const int64_t token = a.rows[r];
     const float* pick = a.pick + r * a.top_pad;
     auto logit = [&](int32_t k, int32_t) { return pick[k]; };
-    const double loss = entries_loss(a, r, lse, s_q, s_d, s_f, logit);
+    const double loss = entries.loss(a, lse, tm, ts, s_q, s_d, logit);
     if (t == 0 && part_no == 0) {
         a.loss[token] = float(loss);
         if (a.lse) a.lse[token] = float(lse);
     }
     if (!a.p) return;
 
-    const float c = a.coef[r];
     const float l32 = float(lse);
     if constexpr (F32) {
         const float* p = static_cast<const float*>(a.p) + r * a.ldp;
@@ -1268,7 +1331,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     }
     __threadfence_block();
     __syncthreads();
-    entries_gradient<F32>(a, r, from, to, lse, c, s_q, logit);
+    entries_gradient<F32, 256>(a, r, from, to, lse, c, s_q, logit);
 }
 
 // Few tiles (a small vocabulary, or few tokens): the logits' sums over d are
@@ -1282,11 +1345,11 @@ struct RawArgs {
     uint32_t ba, bb, segs, slot_bits;
 };
 
-template <bool F32>
-__global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
-    extern __shared__ float s_l[];
-    __shared__ double s_d[4];
-    __shared__ float s_f[4];
+template <bool F32, int T, int COLS>
+__global__ __launch_bounds__(T) void raw_join_kernel(RawArgs q) {
+    __shared__ float s_l[COLS];
+    __shared__ double s_d[T / 32];
+    __shared__ float s_f[T / 32];
     __shared__ float s_q[kHeadMaxTop];
     const JoinArgs& a = q.j;
     const int64_t r = blockIdx.x;
@@ -1294,54 +1357,60 @@ __global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
     const int t = threadIdx.x, cols = a.blocks * kHeadBlock, v = int32_t(q.v);
     if (r >= count) {
         if (a.p && r < (count + kHeadDepth - 1) / kHeadDepth * kHeadDepth)
-            for (int c = t * 8; c < cols; c += 2048)
+            for (int c = t * 8; c < cols; c += T * 8)
                 for (int k = 0; k < (F32 ? 3 : 1); ++k)
                     *reinterpret_cast<u32x4*>(a.g + k * a.plane + r * a.ldp + c) = u32x4{0, 0, 0, 0};
         return;
     }
+    Entries<T> entries;
+    entries.load(a, r);
+    const int64_t token = a.rows[r];
+    const float c = a.coef[r];
     const uint32_t tiles = (uint32_t(v) + q.ba - 1) / q.ba *
                            ((uint32_t(min(int64_t(count), q.len)) + q.bb - 1) / q.bb);
     const uint32_t ns = split_of(tiles, uint32_t(q.dp) / kHeadDepth, q.segs, q.slot_bits);
     const int64_t stride = int64_t(min(int64_t(count), q.len)) * a.ldp;
     const float* raw = q.raw + r * a.ldp;
     float m = -__builtin_inff();
-    for (int c0 = t; c0 < v; c0 += 1024) {
+    for (int c0 = t; c0 < v; c0 += 4 * T) {
         float l[4] = {0.f, 0.f, 0.f, 0.f};
         for (uint32_t s = 0; s < ns; s += 4) {
-            float q[4][4];  // all on their way before the first is added
+            float x[4][4];  // all on their way before the first is added
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    q[k][i] = raw[min(s + k, ns - 1) * stride + min(c0 + i * 256, v - 1)];
+                    x[k][i] = raw[min(s + k, ns - 1) * stride + min(c0 + i * T, v - 1)];
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (s + k < ns) l[i] += q[k][i];
+                    if (s + k < ns) l[i] += x[k][i];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = c0 + i * 256;
-            if (c >= v) break;
+            if (c0 + i * T >= v) break;
             l[i] *= a.inv_temp;
-            s_l[c] = l[i];
+            s_l[c0 + i * T] = l[i];
             m = nan_max(m, l[i]);
         }
     }
-    m = block_max(m, s_f);
+    float tm = entries.largest(a);
+    block_max2<T>(m, tm, s_f);
     float part = 0.0f;
-    for (int c = t; c < v; c += 256) part += fast_exp(s_l[c] - m);
-    const double lse = double(m) + log(block_sum(double(part), s_d));
-    const int64_t token = a.rows[r];
-    const double loss = entries_loss(a, r, lse, s_q, s_d, s_f, [&](int32_t, int32_t e) { return s_l[e]; });
+    for (int i = t; i < v; i += T) part += fast_exp(s_l[i] - m);
+    double s = double(part), ts = entries.total(a, tm);
+    block_sum2<T>(s, ts, s_d);
+    const double lse = double(m) + log(s);
+    auto logit = [&](int32_t, int32_t e) { return s_l[e]; };
+    const double loss = entries.loss(a, lse, tm, ts, s_q, s_d, logit);
     if (t == 0) {
         a.loss[token] = float(loss);
         if (a.lse) a.lse[token] = float(lse);
     }
     if (!a.p) return;
-    const float c = a.coef[r], l32 = float(lse);
-    for (int i = t * 8; i < cols; i += 2048) {
+    const float l32 = float(lse);
+    for (int i = t * 8; i < cols; i += T * 8) {
         float g[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * fast_exp(s_l[i + k] - l32) : 0.0f;
@@ -1349,7 +1418,7 @@ __global__ __launch_bounds__(256) void raw_join_kernel(RawArgs q) {
     }
     __threadfence_block();
     __syncthreads();
-    entries_gradient<F32>(a, r, 0, cols, lse, c, s_q, [&](int32_t, int32_t e) { return s_l[e]; });
+    entries_gradient<F32, T>(a, r, 0, cols, lse, c, s_q, logit);
 }
 
 // The head's gradient of few tokens (bf16): rows of d for every column of the
@@ -1824,7 +1893,11 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
                        c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
             RawArgs q{j, split, s.v, s.dp, len, t.ba, t.bb, t.segs, t.slot_bits};
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
-            raw_join_kernel<F32><<<uint32_t(grads ? pad : len), 256, s.v * 4, stream>>>(q);
+            const uint32_t grid = uint32_t(grads ? pad : len);
+            if (s.v <= kHeadRawSmall)
+                raw_join_kernel<F32, 256, kHeadRawSmall><<<grid, 256, 0, stream>>>(q);
+            else
+                raw_join_kernel<F32, 1024, kHeadRawColumns><<<grid, 1024, 0, stream>>>(q);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         } else if (len > 0 &&
                    (e = pick_gemm<false, false, F32, kLogits>(l, stream)) != hipSuccess) {
@@ -1833,8 +1906,10 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
 
         if (!s.raw && len > 0) {
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
-            // at least 4096 columns each
-            const int64_t most = std::min<int64_t>((blocks + 63) / 64, 1024 / pad);
+            // at least 2048 columns each, in up to 1024 workgroups, since each
+            // reads all partials of its token (2048 workgroups: 96 tokens x
+            // 32000 x 4096 take 203 us in place of 195)
+            const int64_t most = std::min<int64_t>((blocks + 31) / 32, 1024 / pad);
             const int32_t parts = grads ? int32_t(std::max<int64_t>(most, 1)) : 1;
             JoinArgs j{part, l.nblk, blocks, count, first, rows + first, coef + first, l.entry,
                        l.pick, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
@@ -1880,7 +1955,9 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
 }  // namespace
 
 // Whether the logits' sums are worth splitting: a row of them has to fit LDS
-// beside others, and the whole product to leave most of the card idle.
+// beside others, and the whole product to leave most of the card idle. With
+// rows of up to 32768 logits taken this way, 96 tokens x 32000 x 4096 with the
+// head's gradient take 231 us in place of 195.
 bool head_is_raw(const HeadShape& s) {
     if (s.n == 0 || s.v > kHeadRawColumns || s.nchunk > 1) return false;
     const GemmArgs h = raw_product(s, s.n);

@@ -17,7 +17,8 @@ constexpr int32_t kHeadDepth = 64;       // d is padded to it
 constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
 constexpr int32_t kHeadFew = 128;        // tokens whose gradient of the head has a way of its own
 constexpr int32_t kHeadThin = 64;        // tokens that read an fp32 head in place
-constexpr int32_t kHeadRawColumns = 8192;  // logits of a token that a workgroup keeps in LDS
+constexpr int32_t kHeadRawColumns = 8192;   // logits of a token that a workgroup keeps in LDS
+constexpr int32_t kHeadRawSmall = 4096;     // ... of 256 threads
 
 // Sizes of a call, and the byte offsets of its parts of the workspace.
 struct HeadShape {

@@ -493,44 +493,48 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  *     g_iv = T * (p_iv - sum of q_ik over the k with index[i, k] = v)
  * Both leave loss [n] and, unless NULL, lse [n] (fp32) and the gradients of
  *     scale * sum over i of token_weight_i * loss_i
- * with regard to hidden, sum over v of scale * token_weight_i * g_iv * head_v,
- * in grad_hidden [n, d], and with regard to head, sum over i of scale *
- * token_weight_i * g_iv * hidden_i, in grad_head [v, d]. A NULL gradient is
- * not computed; token_weight NULL is 1 for every token.
+ * with regard to hidden, sum over v of scale * token_weight_i * g_iv *
+ * head_v, in grad_hidden [n, d], and with regard to head, sum over i of
+ * scale * token_weight_i * g_iv * hidden_i, in grad_head [v, d]. A NULL
+ * gradient is not computed; token_weight NULL is 1 for every token.
  *   A token counts if its target (one of its indices) lies in [0, v) and its
  * weight is not 0. Of a token that does not count, loss, lse and its row of
- * grad_hidden are 0 and nothing reaches grad_head, whatever its row of hidden
- * holds; the batch costs what the tokens that count cost. Of a token's
- * entries those with an index outside [0, v) or a logit of -infinity are left
- * out; a token without any other does not count. An index that occurs twice
- * is two entries. The logits are not kept: a call
- * with gradients keeps the softmax of at most 4 GiB of its tokens at a time in
+ * grad_hidden are 0 and nothing reaches grad_head, whatever its row of
+ * hidden holds; the batch costs what the tokens that count cost. Of a
+ * token's entries those with an index outside [0, v) or a logit of -infinity
+ * are left out; a token without any other does not count. An index that
+ * occurs twice is two entries. The logits are not kept: a call with
+ * gradients keeps the softmax of at most 4 GiB of its tokens at a time in
  * the workspace.
- *   hidden, head and the gradients are all of `dtype`. Products are summed in
- * fp32 (operands of fp32 type are split into three bf16 values, exactly, and
- * products below 2^-23 of a term left out); the softmax is taken in fp32, its
- * sums, the losses and a target's own g in 64 bits. For bf16, p and
- * token_weight_i * g_iv / T are each rounded to bf16 before the two products
- * that make the gradients; scale * T comes to their sums in fp32. Equal inputs
- * give equal bits.
- *   0 <= n <= 2^24 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024.
- * Pointers need the alignment of their element type only, ws 16 bytes; a head
- * on 16 bytes whose d is a multiple of 8 is read in place (fp32: of 4, by up to
- * 64 tokens), any other is copied into the workspace first. No plan is involved: all tensors are on
- * the current device. Nothing is waited for, copied by the host or allocated,
- * so calls can be captured into a HIP graph. A workspace's contents mean
- * nothing between calls; calls that may run at the same time, replays of
- * captured graphs among them, each need their own.
+ *   hidden, head and the gradients are all of `dtype`. Products are summed
+ * in fp32 (operands of fp32 type are split into three bf16 values, exactly,
+ * and products below 2^-23 of a term left out; of an infinity in hidden or
+ * head a NaN may come); the softmax is taken in fp32, its sums, the losses
+ * and a target's own g in 64 bits. For bf16, p and token_weight_i * g_iv / T
+ * are each rounded to bf16 before the two products that make the gradients;
+ * scale * T comes to their sums in fp32. Equal inputs give equal bits.
+ *   0 <= n <= 2^23 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024, n *
+ * d below about 2^34. Pointers need the alignment of their element type
+ * only, ws 16 bytes; a head on 16 bytes whose d is a multiple of 8 is read
+ * in place (fp32: of 4, by up to 64 tokens), any other is copied into the
+ * workspace first. No plan is involved: all tensors are on the current
+ * device. Nothing is waited for, copied by the host or allocated, so calls
+ * can be captured into a HIP graph. A workspace's contents mean nothing
+ * between calls; calls that may run at the same time, replays of captured
+ * graphs among them, each need their own.
  *   ZSP_EINVAL: a bad dtype, a negative size, v or d of 0, a NULL or
- * misaligned argument, scale or temperature not finite or temperature <= 0,
- * an output that overlaps another argument; ZSP_ERANGE: a size beyond the
- * limits, ws_bytes too small. n = 0: grad_head is set to 0. */
+ * misaligned argument, scale, temperature, their product or 1 / temperature
+ * not finite, temperature <= 0, an output that overlaps another argument;
+ * ZSP_ERANGE: a size beyond the limits, ws_bytes too small. n = 0: grad_head
+ * is set to 0. */
 #define ZSP_HEAD_GRAD_HIDDEN 1 /* grad_hidden is wanted */
 #define ZSP_HEAD_GRAD_HEAD 2   /* grad_head is wanted */
 #define ZSP_HEAD_UNALIGNED 4   /* head may start off a 16-byte boundary */
 
 /* Workspace bytes of a call: top as for zsp_head_distill, 0 for zsp_head_loss;
- * flags of the above. Host only. */
+ * flags of the above. Fewer tokens may need more bytes (their sums are cut
+ * further): a workspace for calls of several sizes is as large as the largest
+ * answer. Host only. */
 zsp_status zsp_head_workspace(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
                               int32_t flags, int64_t* bytes);
 zsp_status zsp_head_loss(const void* hidden, const void* head, zsp_dtype dtype, int64_t n,

@@ -50,6 +50,8 @@ EINVAL, ERANGE = binding.EINVAL, binding.ERANGE
     (EINVAL, "v = 0", dict(v=0)),
     (EINVAL, "d = 0", dict(d=0)),
     (ERANGE, "too large", dict(n=(1 << 24) + 1)),
+    (ERANGE, "too large", dict(n=(1 << 23) + 1)),
+    (ERANGE, "n * d", dict(n=1 << 23, d=65536)),
     (ERANGE, "too large", dict(v=(1 << 22) + 1)),
     (ERANGE, "too large", dict(d=65537)),
     (EINVAL, "hidden is NULL", dict(hidden=None)),
@@ -84,6 +86,8 @@ def test_refusals(distill, status, text, changes):
     (EINVAL, "temperature", dict(temperature=-1.0)),
     (EINVAL, "temperature", dict(temperature=math.nan)),
     (EINVAL, "temperature", dict(temperature=math.inf)),
+    (EINVAL, "temperature", dict(temperature=1e-40)),
+    (EINVAL, "scale", dict(scale=1e30, temperature=1e10)),
     (EINVAL, "index is not aligned to 8", dict(index=BASE + (3 << 20) + 4)),
 ])
 def test_refusals_of_distillation(status, text, changes):

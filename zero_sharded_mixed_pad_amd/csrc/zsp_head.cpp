@@ -10,7 +10,7 @@
 namespace zsp {
 namespace {
 
-constexpr int64_t kMaxTokens = int64_t(1) << 24, kMaxVocab = int64_t(1) << 22, kMaxDepth = 65536;
+constexpr int64_t kMaxTokens = int64_t(1) << 23, kMaxVocab = int64_t(1) << 22, kMaxDepth = 65536;
 // The softmax of at most so many bytes is kept at a time.
 constexpr int64_t kKeptBytes = int64_t(1) << 32;
 
@@ -51,6 +51,9 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.nchunk = std::max<int64_t>((n + chunk - 1) / chunk, 1);
     s.chunk = up((n + s.nchunk - 1) / s.nchunk, kHeadTile);
     if (s.chunk > 0) s.nchunk = std::max<int64_t>((n + s.chunk - 1) / s.chunk, 1);
+    if (!head_fits_launch(s))
+        return set_error(ZSP_ERANGE, "n * d = %lld * %lld elements are too many", (long long)n,
+                         (long long)d);
     s.raw = head_is_raw(s);
 
     int64_t at = 0;
@@ -118,9 +121,12 @@ zsp_status head_call(HeadCall c, int64_t n, int64_t v, int64_t d, zsp_dtype dtyp
     HeadShape s;
     zsp_status st = make_shape(n, v, d, dtype, top, flags, &s);
     if (st != ZSP_OK) return st;
-    if (!std::isfinite(c.scale)) return set_error(ZSP_EINVAL, "scale is not finite");
-    if (!(c.temperature > 0.0f) || !std::isfinite(c.temperature))
-        return set_error(ZSP_EINVAL, "temperature = %g is not above 0", double(c.temperature));
+    if (!(c.temperature > 0.0f) || !std::isfinite(c.temperature) ||
+        !std::isfinite(1.0f / c.temperature))
+        return set_error(ZSP_EINVAL, "temperature = %g is not above 0, or its inverse not finite",
+                         double(c.temperature));
+    if (!std::isfinite(c.scale) || !std::isfinite(c.scale * c.temperature))
+        return set_error(ZSP_EINVAL, "scale is not finite, or its product with the temperature");
     if (!c.head) return set_error(ZSP_EINVAL, "head is NULL");
     if (!c.ws) return set_error(ZSP_EINVAL, "ws is NULL");
     if (n > 0) {

@@ -1782,6 +1782,27 @@ GemmArgs head_product(const HeadShape& s, int64_t len) {
     return h;
 }
 
+// The setup's threads of a row (the most that leave at most a sixth of them
+// idle), and its workgroups.
+struct SetupGrid {
+    int32_t row_threads = kSetupThreads, parts;
+    int64_t x_groups, entry_groups, head_groups;
+    int64_t all() const { return x_groups + entry_groups + head_groups; }
+};
+SetupGrid setup_grid(const HeadShape& s) {
+    SetupGrid m;
+    const int64_t eights = s.dp / 8;
+    auto padded = [&] { return (eights + m.row_threads - 1) / m.row_threads * m.row_threads; };
+    while (m.row_threads > 8 && (padded() - eights) * 6 > eights) m.row_threads /= 2;
+    const int64_t per = kSetupThreads / m.row_threads;
+    m.parts = int32_t(padded() / m.row_threads);
+    const int64_t x_rows = (s.n + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
+    m.x_groups = (x_rows + per - 1) / per * m.parts;
+    m.entry_groups = s.top > 1 ? s.n : 0;
+    m.head_groups = s.pack_head ? (s.v + per * kHeadRun - 1) / (per * kHeadRun) * m.parts : 0;
+    return m;
+}
+
 template <bool F32>
 hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     using T = std::conditional_t<F32, float, uint16_t>;
@@ -1821,25 +1842,13 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     {
-        // the most threads a row that leave at most a sixth of them idle
-        int row_threads = kSetupThreads;
-        const int64_t eights = s.dp / 8;
-        while (row_threads > 8 && ((eights + row_threads - 1) / row_threads * row_threads - eights) * 6 > eights)
-            row_threads /= 2;
-        const int64_t per = kSetupThreads / row_threads;
-        const int32_t parts = int32_t((s.dp / 8 + row_threads - 1) / row_threads);
-        const int64_t x_rows = (s.n + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
-        const int64_t x_groups = (x_rows + per - 1) / per * parts;
-        const int64_t entry_groups = start ? s.n : 0;
-        const int64_t head_groups =
-            packed ? (s.v + per * kHeadRun - 1) / (per * kHeadRun) * parts : 0;
+        const SetupGrid m = setup_grid(s);
         SetupArgs q{c.hidden, c.head, c.index, c.logit, c.token_weight, flag, rows, count, coef,
                     entry, teach, start, x, xt, packed, c.grad_hidden, c.loss, c.lse, s.n, s.v, s.d,
-                    s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, row_threads, parts, few_pad,
-                    uint32_t(x_groups), uint32_t(entry_groups), scans};
-        const int64_t groups = x_groups + entry_groups + head_groups;
-        if (groups > 0) {
-            setup_kernel<T><<<uint32_t(groups), kSetupThreads, 0, stream>>>(q);
+                    s.dp, x_plane, w_plane, s.top, s.top_pad, blocks, m.row_threads, m.parts, few_pad,
+                    uint32_t(m.x_groups), uint32_t(m.entry_groups), scans};
+        if (m.all() > 0) {
+            setup_kernel<T><<<uint32_t(m.all()), kSetupThreads, 0, stream>>>(q);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
     }
@@ -1964,6 +1973,12 @@ bool head_is_raw(const HeadShape& s) {
     const TileShape t = tile_of(h, s.f32, true);
     const uint32_t tiles = uint32_t((h.na + t.ba - 1) / t.ba) * uint32_t((h.nb + t.bb - 1) / t.bb);
     return split_of(tiles, uint32_t(h.k) / kHeadDepth, t.segs, t.slot_bits) > 1;
+}
+
+// A launch holds below 2^32 threads. The others' are bounded by n, or by what
+// is kept at a time.
+bool head_fits_launch(const HeadShape& s) {
+    return setup_grid(s).all() * kSetupThreads < int64_t(1) << 32;
 }
 
 int64_t head_split_bytes(const HeadShape& s) {

@@ -55,6 +55,8 @@ struct HeadCall {
     char* ws;
 };
 
+// Whether its rows can be set up in one launch.
+bool head_fits_launch(const HeadShape& s);
 // Whether a call's logits are summed in parts.
 bool head_is_raw(const HeadShape& s);
 // Bytes for the parts of the sums that are split.

@@ -508,9 +508,9 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * the workspace.
  *   hidden, head and the gradients are all of `dtype`. Products are summed
  * in fp32 (operands of fp32 type are split into three bf16 values, exactly,
- * and products below 2^-23 of a term left out; of an infinity in hidden or
- * head a NaN may come); the softmax is taken in fp32, its sums, the losses
- * and a target's own g in 64 bits. For bf16, p and token_weight_i * g_iv / T
+ * and products below 2^-23 of a term left out; of an infinity, or a value
+ * beyond bf16's largest, in hidden or head a NaN may come); the softmax is
+ * taken in fp32, its sums, the losses and a target's own g in 64 bits. For bf16, p and token_weight_i * g_iv / T
  * are each rounded to bf16 before the two products that make the gradients;
  * scale * T comes to their sums in fp32. Equal inputs give equal bits.
  *   0 <= n <= 2^23 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024, n *

@@ -677,6 +677,10 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
                 if (e_from[b] < e_to[b]) one[b] = g.entry[row * g.top_pad + e_from[b]];
             }
         }
+        // in the sums' own units up to here: 1 / T > 0 comes to a block's
+        // largest, its entries and the exponent alone
+        const float log2e_t = g.inv_temp * kLog2e;
+        const bool edge = a_wave + kHeadBlock > g.na;
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
             const int64_t row = b_wave + b * 16 + lr;
@@ -685,10 +689,9 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
             for (int a = 0; a < TA; ++a)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float l = acc[a][b][k] * g.inv_temp;
-                    if (a_wave + a * 16 + lg * 4 + k >= g.na) l = -__builtin_inff();
-                    acc[a][b][k] = l;
-                    m = fmaxf(m, l);
+                    if (edge && a_wave + a * 16 + lg * 4 + k >= g.na)
+                        acc[a][b][k] = -__builtin_inff();
+                    m = fmaxf(m, acc[a][b][k]);
                 }
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
@@ -702,7 +705,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if ((rel >> 4) == a && (rel & 3) == c) l = acc[a][b][c];
-                g.pick[row * g.top_pad + k] = l;
+                g.pick[row * g.top_pad + k] = l * g.inv_temp;
             };
             if (real && g.top_pad == 1) take(0, one[b]);
             if (g.top_pad > 1 && e_from[b] < e_to[b]) {
@@ -717,12 +720,13 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
             for (int a = 0; a < TA; ++a)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    acc[a][b][k] = fast_exp(acc[a][b][k] - mm);
+                    acc[a][b][k] = __builtin_amdgcn_exp2f((acc[a][b][k] - mm) * log2e_t);
                     s += acc[a][b][k];
                 }
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
-            if (lg == 0 && real) g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m, s);
+            if (lg == 0 && real)
+                g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m * g.inv_temp, s);
             if (g.p) {
                 if constexpr (F32) {
                     float* out = static_cast<float*>(g.p) + row * g.ldp + a_wave + lg * 4;

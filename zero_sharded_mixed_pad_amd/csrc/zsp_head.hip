@@ -710,8 +710,14 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
             if (real && g.top_pad == 1) take(0, one[b]);
             if (g.top_pad > 1 && e_from[b] < e_to[b]) {
                 take(e_from[b], one[b]);
-                for (int32_t k = e_from[b] + 1; k < e_to[b]; ++k)
-                    take(k, g.entry[row * g.top_pad + k]);
+                const int32_t* entry = g.entry + row * g.top_pad;
+                for (int32_t k = e_from[b] + 1; k < e_to[b]; k += 4) {
+                    int32_t e[4];  // on their way together
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[i] = entry[min(k + i, e_to[b] - 1)];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) take(min(k + i, e_to[b] - 1), e[i]);
+                }
             }
             // a block without a column of the vocabulary leaves 0
             const float mm = m == -__builtin_inff() ? 0.0f : m;
@@ -1104,6 +1110,7 @@ __device__ __forceinline__ void block_max2(float& a, float& b, float* s) {
         a = nan_max(a, __shfl_xor(a, o));
         b = nan_max(b, __shfl_xor(b, o));
     }
+    if constexpr (T == 64) return;
     __syncthreads();
     if (threadIdx.x % 64 == 0) {
         s[threadIdx.x / 64] = a;
@@ -1124,6 +1131,7 @@ __device__ __forceinline__ void block_sum2(double& a, double& b, double* s) {
         a += __shfl_xor(a, o);
         b += __shfl_xor(b, o);
     }
+    if constexpr (T == 64) return;
     __syncthreads();
     if (threadIdx.x % 64 == 0) {
         s[threadIdx.x / 64] = a;
@@ -1172,9 +1180,8 @@ __device__ __forceinline__ void put_g8(const JoinArgs& a, int64_t row, int64_t c
 // differences where the model agrees with its target, and with fp32
 // exponentials (32 us in place of 36 for 6354 tokens x 716 x 14 entries) a
 // gradient of 1.5e-6 was 4e-9 off.
-template <int T>
+template <int T, int N>
 struct Entries {
-    static constexpr int N = kHeadMaxTop / T;
     int32_t e[N];
     float t[N];
 
@@ -1258,11 +1265,12 @@ __device__ __forceinline__ void entries_gradient(const JoinArgs& a, int64_t r, i
 
 // A workgroup (several, where tokens are few) per token that counts: lse, the
 // loss, then the token's row of G.
-template <bool F32>
-__global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
-    __shared__ double s_d[8];
-    __shared__ float s_f[8];
-    __shared__ float s_q[kHeadMaxTop];
+template <bool F32, int T>
+__global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
+    constexpr int kTop = T == 64 ? 64 : kHeadMaxTop;
+    __shared__ double s_d[T / 32];
+    __shared__ float s_f[T / 32];
+    __shared__ float s_q[kTop];
     const int64_t r = blockIdx.x / a.parts, count = *a.count - a.first;
     const int32_t part_no = int32_t(blockIdx.x - r * a.parts);
     const int t = threadIdx.x;
@@ -1273,27 +1281,27 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         // zeros behind the last token, as far as a stage of the sum over
         // tokens may read
         if (a.p && r < (count + kHeadDepth - 1) / kHeadDepth * kHeadDepth)
-            for (int64_t c = from + t * 8; c < to; c += 2048)
+            for (int64_t c = from + t * 8; c < to; c += T * 8)
                 for (int k = 0; k < (F32 ? 3 : 1); ++k)
                     *reinterpret_cast<u32x4*>(a.g + k * a.plane + r * a.ldp + c) = u32x4{0, 0, 0, 0};
         return;
     }
-    Entries<256> entries;
+    Entries<T, kTop / T> entries;
     entries.load(a, r);
     const int64_t token = a.rows[r];
     const float c = a.coef[r];
     const float2* part = a.part + r * a.nblk;
     float m = -__builtin_inff();
-    for (int32_t b = t; b < a.blocks; b += 256) m = nan_max(m, part[b].x);
+    for (int32_t b = t; b < a.blocks; b += T) m = nan_max(m, part[b].x);
     float tm = entries.largest(a);
-    block_max2<256>(m, tm, s_f);
+    block_max2<T>(m, tm, s_f);
     double s = 0.0;
-    for (int32_t b = t; b < a.blocks; b += 256) {
+    for (int32_t b = t; b < a.blocks; b += T) {
         const float2 q = part[b];
         s += double(q.y) * double(q.x == m ? 1.0f : fast_exp(q.x - m));
     }
     double ts = entries.total(a, tm);
-    block_sum2<256>(s, ts, s_d);
+    block_sum2<T>(s, ts, s_d);
     const double lse = double(m) + log(s);
     const float* pick = a.pick + r * a.top_pad;
     auto logit = [&](int32_t k, int32_t) { return pick[k]; };
@@ -1307,7 +1315,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     const float l32 = float(lse);
     if constexpr (F32) {
         const float* p = static_cast<const float*>(a.p) + r * a.ldp;
-        for (int64_t i = from + t * 4; i < to; i += 1024) {
+        for (int64_t i = from + t * 4; i < to; i += T * 4) {
             const float f = c * fast_exp(part[i / kHeadBlock].x - l32);
             const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
             uint16_t h[4][3];
@@ -1323,7 +1331,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
         }
     } else {
         uint16_t* p = a.g + r * a.ldp;
-        for (int64_t i = from + t * 8; i < to; i += 2048) {
+        for (int64_t i = from + t * 8; i < to; i += T * 8) {
             const float f = c * fast_exp(part[i / kHeadBlock].x - l32);
             u32x4 v = *reinterpret_cast<const u32x4*>(p + i);
 #pragma unroll
@@ -1335,7 +1343,7 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs a) {
     }
     __threadfence_block();
     __syncthreads();
-    entries_gradient<F32, 256>(a, r, from, to, lse, c, s_q, logit);
+    entries_gradient<F32, T>(a, r, from, to, lse, c, s_q, logit);
 }
 
 // Few tiles (a small vocabulary, or few tokens): the logits' sums over d are
@@ -1366,7 +1374,7 @@ __global__ __launch_bounds__(T) void raw_join_kernel(RawArgs q) {
                     *reinterpret_cast<u32x4*>(a.g + k * a.plane + r * a.ldp + c) = u32x4{0, 0, 0, 0};
         return;
     }
-    Entries<T> entries;
+    Entries<T, kHeadMaxTop / T> entries;
     entries.load(a, r);
     const int64_t token = a.rows[r];
     const float c = a.coef[r];
@@ -1927,7 +1935,16 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             JoinArgs j{part, l.nblk, blocks, count, first, rows + first, coef + first, l.entry,
                        l.pick, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
                        c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, parts};
-            join_kernel<F32><<<uint32_t(grads ? pad * parts : len), 256, 0, stream>>>(j);
+            const uint32_t grid = uint32_t(grads ? pad * parts : len);
+            // One wave a token, where its row is short: no barrier, and four
+            // times the tokens on a CU (16384 tokens x 512 x 256 with gradients
+            // 110 -> 80 us; x 4096 252 -> 241, x 8192 of 4096 tokens 156 ->
+            // 158; without gradients 16384 x 4096 105 -> 81, 8192 x 32000 241
+            // -> 224, 5 x 32000 x 4096 50.3 -> 51.8).
+            if (s.top <= 64 && blocks <= (grads || len < 1024 ? 64 : 512))
+                join_kernel<F32, 64><<<grid, 64, 0, stream>>>(j);
+            else
+                join_kernel<F32, 256><<<grid, 256, 0, stream>>>(j);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
 

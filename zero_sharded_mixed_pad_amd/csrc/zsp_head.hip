@@ -716,7 +716,8 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
 #pragma unroll
                     for (int i = 0; i < 4; ++i) e[i] = entry[min(k + i, e_to[b] - 1)];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) take(min(k + i, e_to[b] - 1), e[i]);
+                    for (int i = 0; i < 4; ++i)
+                        if (k + i < e_to[b]) take(k + i, e[i]);
                 }
             }
             // a block without a column of the vocabulary leaves 0

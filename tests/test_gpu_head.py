@@ -197,6 +197,19 @@ def test_distill(n, v, d, top, T, dtype):
     check(call(x, w, idx, lg, T, scale=0.37), Ref(x, w, idx, lg, T, scale=0.37))
 
 
+@pytest.mark.parametrize("top", [0, 40])
+@pytest.mark.parametrize("want", ["hidden", "both"])
+@pytest.mark.parametrize("n,v,d", [(40, 9001, 512), (100, 9001, 512), (129, 9001, 1024),
+                                   (200, 9100, 1000), (256, 8321, 640), (200, 4000, 328)])
+def test_few_tokens(n, v, d, want, top):
+    """Forms that read the head once, kept in the caches (its gradient not
+    asked for) or not, some of whose tokens do not count."""
+    x, w, t, lg = make(n, v, d, BF, top)
+    t[5::9] = -1
+    x[5::9] = float("nan")
+    check(call(x, w, t, lg, 2.0 if top else 1.0, want=want), Ref(x, w, t, lg, 2.0 if top else 1.0))
+
+
 @pytest.mark.parametrize("want", ["none", "hidden", "head"])
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
 @pytest.mark.parametrize("top", [0, 5])
@@ -375,6 +388,7 @@ def test_differences():
 @pytest.mark.parametrize("n,v,d,dtype,top", [
     (5, 9000, 256, BF, 0),        # few tokens
     (100, 9000, 256, BF, 6),
+    (180, 9000, 1024, BF, 3),
     (9, 9000, 256, F32, 0),       # an fp32 head read in place
     (50, 700, 1000, F32, 4),      # the same, logits in parts
     (40, 500, 333, BF, 0),        # the head copied, logits in parts

@@ -434,6 +434,7 @@ struct GemmArgs {
     int64_t plane_a, plane_b;  // elements between planes
     int64_t a_width;           // columns of A's rows as they lie in memory
     int32_t thin;              // an fp32 head read in place
+    int32_t keep;              // the head is read again, and may stay in the caches
     int64_t na;                // extent of a: further rows or columns are read as the last ones
     int64_t nb;                // extent of b; a product over tokens: bounded by *count - first
     int64_t k;                 // the sum's length, and for M-major A with na_k its real rows
@@ -1604,15 +1605,15 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 
 // A product's tiles: columns and rows of a tile, how many the card runs at once
 // (log2), and which form.
-enum Form { kFormBig, kFormMid, kFormMidOnce, kFormLow, kFormLow2, kFormThin };
+enum Form { kFormBig, kFormWide, kFormMid, kFormMidOnce, kFormLow, kFormLow2, kFormThin };
 struct TileShape {
     uint32_t ba, bb, slot_bits;
     Form form;
     uint32_t segs = 1;  // stages of a step of 64 k's
 };
-constexpr TileShape kBig{256, 256, 8, kFormBig}, kMid{128, 128, 9, kFormMid},
-    kMidOnce{128, 128, 9, kFormMidOnce}, kLow{128, 64, 8, kFormLow},
-    kLow2{128, 128, 8, kFormLow2};
+constexpr TileShape kBig{256, 256, 8, kFormBig}, kWide{128, 256, 8, kFormWide},
+    kMid{128, 128, 9, kFormMid}, kMidOnce{128, 128, 9, kFormMidOnce},
+    kLow{128, 64, 8, kFormLow}, kLow2{128, 128, 8, kFormLow2};
 
 // Largest number of items (tiles times parts) and of partial rows times parts
 // over every number of tokens up to the call's.
@@ -1685,11 +1686,11 @@ hipError_t run_thin(GemmArgs g, TileShape t, hipStream_t stream) {
 // on a full card, tiles of 128 x 128 (four waves, two workgroups on a CU)
 // 1.05: the smaller are taken where the larger leave more of the card idle.
 // For up to 64 and 128 tokens, where reading the head is what takes the time,
-// tiles of 128 x 64 and 128 x 128 with six and four stages on their way. They
-// read it non-temporally: kept in the caches, it would only be driven out by
-// the head's gradient, which they can hold instead until it is written
-// (32000 x 4096 of 5 tokens 46.8 -> 42.3 us alone; 17 tokens with gradients
-// 198 -> 175).
+// tiles of 128 x 64 and 128 x 128 with six and four stages on their way, for up
+// to 256 of 128 x 256 (eight waves, three stages). They read it
+// non-temporally: kept in the caches, it would only be driven out by the
+// head's gradient, which they can hold instead until it is written (32000 x
+// 4096 of 5 tokens 46.8 -> 42.3 us alone; 17 tokens with gradients 198 -> 175).
 TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (g.thin) {
         const uint32_t bb = g.nb <= 16 ? 16 : g.nb <= 32 ? 32 : 64;
@@ -1706,8 +1707,14 @@ TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
         const uint64_t turns = ((uint64_t(tiles) * s - 1) >> t.slot_bits) + 1;
         return turns * ((kt + s - 1) / s * segs + 4) * stage;
     };
-    // a turn's stage: 65536 outputs on a CU at 130, or 2 x 16384 at 105
-    if (cost(kBig, 2 * 105) <= cost(kMid, 130)) return kBig;
+    // A turn's stage: 65536 outputs on a CU, 2 x 16384, or 32768 for up to 256
+    // tokens, which read the head once (192 tokens x 32000 x 4096: logits 90 ->
+    // 77 us, with both gradients 305 -> 282).
+    const uint64_t big = cost(kBig, 2 * 105), mid = cost(kMid, 130);
+    if (low && g.tokens_in_b && segs == 1 && g.nb > 128 && g.nb <= 256 &&
+        cost(kWide, 107) < std::min(big, mid))
+        return kWide;
+    if (big <= mid) return kBig;
     // at most a workgroup a CU (half of one if the sums are split: more parts
     // serve better than more stages): more stages on their way
     const uint32_t tiles = uint32_t((g.na + 127) / 128) * uint32_t((g.nb + 127) / 128);
@@ -1723,6 +1730,18 @@ TileShape tile_of(const GemmArgs& g, bool f32, bool low) {
     return t;
 }
 
+// The forms that read the head once: non-temporally (NT) or kept.
+template <bool NT, bool AM, bool F32, int KIND>
+hipError_t pick_once(const GemmArgs& g, const TileShape& t, hipStream_t stream) {
+    if (t.form == kFormLow) return run_gemm<128, 64, 2, 2, 6, NT, AM, false, F32, KIND>(g, t, stream);
+    if constexpr (!F32)
+        if (t.form == kFormWide)
+            return run_gemm<128, 256, 2, 4, 3, NT, AM, false, F32, KIND>(g, t, stream);
+    if (t.form == kFormMidOnce)
+        return run_gemm<128, 128, 2, 2, 2, NT, AM, false, F32, KIND>(g, t, stream);
+    return run_gemm<128, 128, 2, 2, 4, NT, AM, false, F32, KIND>(g, t, stream);
+}
+
 template <bool AM, bool BM, bool F32, int KIND>
 hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
     const TileShape t = tile_of(g, F32, !BM);
@@ -1730,15 +1749,13 @@ hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
         if (t.form == kFormThin) return run_thin<AM, KIND>(g, t, stream);
     if (t.form == kFormBig)
         return run_gemm<256, 256, 4, 2, 2, false, AM, BM, F32, KIND>(g, t, stream);
-    if constexpr (!BM) {
-        if (t.form == kFormLow)
-            return run_gemm<128, 64, 2, 2, 6, !F32, AM, BM, F32, KIND>(g, t, stream);
+    if constexpr (BM) {
         if (t.form == kFormLow2)
-            return run_gemm<128, 128, 2, 2, 4, !F32, AM, BM, F32, KIND>(g, t, stream);
-        if (t.form == kFormMidOnce)  // fp32: the copied planes are read several times
-            return run_gemm<128, 128, 2, 2, 2, !F32, AM, BM, F32, KIND>(g, t, stream);
-    } else if (t.form == kFormLow2) {
-        return run_gemm<128, 128, 2, 2, 4, false, AM, BM, F32, KIND>(g, t, stream);
+            return run_gemm<128, 128, 2, 2, 4, false, AM, BM, F32, KIND>(g, t, stream);
+    } else if (t.form != kFormMid) {
+        if constexpr (!F32)  // fp32: the copied planes are read several times
+            if (!g.keep) return pick_once<true, AM, F32, KIND>(g, t, stream);
+        return pick_once<false, AM, F32, KIND>(g, t, stream);
     }
     return run_gemm<128, 128, 2, 2, 2, false, AM, BM, F32, KIND>(g, t, stream);
 }
@@ -1869,6 +1886,10 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     // What all tokens have in common comes to the gradients in fp32: a factor
     // of 1/96 within G would give every target's -1 the same error in bf16.
     const float factor = c.scale * c.temperature;
+    // Two reads of a head that the Infinity Cache (256 MiB) holds, and no write of
+    // its gradient between: few tokens let it stay there (100 tokens x 20000 x
+    // 5120: 142 -> 129 us; 131072 x 4096 of 5 tokens 406 -> 430).
+    const bool keep = s.grad_hidden && !s.grad_head && s.v * s.dp * 2 <= int64_t(1) << 28;
     void* p = grads ? ws + s.o_p : nullptr;
     uint16_t* gp = reinterpret_cast<uint16_t*>(ws + (F32 ? s.o_g : s.o_p));
     const int64_t g_plane = s.chunk * s.vp;
@@ -1880,6 +1901,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.a = w;
         l.b = x + first * s.dp;
         l.thin = s.thin;
+        l.keep = keep;
         l.a_width = l.lda = l.k_real = s.pack_head ? s.dp : s.d;
         l.ldb = s.dp;
         l.plane_a = w_plane;
@@ -1902,6 +1924,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.top_pad = s.top_pad;
         if (s.raw && len > 0) {
             GemmArgs h = raw_product(s, len);
+            h.keep = keep;
             h.a = w;
             h.b = l.b;
             h.count = count;
@@ -1951,6 +1974,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
 
         if (s.grad_hidden && len > 0) {
             GemmArgs h = hidden_product(s, len);
+            h.keep = keep;
             h.a = w;
             h.b = gp;
             h.count = count;

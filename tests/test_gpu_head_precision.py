@@ -101,3 +101,18 @@ def test_bf16_gradient_of_logits_far_apart(v, d):
     got, _ = columns_of_g(head, index, None, 1.0, None, n)
     want, cp, _ = definition(head, index, None, 1.0, None, n)
     within(got, want, B * want.abs() + (1 + B) * (2.0 ** -11 * cp + 2.0 ** -63.9), "G")
+
+
+@pytest.mark.parametrize("top", [0, 5])
+@pytest.mark.parametrize("n,v,d", [(16, 9000, 64), (64, 9001, 64), (67, 9001, 67), (300, 9001, 320),
+                                   (64, 700, 1024), (40, 5000, 1001)])
+def test_fp32_gradient_of_large_logits(n, v, d, top):
+    """An lse of about 3000 costs p nothing: it depends on l - lse."""
+    g = gen(n, v, d, top, "large")
+    head = 3000.0 + 2.0 * torch.randn(v, d, device="cuda", generator=g)
+    index = torch.randint(0, v, (n,) if not top else (n, top), device="cuda", generator=g)
+    logit = torch.randn(n, top, device="cuda", generator=g) if top else None
+    got, lse = columns_of_g(head, index, logit, 1.0, None, n)
+    want, cp, ref = definition(head, index, logit, 1.0, None, n)
+    within(got, want, 2.0 ** -17 * cp + 2 * U * want.abs(), "G")
+    within(lse, ref, 2.0 ** -18 + U * ref, "lse")

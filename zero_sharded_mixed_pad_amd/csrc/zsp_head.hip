@@ -1354,11 +1354,12 @@ __global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
     }
     if (!a.p) return;
 
-    const float l32 = float(lse);
+    // m_b - lse from 64 bits: rounded to fp32 first, an lse of 3000 would leave
+    // every p with an error of 1e-4
     if constexpr (F32) {
         const float* p = static_cast<const float*>(a.p) + r * a.ldp;
         for (int64_t i = from + t * 4; i < to; i += T * 4) {
-            const float f = c * fast_exp(part[i / kHeadBlock].x - l32);
+            const float f = c * fast_exp(float(double(part[i / kHeadBlock].x) - lse));
             const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
             uint16_t h[4][3];
 #pragma unroll
@@ -1374,7 +1375,7 @@ __global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
     } else {
         uint16_t* p = a.g + r * a.ldp;
         for (int64_t i = from + t * 8; i < to; i += T * 8) {
-            const float at = (part[i / kHeadBlock].x - l32) * kLog2e;
+            const float at = float(double(part[i / kHeadBlock].x) - lse) * kLog2e;
             u32x4 v = *reinterpret_cast<const u32x4*>(p + i);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -1462,11 +1463,11 @@ __global__ __launch_bounds__(T) void raw_join_kernel(RawArgs q) {
         if (a.lse) a.lse[token] = float(lse);
     }
     if (!a.p) return;
-    const float l32 = float(lse);
+    const float shift = float(double(m) - lse);  // as in join_kernel
     for (int i = t * 8; i < cols; i += T * 8) {
         float g[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * fast_exp(s_l[i + k] - l32) : 0.0f;
+        for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * fast_exp(s_l[i + k] - m + shift) : 0.0f;
         put_g8<F32>(a, r, i, g);
     }
     __threadfence_block();

@@ -526,10 +526,10 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * between calls; calls that may run at the same time, replays of captured
  * graphs among them, each need their own.
  *   ZSP_EINVAL: a bad dtype, a negative size, v or d of 0, a NULL or
- * misaligned argument, scale, temperature, their product or 1 / temperature
- * not finite, temperature <= 0, an output that overlaps another argument;
- * ZSP_ERANGE: a size beyond the limits, ws_bytes too small. n = 0: grad_head
- * is set to 0. */
+ * misaligned argument, scale, temperature, their product or log2(e) /
+ * temperature not finite, temperature <= 0, an output that overlaps another
+ * argument; ZSP_ERANGE: a size beyond the limits, ws_bytes too small. n = 0:
+ * grad_head is set to 0. */
 #define ZSP_HEAD_GRAD_HIDDEN 1 /* grad_hidden is wanted */
 #define ZSP_HEAD_GRAD_HEAD 2   /* grad_head is wanted */
 #define ZSP_HEAD_UNALIGNED 4   /* head may start off a 16-byte boundary */

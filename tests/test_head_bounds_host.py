@@ -1,0 +1,40 @@
+"""The losses over the head: bounds of their arguments, and what a workspace
+serves (host only)."""
+import torch
+
+import zero_sharded_mixed_pad_amd as zsp
+from zero_sharded_mixed_pad_amd import binding
+
+BASE = 1 << 40                 # addresses that are only compared
+EINVAL, ERANGE = binding.EINVAL, binding.ERANGE
+
+
+def call(n, v, d, dtype, top=0, ws_bytes=None, grads=(True, True), temperature=1.0, bad=True):
+    """The status of a call with good arguments but, where `bad`, the last that
+    is looked at: a loss off its alignment, refused with EINVAL if all others
+    (the workspace's size among them) are taken."""
+    size = 2 if dtype == torch.bfloat16 else 4
+    code = zsp.BF16 if size == 2 else zsp.F32
+    if ws_bytes is None:
+        ws_bytes = binding.zsp_head_workspace(n, v, d, dtype, top, *grads)
+    at, step = {}, BASE
+    for name, nbytes in (("hidden", n * d * size), ("head", v * d * size), ("index", n * max(top, 1) * 8),
+                         ("logit", n * top * 4), ("loss", n * 4), ("grad_hidden", n * d * size),
+                         ("grad_head", v * d * size), ("ws", ws_bytes)):
+        at[name] = step
+        step += (nbytes + 4096) // 4096 * 4096
+    at["loss"] += 2 * bad
+    head = [at["hidden"], at["head"], code, n, v, d]
+    tail = [None, 1.0, at["loss"], None, at["grad_hidden"] if grads[0] else None,
+            at["grad_head"] if grads[1] else None, at["ws"], ws_bytes, None]
+    if top:
+        return binding.lib.zsp_head_distill(*head, at["index"], at["logit"], top, temperature, *tail)
+    return binding.lib.zsp_head_loss(*head, at["index"], *tail)
+
+
+def test_temperature_whose_exponents_are_not_finite():
+    """1 / 3.5e-39 is finite, log2(e) times that is not: every p would be NaN."""
+    assert call(10, 100, 64, torch.bfloat16, 4, temperature=3.5e-39) == EINVAL
+    assert "temperature" in zsp.last_error()
+    assert call(10, 100, 64, torch.bfloat16, 4, temperature=4.3e-39) == EINVAL
+    assert "loss is not aligned" in zsp.last_error()

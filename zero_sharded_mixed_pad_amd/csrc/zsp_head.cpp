@@ -121,9 +121,11 @@ zsp_status head_call(HeadCall c, int64_t n, int64_t v, int64_t d, zsp_dtype dtyp
     HeadShape s;
     zsp_status st = make_shape(n, v, d, dtype, top, flags, &s);
     if (st != ZSP_OK) return st;
+    // the softmax's exponents are taken in units of T / log2(e)
     if (!(c.temperature > 0.0f) || !std::isfinite(c.temperature) ||
-        !std::isfinite(1.0f / c.temperature))
-        return set_error(ZSP_EINVAL, "temperature = %g is not above 0, or its inverse not finite",
+        !std::isfinite(1.0f / c.temperature * 1.4426950408889634f))
+        return set_error(ZSP_EINVAL,
+                         "temperature = %g is not above 0, or 1.4427 times its inverse not finite",
                          double(c.temperature));
     if (!std::isfinite(c.scale) || !std::isfinite(c.scale * c.temperature))
         return set_error(ZSP_EINVAL, "scale is not finite, or its product with the temperature");

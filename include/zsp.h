@@ -504,8 +504,9 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * token's entries those with an index outside [0, v) or a logit of -infinity
  * are left out; a token without any other does not count. An index that
  * occurs twice is two entries. The logits are not kept: a call with
- * gradients keeps the softmax of at most 4 GiB of its tokens at a time in
- * the workspace.
+ * gradients keeps the softmax of some of its tokens at a time in the
+ * workspace, up to 4 GiB, or of 256 tokens (64, of a call with no more) where
+ * those take more.
  *   hidden, head and the gradients are all of `dtype`. Products are summed
  * in fp32 (operands of fp32 type are split into three bf16 values, exactly,
  * and products below 2^-23 of a term left out; of an infinity, or a value

@@ -1,0 +1,59 @@
+"""The losses over the head keep to their workspace and outputs, on the GPU."""
+import zlib
+
+import pytest
+import torch
+
+import zero_sharded_mixed_pad_amd as zsp
+from zero_sharded_mixed_pad_amd import binding
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+GUARD = 1 << 16
+
+
+def gen(*key):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(zlib.crc32(repr(key).encode()))
+    return g
+
+
+def inputs(n, v, d, dtype, top):
+    g = gen(n, v, d, top)
+    x = torch.randn(n, d, device="cuda", generator=g).to(dtype)
+    w = (torch.randn(v, d, device="cuda", generator=g) * d ** -0.5).to(dtype)
+    index = torch.randint(0, v, (n, top) if top else (n,), device="cuda", generator=g)
+    return x, w, index, torch.randn(n, top, device="cuda", generator=g) if top else None
+
+
+def run(x, w, index, logit, ws, out, **more):
+    more.update(lse=out[1], grad_hidden=out[2], grad_head=out[3])
+    if logit is None:
+        zsp.head_loss(x, w, index, out[0], ws, **more)
+    else:
+        zsp.head_distill(x, w, index, logit, out[0], ws, temperature=1.5, **more)
+
+
+def outputs(x, w, fill=float("nan")):
+    n = len(x)
+    return [torch.full((n,), fill, device="cuda"), torch.full((n,), fill, device="cuda"),
+            torch.full_like(x, fill), torch.full_like(w, fill)]
+
+
+@pytest.mark.parametrize("top", [0, 3])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,v,d", [(1, 9001, 64), (16, 9001, 200), (33, 9100, 77), (64, 9001, 512),
+                                   (64, 700, 1024), (50, 300, 130), (65, 9001, 64), (300, 700, 96)])
+def test_nothing_behind_the_workspace_is_touched(n, v, d, dtype, top):
+    """Bytes behind it stay, and what they hold reaches no output."""
+    x, w, index, logit = inputs(n, v, d, dtype, top)
+    need = binding.zsp_head_workspace(n, v, d, dtype, top)
+    outs = []
+    for fill in (255, 0):
+        buf = torch.full((need + GUARD,), fill, dtype=torch.uint8, device="cuda")
+        outs.append(outputs(x, w))
+        run(x, w, index, logit, buf[:need], outs[-1])
+        assert (buf[need:] == fill).all()
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and not a.isnan().any()

@@ -38,3 +38,18 @@ def test_temperature_whose_exponents_are_not_finite():
     assert "temperature" in zsp.last_error()
     assert call(10, 100, 64, torch.bfloat16, 4, temperature=4.3e-39) == EINVAL
     assert "loss is not aligned" in zsp.last_error()
+
+
+def test_what_is_kept_of_the_largest_vocabulary():
+    """The softmax takes 10 bytes a column in fp32, 2 in bf16, and partials an
+    eighth of a byte a column: of up to 64 tokens 64 rows are kept, of more what
+    4 GiB hold and 256 rows at least."""
+    v, d = 1 << 22, 16
+    planes, acc, small = v * 64 * 2 * 3, v * 64 * 4, 1 << 26
+    size = lambda n, dt: binding.zsp_head_workspace(n, v, d, dt)  # noqa: E731
+    for n in (1, 17, 64):
+        assert size(n, torch.float32) < 64 * v * 10.125 + small
+        assert size(n, torch.bfloat16) < 64 * v * 2.125 + small
+    for n in (65, 256, 300, 5000):
+        assert size(n, torch.float32) < 256 * v * 10.125 + planes + acc + small
+        assert size(n, torch.bfloat16) < (1 << 32) * 2.125 / 2 + acc + small

@@ -11,7 +11,8 @@ namespace zsp {
 namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 23, kMaxVocab = int64_t(1) << 22, kMaxDepth = 65536;
-// The softmax of at most so many bytes is kept at a time.
+// The softmax of at most so many bytes is kept at a time, or of a tile's tokens
+// where those take more (fp32 beyond 1.6 million columns; 10.7 GB at 2^22).
 constexpr int64_t kKeptBytes = int64_t(1) << 32;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
@@ -38,7 +39,10 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.grad_hidden = flags & ZSP_HEAD_GRAD_HIDDEN;
     s.grad_head = flags & ZSP_HEAD_GRAD_HEAD;
     s.planes = s.f32 ? 3 : 1;
-    s.rows = up(n, kHeadTile);
+    // up to 64 tokens are in tiles of at most 64: one of 2^22 fp32 columns would
+    // else keep 10.7 GB, and keeps 2.7
+    const int64_t tile = n <= kHeadThin ? kHeadThin : kHeadTile;
+    s.rows = up(n, tile);
     s.vp = up(v, kHeadTile);
     s.dp = up(d, kHeadDepth);
     const bool aligned = !(flags & ZSP_HEAD_UNALIGNED);
@@ -49,7 +53,7 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     const int64_t per = grads ? s.vp * (s.f32 ? 4 + 2 * s.planes : 2) : s.vp / kHeadBlock * 8;
     int64_t chunk = std::max<int64_t>(kKeptBytes / per / kHeadTile * kHeadTile, kHeadTile);
     s.nchunk = std::max<int64_t>((n + chunk - 1) / chunk, 1);
-    s.chunk = up((n + s.nchunk - 1) / s.nchunk, kHeadTile);
+    s.chunk = up((n + s.nchunk - 1) / s.nchunk, tile);
     if (s.chunk > 0) s.nchunk = std::max<int64_t>((n + s.chunk - 1) / s.chunk, 1);
     if (!head_fits_launch(s))
         return set_error(ZSP_ERANGE, "n * d = %lld * %lld elements are too many", (long long)n,

@@ -1738,7 +1738,8 @@ TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
         // two workgroups a CU, or one where 64 tokens leave no room for them
         return {256, bb, bb == 64 ? 8u : 9u, kFormThin, kThinSegs};
     }
-    if (low && g.tokens_in_b && g.nb <= 64) return kLow;
+    // P and X of so many tokens are not padded past 64 rows
+    if (low && g.tokens_in_b && g.nb <= kHeadThin) return kLow;
     const bool few = low && g.tokens_in_b && g.nb <= 128;
     if (few && !g.slot_bits) return kLow2;
     auto cost = [&](TileShape t, uint64_t stage) {

@@ -11,12 +11,13 @@
 
 namespace zsp {
 
-constexpr int32_t kHeadTile = 256;       // rows and columns of P are padded to it
+constexpr int32_t kHeadTile = 256;       // rows (of more than 64 tokens) and columns of P are padded to it
 constexpr int32_t kHeadBlock = 64;       // vocabulary columns per partial of a softmax
 constexpr int32_t kHeadDepth = 64;       // d is padded to it
 constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
 constexpr int32_t kHeadFew = 128;        // tokens whose gradient of the head has a way of its own
-constexpr int32_t kHeadThin = 64;        // tokens that read an fp32 head in place
+constexpr int32_t kHeadThin = 64;        // tokens whose tiles hold so many at most; they read an
+                                         // fp32 head in place
 constexpr int32_t kHeadRawColumns = 8192;   // logits of a token that a workgroup keeps in LDS
 constexpr int32_t kHeadRawSmall = 4096;     // ... of 256 threads
 
@@ -31,7 +32,7 @@ struct HeadShape {
     bool raw = false;             // logits summed in parts, in the workspace
     int32_t planes = 1;           // bf16 planes of an operand: 3 hold an fp32 value
     int32_t top_pad = 1;          // entries per row in the workspace
-    int64_t rows = 0;             // n padded to kHeadTile
+    int64_t rows = 0;             // n padded to the tokens of a tile
     int64_t vp = 0, dp = 0;       // v padded to kHeadTile, d to kHeadDepth
     int64_t chunk = 0;            // tokens whose softmax is kept at a time
     int64_t nchunk = 0;

@@ -1,5 +1,8 @@
 """The losses over the head: bounds of their arguments, and what a workspace
 serves (host only)."""
+import time
+
+import pytest
 import torch
 
 import zero_sharded_mixed_pad_amd as zsp
@@ -53,3 +56,17 @@ def test_what_is_kept_of_the_largest_vocabulary():
     for n in (65, 256, 300, 5000):
         assert size(n, torch.float32) < 256 * v * 10.125 + planes + acc + small
         assert size(n, torch.bfloat16) < (1 << 32) * 2.125 / 2 + acc + small
+
+
+@pytest.mark.parametrize("n,v,d,dtype", [(1 << 23, 64, 64, torch.bfloat16), (1 << 22, 256, 2048, torch.bfloat16),
+                                         (1 << 23, 64, 1024, torch.float32)])
+def test_a_call_of_many_tokens_plans_in_a_moment(n, v, d, dtype):
+    """Parts of sums for every number of tokens that may count are bounded
+    without trying each (which took 4 to 8 ms here)."""
+    ws_bytes, least = binding.zsp_head_workspace(n, v, d, dtype), 1.0
+    for _ in range(5):
+        t0 = time.perf_counter()
+        assert call(n, v, d, dtype, ws_bytes=ws_bytes) == EINVAL
+        least = min(least, time.perf_counter() - t0)
+    assert "loss is not aligned" in zsp.last_error()
+    assert least < 1.5e-3, least

@@ -58,7 +58,7 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     if (!head_fits_launch(s))
         return set_error(ZSP_ERANGE, "n * d = %lld * %lld elements are too many", (long long)n,
                          (long long)d);
-    s.raw = head_is_raw(s);
+    head_products(&s);
 
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -82,7 +82,7 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.o_part = take(s.chunk * (s.vp / kHeadBlock) * 8);
     if (grads) s.o_p = take(s.chunk * s.vp * (s.f32 ? 4 : 2));
     if (grads && s.f32) s.o_g = take(s.chunk * s.vp * 2 * s.planes);
-    s.o_split = take(head_split_bytes(s));
+    s.o_split = take(s.split_bytes);
     if (s.grad_head && s.nchunk > 1) s.o_acc = take(v * s.dp * 4);
     s.bytes = at;
     *out = s;

@@ -1651,50 +1651,82 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a) {
 // A product's tiles: columns and rows of a tile, how many the card runs at once
 // (log2), and which form.
 enum Form { kFormBig, kFormWide, kFormMid, kFormMidOnce, kFormLow, kFormLow2, kFormThin };
-struct TileShape {
-    uint32_t ba, bb, slot_bits;
-    Form form;
-    uint32_t segs = 1;  // stages of a step of 64 k's
-};
-constexpr TileShape kBig{256, 256, 8, kFormBig}, kWide{128, 256, 8, kFormWide},
+constexpr HeadTiles kBig{256, 256, 8, kFormBig}, kWide{128, 256, 8, kFormWide},
     kMid{128, 128, 9, kFormMid}, kMidOnce{128, 128, 9, kFormMidOnce},
     kLow{128, 64, 8, kFormLow}, kLow2{128, 128, 8, kFormLow2};
 
-// Largest number of items (tiles times parts) and of partial rows times parts
-// over every number of tokens up to the call's.
-struct Bound {
-    uint64_t items = 0, split_rows = 0;
-};
-Bound bound_of(const GemmArgs& g, TileShape t) {
-    Bound m;
-    const uint32_t ta = uint32_t((g.na + t.ba - 1) / t.ba), tb = uint32_t((g.nb + t.bb - 1) / t.bb);
-    const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
-    auto one = [&](uint32_t b, uint32_t k) {
-        const uint32_t s = split_of(ta * b, k, t.segs, g.slot_bits ? t.slot_bits : 0);
-        m.items = std::max<uint64_t>(m.items, uint64_t(ta) * b * s);
+uint32_t tiles_along(int64_t extent, uint32_t tile) { return uint32_t((extent + tile - 1) / tile); }
+uint32_t stages_of(int64_t k) { return uint32_t((k + kHeadDepth - 1) / kHeadDepth); }
+
+// Where split_of may answer more than 1: two parts take two stages of eight at
+// least, and parts save less than one turn of 16 x stages, while s of them cost
+// the joining of tiles * s and the ends of the further turns: nothing is saved
+// beyond eight tiles a stage. (The host's bound: on the device the test takes as
+// long as what it spares, 333 tokens x 10007 x 768 fp32 138 -> 141 us.)
+bool split_may_pay(uint32_t tiles, uint32_t stages, uint32_t segs, uint32_t slot_bits) {
+    return slot_bits != 0 && tiles != 0 && tiles >> slot_bits < 64 && stages * segs >= 16 &&
+           tiles < stages * segs * 8 + 32;
+}
+
+// The most parts that split_of makes of sums of up to `stages`, by trying all
+// lengths from the longest on, until the largest number is met that a smaller
+// one does not beat at every length: with costs between those of k / s stages
+// and of (k + s - 1) / s, which are straight lines, at both ends of its range.
+uint32_t most_parts(uint32_t tiles, uint32_t stages, uint32_t segs, uint32_t slot_bits) {
+    if (!split_may_pay(tiles, stages, segs, slot_bits)) return 1;
+    constexpr uint32_t kParts[] = {2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64};  // split_of's
+    auto turns = [&](uint32_t s) { return double((tiles * s + (1u << slot_bits) - 1) >> slot_bits); };
+    auto cost = [&](uint32_t s, double part) {
+        return turns(s) * (part * segs + 4) * 16 + (s > 1 ? double(tiles) * s : 0.0);
+    };
+    uint32_t largest = 1;
+    for (uint32_t s : kParts) {
+        const uint32_t from = std::max(s, (s * 8 + segs - 1) / segs);  // its shortest sum
+        if (from > stages || turns(s) > 64) continue;
+        auto beats = [&](uint32_t o) {
+            auto better = [&](double k) { return cost(o, (k + o - 1) / o) <= cost(s, k / s); };
+            return better(from) && better(stages);
+        };
+        bool beaten = beats(1);
+        for (uint32_t o : kParts)
+            if (o < s) beaten |= beats(o);
+        if (!beaten) largest = s;
+    }
+    uint32_t most = 1;
+    for (uint32_t k = stages; k > 0 && most < largest; --k)
+        most = std::max(most, split_of(tiles, k, segs, slot_bits));
+    return most;
+}
+
+// t with the largest number of items (tiles times parts) and of partial rows
+// times parts over every number of tokens up to the call's. Asked once a call,
+// and within split_may_pay's and most_parts' bounds, since the host waits for it
+// (2^20 tokens x 64 x 64 1000 us by trying every number of tiles, now 4).
+HeadTiles bounded(const GemmArgs& g, HeadTiles t) {
+    const uint32_t ta = tiles_along(g.na, t.ba), tb = tiles_along(g.nb, t.bb);
+    const uint32_t kt = stages_of(g.k), slot_bits = g.slot_bits ? t.slot_bits : 0;
+    auto take = [&](uint32_t b, uint32_t s) {
+        t.items = std::max<uint64_t>(t.items, uint64_t(ta) * b * s);
         if (s > 1)
-            m.split_rows = std::max<uint64_t>(m.split_rows,
+            t.split_rows = std::max<uint64_t>(t.split_rows,
                                               s * std::min<uint64_t>(uint64_t(b) * t.bb, g.nb));
     };
-    // a split needs turns: past 64 of them there is none
-    if (g.tokens_in_b)
-        for (uint32_t b = tb; b > 0; --b) {
-            one(b, kt);
-            if (!g.slot_bits) break;
-        }
-    else if (g.tokens_in_k)
-        for (uint32_t k = 0; k <= kt; ++k) one(tb, k);
-    else
-        one(tb, kt);
-    return m;
+    t.items = t.split_rows = 0;
+    if (g.tokens_in_k) {
+        take(tb, most_parts(ta * tb, kt, t.segs, slot_bits));
+        return t;
+    }
+    take(tb, split_of(ta * tb, kt, t.segs, slot_bits));
+    for (uint32_t b = 1; g.tokens_in_b && b < tb && split_may_pay(ta * b, kt, t.segs, slot_bits); ++b)
+        take(b, split_of(ta * b, kt, t.segs, slot_bits));
+    return t;
 }
 
 // The parts of a split product joined, unless the caller does it.
 template <bool F32, int KIND>
-hipError_t join_parts(const GemmArgs& g, TileShape t, const Bound& m, hipError_t e,
-                      hipStream_t stream) {
+hipError_t join_parts(const GemmArgs& g, const HeadTiles& t, hipError_t e, hipStream_t stream) {
     if constexpr (KIND == kOut) {
-        if (e == hipSuccess && m.split_rows && !g.keep_parts) {
+        if (e == hipSuccess && t.split_rows && !g.keep_parts) {
             SplitArgs q{g, t.ba, t.bb, t.segs, uint32_t((g.ldo + 1023) / 1024)};
             const int64_t rows = g.nb * q.parts;
             split_kernel<F32><<<uint32_t(std::min<int64_t>(rows, 4096)), 256, 0, stream>>>(q);
@@ -1705,26 +1737,24 @@ hipError_t join_parts(const GemmArgs& g, TileShape t, const Bound& m, hipError_t
 }
 
 template <int BA, int BB, int WA, int WB, int NST, bool NT, bool AM, bool BM, bool F32, int KIND>
-hipError_t run_gemm(GemmArgs g, TileShape t, hipStream_t stream) {
+hipError_t run_gemm(GemmArgs g, const HeadTiles& t, hipStream_t stream) {
     static_assert(BA <= kHeadTile && BB <= kHeadTile, "");
     if (g.slot_bits) g.slot_bits = t.slot_bits;
-    const Bound m = bound_of(g, t);
-    if (m.items == 0) return hipSuccess;
+    if (t.items == 0) return hipSuccess;
     gemm_kernel<BA, BB, WA, WB, NST, NT, AM, BM, F32, KIND>
-        <<<uint32_t((m.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
-    return join_parts<F32, KIND>(g, t, m, hipGetLastError(), stream);
+        <<<uint32_t((t.items + 7) / 8 * 8), 64 * WA * WB, 0, stream>>>(g);
+    return join_parts<F32, KIND>(g, t, hipGetLastError(), stream);
 }
 
 template <bool AM, int KIND>
-hipError_t run_thin(GemmArgs g, TileShape t, hipStream_t stream) {
+hipError_t run_thin(GemmArgs g, const HeadTiles& t, hipStream_t stream) {
     if (g.slot_bits) g.slot_bits = t.slot_bits;
-    const Bound m = bound_of(g, t);
-    if (m.items == 0) return hipSuccess;
-    const uint32_t grid = uint32_t((m.items + 7) / 8 * 8);
+    if (t.items == 0) return hipSuccess;
+    const uint32_t grid = uint32_t((t.items + 7) / 8 * 8);
     if (t.bb == 16) thin_kernel<1, AM, KIND><<<grid, 256, 0, stream>>>(g);
     else if (t.bb == 32) thin_kernel<2, AM, KIND><<<grid, 256, 0, stream>>>(g);
     else thin_kernel<4, AM, KIND><<<grid, 256, 0, stream>>>(g);
-    return join_parts<true, KIND>(g, t, m, hipGetLastError(), stream);
+    return join_parts<true, KIND>(g, t, hipGetLastError(), stream);
 }
 
 // Tiles of 256 x 256 (eight waves, one workgroup on a CU) reach 1.3 PFLOP/s
@@ -1736,7 +1766,7 @@ hipError_t run_thin(GemmArgs g, TileShape t, hipStream_t stream) {
 // non-temporally: kept in the caches, it would only be driven out by the
 // head's gradient, which they can hold instead until it is written (32000 x
 // 4096 of 5 tokens 46.8 -> 42.3 us alone; 17 tokens with gradients 198 -> 175).
-TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
+HeadTiles shape_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (g.thin) {
         const uint32_t bb = g.nb <= 16 ? 16 : g.nb <= 32 ? 32 : 64;
         // two workgroups a CU, or one where 64 tokens leave no room for them
@@ -1746,9 +1776,9 @@ TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (low && g.tokens_in_b && g.nb <= kHeadThin) return kLow;
     const bool few = low && g.tokens_in_b && g.nb <= 128;
     if (few && !g.slot_bits) return kLow2;
-    auto cost = [&](TileShape t, uint64_t stage) {
-        const uint32_t tiles = uint32_t((g.na + t.ba - 1) / t.ba) * uint32_t((g.nb + t.bb - 1) / t.bb);
-        const uint32_t kt = uint32_t((g.k + kHeadDepth - 1) / kHeadDepth);
+    auto cost = [&](HeadTiles t, uint64_t stage) {
+        const uint32_t tiles = tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb);
+        const uint32_t kt = stages_of(g.k);
         const uint32_t s = split_of(tiles, kt, segs, g.slot_bits ? t.slot_bits : 0);
         const uint64_t turns = ((uint64_t(tiles) * s - 1) >> t.slot_bits) + 1;
         return turns * ((kt + s - 1) / s * segs + 4) * stage;
@@ -1763,22 +1793,21 @@ TileShape shape_of(const GemmArgs& g, uint32_t segs, bool low) {
     if (big <= mid) return kBig;
     // at most a workgroup a CU (half of one if the sums are split: more parts
     // serve better than more stages): more stages on their way
-    const uint32_t tiles = uint32_t((g.na + 127) / 128) * uint32_t((g.nb + 127) / 128);
-    const uint32_t parts = split_of(tiles, uint32_t((g.k + kHeadDepth - 1) / kHeadDepth), segs,
-                                    g.slot_bits ? kMid.slot_bits : 0);
+    const uint32_t tiles = tiles_along(g.na, 128) * tiles_along(g.nb, 128);
+    const uint32_t parts = split_of(tiles, stages_of(g.k), segs, g.slot_bits ? kMid.slot_bits : 0);
     if (tiles * parts <= (g.slot_bits ? 128u : 256u)) return kLow2;
     return few ? kMidOnce : kMid;
 }
 
-TileShape tile_of(const GemmArgs& g, bool f32, bool low) {
-    TileShape t = shape_of(g, f32 ? 6 : 1, low);
+HeadTiles tile_of(const GemmArgs& g, bool f32, bool low) {
+    HeadTiles t = shape_of(g, f32 ? 6 : 1, low);
     if (t.form != kFormThin) t.segs = f32 ? 6 : 1;
     return t;
 }
 
 // The forms that read the head once: non-temporally (NT) or kept.
 template <bool NT, bool AM, bool F32, int KIND>
-hipError_t pick_once(const GemmArgs& g, const TileShape& t, hipStream_t stream) {
+hipError_t pick_once(const GemmArgs& g, const HeadTiles& t, hipStream_t stream) {
     if (t.form == kFormLow) return run_gemm<128, 64, 2, 2, 6, NT, AM, false, F32, KIND>(g, t, stream);
     if constexpr (!F32)
         if (t.form == kFormWide)
@@ -1789,8 +1818,7 @@ hipError_t pick_once(const GemmArgs& g, const TileShape& t, hipStream_t stream) 
 }
 
 template <bool AM, bool BM, bool F32, int KIND>
-hipError_t pick_gemm(const GemmArgs& g, hipStream_t stream) {
-    const TileShape t = tile_of(g, F32, !BM);
+hipError_t pick_gemm(const GemmArgs& g, const HeadTiles& t, hipStream_t stream) {
     if constexpr (F32 && !BM)
         if (t.form == kFormThin) return run_thin<AM, KIND>(g, t, stream);
     if (t.form == kFormBig)
@@ -1943,6 +1971,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     float* acc = reinterpret_cast<float*>(ws + s.o_acc);
     for (int64_t ch = 0; ch < s.nchunk; ++ch) {
         const int64_t first = ch * s.chunk, len = std::min(s.chunk, s.n - first);
+        const bool last = ch + 1 == s.nchunk;
         GemmArgs l{};
         l.a = w;
         l.b = x + first * s.dp;
@@ -1977,8 +2006,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.first = first;
             h.split = h.acc_out = split;
             h.keep_parts = 1;
-            const TileShape t = tile_of(h, F32, true);
-            if ((e = pick_gemm<false, false, F32, kOut>(h, stream)) != hipSuccess) return e;
+            const HeadTiles& t = s.raw_tiles;
+            if ((e = pick_gemm<false, false, F32, kOut>(h, t, stream)) != hipSuccess) return e;
             JoinArgs j{nullptr, 0, blocks, count, first, rows + first, coef + first, l.entry,
                        nullptr, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
                        c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
@@ -1991,7 +2020,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
                 raw_join_kernel<F32, 1024, kHeadRawColumns><<<grid, 1024, 0, stream>>>(q);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         } else if (len > 0 &&
-                   (e = pick_gemm<false, false, F32, kLogits>(l, stream)) != hipSuccess) {
+                   (e = pick_gemm<false, false, F32, kLogits>(l, bounded(l, tile_of(l, F32, true)), stream)) !=
+                       hipSuccess) {
             return e;
         }
 
@@ -2029,7 +2059,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.factor = factor;
             h.rows = rows + first;
             h.split = split;
-            if ((e = pick_gemm<true, false, F32, kOut>(h, stream)) != hipSuccess) return e;
+            if ((e = pick_gemm<true, false, F32, kOut>(h, s.hidden_tiles[last], stream)) != hipSuccess) return e;
         }
         if (few_tokens) {
             const OuterArgs o{xt, gp, static_cast<uint16_t*>(c.grad_head), count, s.v, s.d, s.dp,
@@ -2047,7 +2077,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.split = split;
             h.acc_in = ch > 0 ? acc : nullptr;
             h.acc_out = ch + 1 < s.nchunk ? acc : nullptr;
-            if ((e = pick_gemm<true, true, F32, kOut>(h, stream)) != hipSuccess) return e;
+            if ((e = pick_gemm<true, true, F32, kOut>(h, s.head_tiles[last], stream)) != hipSuccess) return e;
         }
     }
     return hipSuccess;
@@ -2055,37 +2085,43 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
 
 }  // namespace
 
-// Whether the logits' sums are worth splitting: a row of them has to fit LDS
-// beside others, and the whole product to leave most of the card idle. With
-// rows of up to 32768 logits taken this way, 96 tokens x 32000 x 4096 with the
-// head's gradient take 231 us in place of 195.
-bool head_is_raw(const HeadShape& s) {
-    if (s.n == 0 || s.v > kHeadRawColumns || s.nchunk > 1) return false;
-    const GemmArgs h = raw_product(s, s.n);
-    const TileShape t = tile_of(h, s.f32, true);
-    const uint32_t tiles = uint32_t((h.na + t.ba - 1) / t.ba) * uint32_t((h.nb + t.bb - 1) / t.bb);
-    return split_of(tiles, uint32_t(h.k) / kHeadDepth, t.segs, t.slot_bits) > 1;
-}
-
 // A launch holds below 2^32 threads. The others' are bounded by n, or by what
 // is kept at a time.
 bool head_fits_launch(const HeadShape& s) {
     return setup_grid(s).all() * kSetupThreads < int64_t(1) << 32;
 }
 
-int64_t head_split_bytes(const HeadShape& s) {
+// Whether the logits' sums are worth splitting: a row of them has to fit LDS
+// beside others, and the whole product to leave most of the card idle. With
+// rows of up to 32768 logits taken this way, 96 tokens x 32000 x 4096 with the
+// head's gradient take 231 us in place of 195.
+void head_products(HeadShape* s) {
+    auto tiles = [&](const GemmArgs& g, bool low) { return bounded(g, tile_of(g, s->f32, low)); };
     int64_t bytes = 0;
-    for (int64_t ch = 0; ch < s.nchunk; ++ch) {
-        const int64_t len = std::min(s.chunk, s.n - ch * s.chunk);
-        auto add = [&](const GemmArgs& h, bool low, int64_t rows) {
-            const Bound m = bound_of(h, tile_of(h, s.f32, low));
-            bytes = std::max(bytes, std::max(int64_t(m.split_rows), rows) * h.ldf * 4);
-        };
-        if (s.raw && len > 0) add(raw_product(s, len), true, len);
-        if (s.grad_hidden && len > 0) add(hidden_product(s, len), true, 0);
-        if (s.grad_head) add(head_product(s, len), false, 0);
+    auto add = [&](const GemmArgs& g, const HeadTiles& t, int64_t rows) {
+        bytes = std::max(bytes, std::max(int64_t(t.split_rows), rows) * g.ldf * 4);
+    };
+    s->raw = false;
+    if (s->n > 0 && s->v <= kHeadRawColumns && s->nchunk == 1) {
+        const GemmArgs g = raw_product(*s, s->n);
+        const HeadTiles t = tile_of(g, s->f32, true);
+        s->raw = split_of(tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb), stages_of(g.k), t.segs,
+                          t.slot_bits) > 1;
+        if (s->raw) add(g, s->raw_tiles = bounded(g, t), s->n);
     }
-    return bytes;
+    for (int last = 0; last < 2; ++last) {
+        const int64_t len = last ? s->n - (s->nchunk - 1) * s->chunk : s->chunk;
+        if (!last && s->nchunk == 1) continue;
+        if (s->grad_hidden && len > 0) {
+            const GemmArgs g = hidden_product(*s, len);
+            add(g, s->hidden_tiles[last] = tiles(g, true), 0);
+        }
+        if (s->grad_head) {
+            const GemmArgs g = head_product(*s, len);
+            add(g, s->head_tiles[last] = tiles(g, false), 0);
+        }
+    }
+    s->split_bytes = bytes;
 }
 
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {

@@ -21,6 +21,17 @@ constexpr int32_t kHeadThin = 64;        // tokens whose tiles hold so many at m
 constexpr int32_t kHeadRawColumns = 8192;   // logits of a token that a workgroup keeps in LDS
 constexpr int32_t kHeadRawSmall = 4096;     // ... of 256 threads
 
+// How a product is cut: columns and rows of a tile, how many the card runs at
+// once (log2), which form, and the most of a call that the device may make of
+// them once it knows the tokens that count.
+struct HeadTiles {
+    uint32_t ba = 0, bb = 0, slot_bits = 0;
+    int32_t form = 0;
+    uint32_t segs = 1;            // stages of a step of 64 k's
+    uint64_t items = 0;           // tiles times the parts of their sums
+    uint64_t split_rows = 0;      // rows times parts, where sums are split
+};
+
 // Sizes of a call, and the byte offsets of its parts of the workspace.
 struct HeadShape {
     int64_t n = 0, v = 0, d = 0;
@@ -36,6 +47,9 @@ struct HeadShape {
     int64_t vp = 0, dp = 0;       // v padded to kHeadTile, d to kHeadDepth
     int64_t chunk = 0;            // tokens whose softmax is kept at a time
     int64_t nchunk = 0;
+    HeadTiles raw_tiles;          // of the logits in parts
+    HeadTiles hidden_tiles[2], head_tiles[2];   // the gradients' of a chunk, and of the last one
+    int64_t split_bytes = 0;      // for the parts of the sums that are split
     // offsets
     int64_t o_count = 0, o_rows = 0, o_coef = 0, o_entry = 0, o_pick = 0, o_teach = 0, o_start = 0,
             o_flag = 0, o_x = 0, o_xt = 0, o_w = 0, o_part = 0, o_p = 0, o_g = 0, o_split = 0, o_acc = 0;
@@ -58,10 +72,9 @@ struct HeadCall {
 
 // Whether its rows can be set up in one launch.
 bool head_fits_launch(const HeadShape& s);
-// Whether a call's logits are summed in parts.
-bool head_is_raw(const HeadShape& s);
-// Bytes for the parts of the sums that are split.
-int64_t head_split_bytes(const HeadShape& s);
+// How its products are cut, whether its logits are summed in parts, and the
+// bytes for parts of sums.
+void head_products(HeadShape* s);
 // Every launch of a call, in order, on `stream`.
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream);
 

@@ -105,3 +105,18 @@ def test_chunks_without_a_token_that_counts_cost_next_to_nothing():
         least.append(min(times[1:]))
     print("ms of 2 and 12 chunks", least)
     assert (least[1] - least[0]) / 10 < 0.15, least
+
+
+@pytest.mark.parametrize("n,m,v,d,dtype,top", [(130, 127, 9000, 4096, BF, 0), (300, 33, 9000, 512, F32, 0),
+                                               (900, 257, 700, 2048, BF, 4), (2500, 2000, 1 << 20, 64, BF, 0)])
+def test_a_smaller_last_batch(n, m, v, d, dtype, top):
+    """With the workspace of the others, whose parts it cuts otherwise."""
+    x, w, index, logit = inputs(n, v, d, dtype, top)
+    ws = zsp.head_workspace(n, v, d, dtype, top=top)
+    for k in (n, m, n, m):
+        out, own = outputs(x[:k], w), outputs(x[:k], w)
+        few = (x[:k], w, index[:k], logit if logit is None else logit[:k])
+        run(*few, ws, out)
+        run(*few, zsp.head_workspace(k, v, d, dtype, top=top), own)
+        for a, b in zip(out, own):
+            assert torch.equal(a, b) and not a.isnan().any()

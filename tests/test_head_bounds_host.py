@@ -1,5 +1,6 @@
 """The losses over the head: bounds of their arguments, and what a workspace
 serves (host only)."""
+import random
 import time
 
 import pytest
@@ -70,3 +71,37 @@ def test_a_call_of_many_tokens_plans_in_a_moment(n, v, d, dtype):
         least = min(least, time.perf_counter() - t0)
     assert "loss is not aligned" in zsp.last_error()
     assert least < 1.5e-3, least
+
+
+SERVED = [(300, 32000, 4096, torch.bfloat16, 0), (130, 32000, 4096, torch.bfloat16, 0),
+          (8457, 50257, 2048, torch.float32, 0), (70000, 32000, 64, torch.bfloat16, 0),
+          (200, 1000, 1003, torch.float32, 5), (400, 6000, 4096, torch.bfloat16, 0),
+          (2000, 130, 512, torch.float32, 1), (64, 5000, 2048, torch.float32, 0),
+          (3000, 1 << 20, 128, torch.bfloat16, 8), (90000, 256, 8192, torch.bfloat16, 0)]
+
+
+@pytest.mark.parametrize("n,v,d,dtype,top", SERVED)
+@pytest.mark.parametrize("grads", [(True, True), (True, False), (False, False)])
+def test_a_workspace_serves_fewer_tokens(n, v, d, dtype, top, grads):
+    """One sized for the largest batch takes every smaller one, also where its
+    sums are cut into more parts or its chunks are larger."""
+    ws_bytes = binding.zsp_head_workspace(n, v, d, dtype, top, *grads)
+    near = [m + o for m in (64, 128, 192, 256, 512, n // 2, n // 3) for o in (-1, 0, 1)]
+    for m in sorted({1, 16, 17, 32, 33, *near, *range(1, n, max(1, n // 400)), n}):
+        if m <= n:
+            assert call(m, v, d, dtype, top, ws_bytes, grads) == EINVAL
+            assert "loss is not aligned" in zsp.last_error(), (m, zsp.last_error())
+            assert binding.zsp_head_workspace(m, v, d, dtype, top, *grads) <= ws_bytes
+
+
+def test_workspaces_serve_fewer_tokens_whatever_the_sizes():
+    rng = random.Random(11)
+    log = lambda lo, hi: int(2 ** rng.uniform(lo, hi))  # noqa: E731
+    for _ in range(4000):
+        n, v, d = log(0, 18), log(0, 20), log(0, 13)
+        dtype = rng.choice([torch.bfloat16, torch.float32])
+        top, grads = rng.choice([0, 0, 3]), (rng.random() < 0.7, rng.random() < 0.7)
+        ws_bytes = binding.zsp_head_workspace(n, v, d, dtype, top, *grads)
+        for m in {rng.randint(1, n), log(0, n.bit_length()) % n + 1, n}:
+            assert call(m, v, d, dtype, top, ws_bytes, grads) == EINVAL
+            assert "loss is not aligned" in zsp.last_error(), (n, m, v, d, dtype, top, grads)

@@ -17,6 +17,39 @@ constexpr int64_t kKeptBytes = int64_t(1) << 32;
 
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
+// The workspace's parts, one behind another. All grow with the tokens but the
+// copy of X^T, which calls of more than a few do without, and the parts of sums
+// (split_bytes).
+void lay_out(HeadShape* s) {
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t o = at;
+        at = up(at + bytes, 256);
+        return o;
+    };
+    const bool grads = s->grad_hidden || s->grad_head;
+    s->o_count = take(4);
+    s->o_rows = take(s->rows * 4);
+    s->o_coef = take(s->rows * 4);
+    s->o_entry = take(s->rows * s->top_pad * 4);
+    s->o_pick = take(s->rows * s->top_pad * 4);
+    if (s->teacher) {
+        s->o_flag = take(s->n);
+        s->o_teach = take(s->rows * s->top_pad * 4);
+        if (s->top > 1) s->o_start = take(s->n * ((s->v + kHeadBlock - 1) / kHeadBlock + 1) * 2);
+    }
+    s->o_x = take(s->rows * s->dp * 2 * s->planes);
+    s->o_xt = take(s->xt_tokens * s->dp * 2);
+    if (s->pack_head) s->o_w = take(s->v * s->dp * 2 * s->planes);
+    s->o_part = take(s->chunk * (s->vp / kHeadBlock) * 8);
+    if (grads) s->o_p = take(s->chunk * s->vp * (s->f32 ? 4 : 2));
+    if (grads && s->f32) s->o_g = take(s->chunk * s->vp * 2 * s->planes);
+    s->o_split = take(s->split_bytes);
+    if (s->grad_head && s->nchunk > 1) s->o_acc = take(s->v * s->dp * 4);
+    s->bytes = at;
+}
+
+// What a call of n tokens takes.
 zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
                       int32_t flags, HeadShape* out) {
     if (dtype != ZSP_F32 && dtype != ZSP_BF16) return set_error(ZSP_EINVAL, "bad dtype %d", dtype);
@@ -46,45 +79,22 @@ zsp_status make_shape(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t 
     s.vp = up(v, kHeadTile);
     s.dp = up(d, kHeadDepth);
     const bool aligned = !(flags & ZSP_HEAD_UNALIGNED);
-    s.thin = s.f32 && n <= kHeadThin && d % 4 == 0 && aligned;
+    s.in_place = s.f32 && d % 4 == 0 && aligned;
+    s.thin = s.in_place && n <= kHeadThin;
     s.pack_head = s.f32 ? !s.thin : d % 8 != 0 || !aligned;
+    if (s.grad_head && !s.f32 && n <= kHeadFew) s.xt_tokens = up(n, 32);
     const bool grads = s.grad_hidden || s.grad_head;
     // per token: P (and its planes), or the partials alone
     const int64_t per = grads ? s.vp * (s.f32 ? 4 + 2 * s.planes : 2) : s.vp / kHeadBlock * 8;
-    int64_t chunk = std::max<int64_t>(kKeptBytes / per / kHeadTile * kHeadTile, kHeadTile);
-    s.nchunk = std::max<int64_t>((n + chunk - 1) / chunk, 1);
+    s.chunk_most = std::max<int64_t>(kKeptBytes / per / kHeadTile * kHeadTile, kHeadTile);
+    s.nchunk = std::max<int64_t>((n + s.chunk_most - 1) / s.chunk_most, 1);
     s.chunk = up((n + s.nchunk - 1) / s.nchunk, tile);
     if (s.chunk > 0) s.nchunk = std::max<int64_t>((n + s.chunk - 1) / s.chunk, 1);
     if (!head_fits_launch(s))
         return set_error(ZSP_ERANGE, "n * d = %lld * %lld elements are too many", (long long)n,
                          (long long)d);
     head_products(&s);
-
-    int64_t at = 0;
-    auto take = [&](int64_t bytes) {
-        const int64_t o = at;
-        at = up(at + bytes, 256);
-        return o;
-    };
-    s.o_count = take(4);
-    s.o_rows = take(s.rows * 4);
-    s.o_coef = take(s.rows * 4);
-    s.o_entry = take(s.rows * s.top_pad * 4);
-    s.o_pick = take(s.rows * s.top_pad * 4);
-    if (s.teacher) {
-        s.o_flag = take(n);
-        s.o_teach = take(s.rows * s.top_pad * 4);
-        if (s.top > 1) s.o_start = take(n * ((v + kHeadBlock - 1) / kHeadBlock + 1) * 2);
-    }
-    s.o_x = take(s.rows * s.dp * 2 * s.planes);
-    if (s.grad_head && !s.f32 && n <= kHeadFew) s.o_xt = take(up(n, 32) * s.dp * 2);
-    if (s.pack_head) s.o_w = take(v * s.dp * 2 * s.planes);
-    s.o_part = take(s.chunk * (s.vp / kHeadBlock) * 8);
-    if (grads) s.o_p = take(s.chunk * s.vp * (s.f32 ? 4 : 2));
-    if (grads && s.f32) s.o_g = take(s.chunk * s.vp * 2 * s.planes);
-    s.o_split = take(s.split_bytes);
-    if (s.grad_head && s.nchunk > 1) s.o_acc = take(v * s.dp * 4);
-    s.bytes = at;
+    lay_out(&s);
     *out = s;
     return ZSP_OK;
 }
@@ -174,8 +184,14 @@ zsp_status zsp_head_workspace(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, 
     if (!bytes) return set_error(ZSP_EINVAL, "bytes is NULL");
     HeadShape s;
     const zsp_status st = make_shape(n, v, d, dtype, top, flags, &s);
-    if (st == ZSP_OK) *bytes = s.bytes;
-    return st;
+    if (st != ZSP_OK) return st;
+    // of every call of up to n tokens, whose parts of sums or chunks may be larger
+    s.split_bytes = head_split_most(s);
+    s.chunk = std::min(s.rows, s.chunk_most);
+    if (s.grad_head && !s.f32) s.xt_tokens = up(std::min<int64_t>(n, kHeadFew), 32);
+    lay_out(&s);
+    *bytes = s.bytes;
+    return ZSP_OK;
 }
 
 zsp_status zsp_head_loss(const void* hidden, const void* head, zsp_dtype dtype, int64_t n,

@@ -2124,6 +2124,64 @@ void head_products(HeadShape* s) {
     s->split_bytes = bytes;
 }
 
+// By asking every number of tokens which form it takes (64 of them at a time,
+// and the in-place forms' 16 and 32: what the choice goes by does not change
+// between), then each form for the most that it serves. Past kAsked tokens, all
+// forms that those may take.
+int64_t head_split_most(const HeadShape& s) {
+    constexpr int64_t kAsked = 65536;
+    const int64_t most = std::min(s.n, s.chunk_most);
+    const bool thin = s.in_place;
+    int64_t bytes = 0;
+    auto product = [&](auto make, bool low, bool raw) {
+        struct Seen {
+            HeadTiles t;
+            int64_t len;
+            bool thin;
+        } seen[12];
+        int count = 0;
+        auto note = [&](const HeadTiles& t, int64_t len, bool in_place) {
+            int i = 0;
+            while (i < count && (seen[i].t.form != t.form || seen[i].t.bb != t.bb)) ++i;
+            if (i == count) seen[count++] = {t, len, in_place};
+            else seen[i].len = std::max(seen[i].len, len);
+        };
+        HeadShape q = s;
+        auto ask = [&](int64_t len, bool in_place) {
+            q.thin = in_place;
+            const GemmArgs g = make(q, len);
+            const HeadTiles t = tile_of(g, s.f32, low);
+            if (raw && split_of(tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb), stages_of(g.k), t.segs,
+                                t.slot_bits) == 1)
+                return;
+            note(t, len, in_place);
+        };
+        for (int64_t len : {16, 32, 64}) ask(std::min<int64_t>(len, most), thin);
+        if (s.n > most) ask(64, false);  // a last chunk
+        for (int64_t len = 128; len < std::min(most, kAsked); len += 64) ask(len, false);
+        if (most > 64) ask(std::min(most, kAsked), false);
+        if (most > kAsked)
+            for (HeadTiles t : {kBig, kMid, kLow2}) {
+                t.segs = s.f32 ? 6 : 1;
+                q.thin = false;
+                const GemmArgs g = make(q, kAsked);
+                if (!raw || split_may_pay(tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb), stages_of(g.k),
+                                          t.segs, t.slot_bits))
+                    note(t, most, false);
+            }
+        for (int i = 0; i < count; ++i) {
+            q.thin = seen[i].thin;
+            const GemmArgs g = make(q, seen[i].len);
+            const int64_t rows = int64_t(bounded(g, seen[i].t).split_rows);
+            bytes = std::max(bytes, std::max(rows, raw ? seen[i].len : 0) * g.ldf * 4);
+        }
+    };
+    if (most > 0 && s.v <= kHeadRawColumns) product(raw_product, true, true);
+    if (most > 0 && s.grad_hidden) product(hidden_product, true, false);
+    if (most > 0 && s.grad_head) product(head_product, false, false);
+    return bytes;
+}
+
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     return s.f32 ? run_head<true>(s, c, stream) : run_head<false>(s, c, stream);
 }

@@ -38,7 +38,8 @@ struct HeadShape {
     int32_t top = 1;              // entries per token (a target is one)
     bool f32 = false, teacher = false;
     bool grad_hidden = false, grad_head = false;
-    bool thin = false;            // an fp32 head is read in place by few tokens
+    bool in_place = false;        // an fp32 head may be read in place
+    bool thin = false;            // and is, by few tokens
     bool pack_head = false;       // the head is copied: fp32, d or its address not aligned
     bool raw = false;             // logits summed in parts, in the workspace
     int32_t planes = 1;           // bf16 planes of an operand: 3 hold an fp32 value
@@ -46,7 +47,9 @@ struct HeadShape {
     int64_t rows = 0;             // n padded to the tokens of a tile
     int64_t vp = 0, dp = 0;       // v padded to kHeadTile, d to kHeadDepth
     int64_t chunk = 0;            // tokens whose softmax is kept at a time
+    int64_t chunk_most = 0;       // ... of a call with any number of tokens
     int64_t nchunk = 0;
+    int64_t xt_tokens = 0;        // columns of the copy of X^T, for few tokens
     HeadTiles raw_tiles;          // of the logits in parts
     HeadTiles hidden_tiles[2], head_tiles[2];   // the gradients' of a chunk, and of the last one
     int64_t split_bytes = 0;      // for the parts of the sums that are split
@@ -75,6 +78,8 @@ bool head_fits_launch(const HeadShape& s);
 // How its products are cut, whether its logits are summed in parts, and the
 // bytes for parts of sums.
 void head_products(HeadShape* s);
+// No fewer bytes for parts of sums than any call with up to s.n tokens needs.
+int64_t head_split_most(const HeadShape& s);
 // Every launch of a call, in order, on `stream`.
 hipError_t launch_head(const HeadShape& s, const HeadCall& c, hipStream_t stream);
 

@@ -116,3 +116,23 @@ def test_fp32_gradient_of_large_logits(n, v, d, top):
     want, cp, ref = definition(head, index, logit, 1.0, None, n)
     within(got, want, 2.0 ** -17 * cp + 2 * U * want.abs(), "G")
     within(lse, ref, 2.0 ** -18 + U * ref, "lse")
+
+
+def test_bf16_gradient_is_rounded_once_over_chunks():
+    """2^22 columns: 512 tokens at a time, the head's gradient summed over two
+    chunks in fp32. A few tokens of either."""
+    n = d = 600
+    v = 1 << 22
+    g = gen("chunks")
+    head = torch.empty(v, d, device="cuda", dtype=BF).normal_(0.0, 2.0, generator=g)
+    index = torch.randint(0, v, (n,), device="cuda", generator=g)
+    x = torch.eye(d, device="cuda", dtype=BF)
+    loss, gw = torch.empty(n, device="cuda"), torch.full_like(head, float("nan"))
+    zsp.head_loss(x, head, index, loss, zsp.head_workspace(n, v, d, BF, grad_hidden=False), grad_head=gw)
+    for i in (0, 300, 511, 512, 599):
+        l = head[:, i].double()
+        p = torch.softmax(l, 0)
+        want = p.clone()
+        want[index[i]] -= 1.0
+        tol = B * want.abs() + (1 + B) * (2.0 ** -11 * p + 2.0 ** -63.9)
+        within(gw[:, i].double(), want, tol, f"G of token {i}")

@@ -136,3 +136,20 @@ def test_bf16_gradient_is_rounded_once_over_chunks():
         want[index[i]] -= 1.0
         tol = B * want.abs() + (1 + B) * (2.0 ** -11 * p + 2.0 ** -63.9)
         within(gw[:, i].double(), want, tol, f"G of token {i}")
+
+
+@pytest.mark.parametrize("T", [0.7, 3.0])
+@pytest.mark.parametrize("n,v,d", [(16, 9000, 64), (67, 9001, 67), (300, 9001, 320), (64, 700, 1024)])
+def test_fp32_gradient_of_large_logits_at_a_temperature(n, v, d, T):
+    """l / T is not rounded to fp32 before its difference from lse is taken:
+    |l - m| / T log2(e) <= 40 leaves 40 u + 2^-22 of p."""
+    g = gen(n, v, d, "T")
+    head = 3000.0 + 2.0 * torch.randn(v, d, device="cuda", generator=g)
+    index = torch.randint(0, v, (n, 5), device="cuda", generator=g)
+    logit = torch.randn(n, 5, device="cuda", generator=g)
+    T32 = float(torch.tensor(T))
+    got, lse = columns_of_g(head, index, logit, T32, None, n)
+    want, cp, ref = definition(head, index, logit, T32, None, n)
+    # scale * T: 1 / T and its product with T round once each
+    within(got, want, 2.0 ** -17 * cp + 5 * U * want.abs(), "G")
+    within(lse, ref, 2.0 ** -18 + U * ref, "lse")

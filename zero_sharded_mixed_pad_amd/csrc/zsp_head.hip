@@ -467,16 +467,16 @@ struct GemmArgs {
     int32_t tokens_in_b, tokens_in_k;
     uint32_t slot_bits;        // log2 of the tiles the card runs at once; 0: sums are not split
     // logits
-    float inv_temp;
+    float log2e_t;             // log2(e) / T
     float factor;              // of what goes to out
-    float2* part;              // [b][na_blocks]
+    float2* part;              // [b][na_blocks]: the largest sum, and of exp((sum - it) / T)
     int64_t nblk;
     void* p;                   // [b][ldp] steps (fp32: P), or NULL
     int64_t ldp;
     const int32_t* entry;      // [b][top_pad]
     const uint16_t* start;     // [b][blocks + 1]: a block's first entry, if top_pad > 1
     int32_t blocks;
-    float* pick;
+    float* pick;               // the entries' sums
     int32_t top_pad;
     // outputs
     void* out;                 // final: [row][ldo] of the output's type, or NULL
@@ -705,9 +705,8 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
                 if (e_from[b] < e_to[b]) one[b] = g.entry[row * g.top_pad + e_from[b]];
             }
         }
-        // in the sums' own units up to here: 1 / T > 0 comes to a block's
-        // largest, its entries and the exponent alone
-        const float log2e_t = g.inv_temp * kLog2e;
+        // in the sums' own units: 1 / T > 0 comes to the exponent alone here, and
+        // to the rest in 64 bits, when the blocks are joined
         const bool edge = a_wave + kHeadBlock > g.na;
 #pragma unroll
         for (int b = 0; b < TB; ++b) {
@@ -733,7 +732,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if ((rel >> 4) == a && (rel & 3) == c) l = acc[a][b][c];
-                g.pick[row * g.top_pad + k] = l * g.inv_temp;
+                g.pick[row * g.top_pad + k] = l;
             };
             if (real && g.top_pad == 1) take(0, one[b]);
             if (g.top_pad > 1 && e_from[b] < e_to[b]) {
@@ -755,7 +754,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
             for (int a = 0; a < TA; ++a)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float x = (acc[a][b][k] - mm) * log2e_t;
+                    const float x = (acc[a][b][k] - mm) * g.log2e_t;
                     const float e = __builtin_amdgcn_exp2f(x);
                     acc[a][b][k] = F32 ? e : -x;
                     s += e;
@@ -763,7 +762,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, f32x4 (&acc)[TA][TB], 
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
             if (lg == 0 && real)
-                g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m * g.inv_temp, s);
+                g.part[row * g.nblk + a_wave / kHeadBlock] = make_float2(m, s);
             if (g.p) {
                 if constexpr (F32) {
                     float* out = static_cast<float*>(g.p) + row * g.ldp + a_wave + lg * 4;
@@ -1133,7 +1132,8 @@ struct JoinArgs {
     const float* pick;
     const float* teach;       // the teacher's logits in the entries' order, or NULL
     int32_t top, top_pad;
-    float temp, inv_temp;
+    float temp, log2e_t;      // T, log2(e) / T
+    double inv_temp;
     float* loss;
     float* lse;
     void* p;                  // [chunk][ldp], or NULL: no gradients
@@ -1262,7 +1262,7 @@ struct Entries {
                                            float* s_q, double* s_d, F logit) const {
         if (!a.teach) {
             if (threadIdx.x == 0) s_q[0] = 1.0f;
-            return threadIdx.x == 0 ? lse - double(logit(0, e[0])) : 0.0;
+            return threadIdx.x == 0 ? lse - logit(0, e[0]) : 0.0;
         }
         const double lq = log(total);
         double sum = 0.0, none = 0.0;
@@ -1274,7 +1274,7 @@ struct Entries {
             if (e[i] >= 0) {
                 const double l = (double(t[i]) - double(m)) / double(a.temp) - lq;
                 q = exp(l);
-                if (q != 0.0) sum += q * (l - (double(logit(k, e[i])) - lse));
+                if (q != 0.0) sum += q * (l - (logit(k, e[i]) - lse));
             }
             s_q[k] = float(q);
         }
@@ -1301,16 +1301,17 @@ __device__ __forceinline__ void entries_gradient(const JoinArgs& a, int64_t r, i
         double q = 0.0;
         for (int32_t o = first; o < a.top && entry[o] >= 0 && entry[o] / kHeadBlock == block; ++o)
             if (entry[o] == e) q += double(s_q[o]);
-        const double x = double(logit(k, e)) - lse;
+        const double x = logit(k, e) - lse;
         put_g<F32>(a, r, e, float(double(c) * (expm1(x) + (1.0 - q))));
     }
 }
 
 // A workgroup (several, where tokens are few) per token that counts: lse =
 // m + log sum_b s_b exp(m_b - m) over the blocks, the loss, then the token's row
-// of G = c exp(m_b - lse) P, its steps read and G written in place: bound by those bytes (4
-// an element, fp32 10; 4096 tokens x 32000 in 92 us, 5.7 TB/s) or, where rows
-// are short, by the joins over the workgroup.
+// of G = c exp(m_b - lse) P, its steps read and G written in place: bound by
+// those bytes (4 an element, fp32 10; 4096 tokens x 32000 in 93 us, 5.7 TB/s)
+// or, where rows are short, by the joins over the workgroup. Largest logits and
+// entries come as they were summed; 1 / T is applied in 64 bits.
 template <bool F32, int T>
 __global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
     constexpr int kTop = T == 64 ? 64 : kHeadMaxTop;
@@ -1344,13 +1345,13 @@ __global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
     double s = 0.0;
     for (int32_t b = t; b < a.blocks; b += T) {
         const float2 q = part[b];
-        s += double(q.y) * double(q.x == m ? 1.0f : fast_exp(q.x - m));
+        s += double(q.y) * double(q.x == m ? 1.0f : __builtin_amdgcn_exp2f((q.x - m) * a.log2e_t));
     }
     double ts = entries.total(a, tm);
     block_sum2<T>(s, ts, s_d);
-    const double lse = double(m) + log(s);
+    const double lse = double(m) * a.inv_temp + log(s);
     const float* pick = a.pick + r * a.top_pad;
-    auto logit = [&](int32_t k, int32_t) { return pick[k]; };
+    auto logit = [&](int32_t k, int32_t) { return double(pick[k]) * a.inv_temp; };
     const double loss = entries.loss(a, lse, tm, ts, s_q, s_d, logit);
     if (t == 0 && part_no == 0) {
         a.loss[token] = float(loss);
@@ -1358,12 +1359,13 @@ __global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
     }
     if (!a.p) return;
 
-    // m_b - lse from 64 bits: rounded to fp32 first, an lse of 3000 would leave
-    // every p with an error of 1e-4
+    // m_b / T - lse from 64 bits: rounded to fp32 first, an lse of 3000 would
+    // leave every p with an error of 1e-4
+    auto below = [&](float m_b) { return float(double(m_b) * a.inv_temp - lse); };
     if constexpr (F32) {
         const float* p = static_cast<const float*>(a.p) + r * a.ldp;
         for (int64_t i = from + t * 4; i < to; i += T * 4) {
-            const float f = c * fast_exp(float(double(part[i / kHeadBlock].x) - lse));
+            const float f = c * fast_exp(below(part[i / kHeadBlock].x));
             const f32x4 v = *reinterpret_cast<const f32x4*>(p + i);
             uint16_t h[4][3];
 #pragma unroll
@@ -1379,7 +1381,7 @@ __global__ __launch_bounds__(T) void join_kernel(JoinArgs a) {
     } else {
         uint16_t* p = a.g + r * a.ldp;
         for (int64_t i = from + t * 8; i < to; i += T * 8) {
-            const float at = float(double(part[i / kHeadBlock].x) - lse) * kLog2e;
+            const float at = below(part[i / kHeadBlock].x) * kLog2e;
             u32x4 v = *reinterpret_cast<const u32x4*>(p + i);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -1448,7 +1450,6 @@ __global__ __launch_bounds__(T) void raw_join_kernel(RawArgs q) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (c0 + i * T >= v) break;
-            l[i] *= a.inv_temp;
             s_l[c0 + i * T] = l[i];
             m = nan_max(m, l[i]);
         }
@@ -1456,22 +1457,22 @@ __global__ __launch_bounds__(T) void raw_join_kernel(RawArgs q) {
     float tm = entries.largest(a);
     block_max2<T>(m, tm, s_f);
     float part = 0.0f;
-    for (int i = t; i < v; i += T) part += fast_exp(s_l[i] - m);
+    for (int i = t; i < v; i += T) part += __builtin_amdgcn_exp2f((s_l[i] - m) * a.log2e_t);
     double s = double(part), ts = entries.total(a, tm);
     block_sum2<T>(s, ts, s_d);
-    const double lse = double(m) + log(s);
-    auto logit = [&](int32_t, int32_t e) { return s_l[e]; };
+    const double lse = double(m) * a.inv_temp + log(s);
+    auto logit = [&](int32_t, int32_t e) { return double(s_l[e]) * a.inv_temp; };
     const double loss = entries.loss(a, lse, tm, ts, s_q, s_d, logit);
     if (t == 0) {
         a.loss[token] = float(loss);
         if (a.lse) a.lse[token] = float(lse);
     }
     if (!a.p) return;
-    const float shift = float(double(m) - lse);  // as in join_kernel
+    const float shift = float(double(m) * a.inv_temp - lse) * kLog2e;  // as in join_kernel
     for (int i = t * 8; i < cols; i += T * 8) {
         float g[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * fast_exp(s_l[i + k] - m + shift) : 0.0f;
+        for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * __builtin_amdgcn_exp2f((s_l[i + k] - m) * a.log2e_t + shift) : 0.0f;
         put_g8<F32>(a, r, i, g);
     }
     __threadfence_block();
@@ -1960,6 +1961,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
     // What all tokens have in common comes to the gradients in fp32: a factor
     // of 1/96 within G would give every target's -1 the same error in bf16.
     const float factor = c.scale * c.temperature;
+    const float log2e_t = 1.0f / c.temperature * kLog2e;
     // Two reads of a head that the Infinity Cache (256 MiB) holds, and no write of
     // its gradient between: few tokens let it stay there (100 tokens x 20000 x
     // 5120: 142 -> 129 us; 131072 x 4096 of 5 tokens 406 -> 430).
@@ -1987,7 +1989,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
         l.count = count;
         l.first = first;
         l.tokens_in_b = 1;
-        l.inv_temp = 1.0f / c.temperature;
+        l.log2e_t = log2e_t;
         l.part = part;
         l.nblk = s.vp / kHeadBlock;
         l.p = p;
@@ -2010,7 +2012,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             if ((e = pick_gemm<false, false, F32, kOut>(h, t, stream)) != hipSuccess) return e;
             JoinArgs j{nullptr, 0, blocks, count, first, rows + first, coef + first, l.entry,
                        nullptr, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
-                       c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
+                       c.temperature, log2e_t, 1.0 / c.temperature, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
             RawArgs q{j, split, s.v, s.dp, len, t.ba, t.bb, t.segs, t.slot_bits};
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
             const uint32_t grid = uint32_t(grads ? pad : len);
@@ -2034,7 +2036,7 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             const int32_t parts = grads ? int32_t(std::max<int64_t>(most, 1)) : 1;
             JoinArgs j{part, l.nblk, blocks, count, first, rows + first, coef + first, l.entry,
                        l.pick, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
-                       c.temperature, l.inv_temp, c.loss, c.lse, p, gp, s.vp, g_plane, parts};
+                       c.temperature, log2e_t, 1.0 / c.temperature, c.loss, c.lse, p, gp, s.vp, g_plane, parts};
             const uint32_t grid = uint32_t(grads ? pad * parts : len);
             // One wave a token, where its row is short: no barrier, and four
             // times the tokens on a CU (16384 tokens x 512 x 256 with gradients

@@ -120,3 +120,65 @@ def test_a_smaller_last_batch(n, m, v, d, dtype, top):
         run(*few, zsp.head_workspace(k, v, d, dtype, top=top), own)
         for a, b in zip(out, own):
             assert torch.equal(a, b) and not a.isnan().any()
+
+
+def near_the_definition(out, x, w, index, on, dl, run_of_tokens):
+    """Against 64 bits, in norm. dl: a logit's error; G: e c (p + q) with e = 2^-8
+    + 2^-10 + dl (bf16) or 2^-16 + dl (fp32); a gradient: that times the other
+    operand's largest singular value, k u |G| |the other| for a sum of k at a
+    time and one rounding."""
+    f32, u = x.dtype == F32, 2.0 ** -24
+    X, W = x.double() * on[:, None], w.double()
+    l = X @ W.t().contiguous()
+    lse = torch.logsumexp(l, 1)
+    at = torch.where(on, index, 0)[:, None]
+    loss = (lse - l.gather(1, at)[:, 0]) * on
+    lse *= on
+    for got, ref in zip(out[:2], (loss, lse)):
+        assert float((got.double() - ref).abs().max()) <= 2 * dl + 2.0 ** -18 + 2 * u * float(ref.abs().max())
+    p = torch.softmax(l, 1) * on[:, None]
+    q = torch.zeros_like(p).scatter_(1, at, 1.0) * on[:, None]
+    e = float(torch.linalg.norm(p + q)) * ((2.0 ** -16 if f32 else 2.0 ** -8 + 2.0 ** -10) + dl)
+    G = p - q
+    last = u if f32 else 2.0 ** -8
+    for got, g, m, k in ((out[2], G, W, len(W)), (out[3], G.t().contiguous(), X, run_of_tokens)):
+        ref, small = g @ m, m if m.shape[0] < m.shape[1] else m.t()
+        two = float(torch.linalg.eigvalsh((small @ small.t().contiguous()).cpu()).max()) ** 0.5
+        tol = (e * two + (6 if f32 else 1) * k * u * float(torch.linalg.norm(g.abs() @ m.abs()))
+               + last * float(torch.linalg.norm(ref)))
+        far, size = float(torch.linalg.norm(got.double() - ref)), float(torch.linalg.norm(ref))
+        assert far <= tol and tol < 0.1 * size, (far, tol, size)
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_the_most_tokens(half):
+    """2^23, of which all or about half count; the head's gradient is summed over
+    2^17 of them at a time, and then over 64 parts."""
+    n, v, d = 1 << 23, 70, 8
+    x, w, index, _ = inputs(n, v, d, BF, 0)
+    on = torch.ones(n, dtype=torch.bool, device="cuda")
+    if half:
+        on = torch.rand(n, device="cuda", generator=gen("half")) < 0.5
+        on[-1] = True
+        index[~on] = -1
+    out = outputs(x, w)
+    run(x, w, index, None, zsp.head_workspace(n, v, d, BF), out)
+    sum_xw = float((x[:1 << 16].double().abs() @ w.double().abs().t().contiguous()).max()) * 2
+    near_the_definition(out, x, w, index, on, d * 2.0 ** -24 * sum_xw, (1 << 17) + 64)
+    assert not half or not any(o[~on].any() for o in out[:3])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n", [3, 70, 300])
+def test_the_longest_rows(n, dtype):
+    """d = 65536. Products of -1, 0 and 1 by 2^-7 of them: sums of any order are
+    exact, and logits spread by 1.3."""
+    v, d = 200, 65536
+    g = gen(n, "rows")
+    x = torch.randint(-1, 2, (n, d), device="cuda", generator=g).to(dtype)
+    w = (torch.randint(-1, 2, (v, d), device="cuda", generator=g) * 2.0 ** -7).to(dtype)
+    index = torch.randint(0, v, (n,), device="cuda", generator=g)
+    out = outputs(x, w)
+    run(x, w, index, None, zsp.head_workspace(n, v, d, dtype), out)
+    assert not any(o.isnan().any() for o in out)
+    near_the_definition(out, x, w, index, torch.ones(n, dtype=torch.bool, device="cuda"), 0.0, n)

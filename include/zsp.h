@@ -509,14 +509,16 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
  * those take more.
  *   hidden, head and the gradients are all of `dtype`. Products are summed
  * in fp32 (operands of fp32 type are split into three bf16 values, exactly,
- * and products below 2^-23 of a term left out; of an infinity, or a value
- * beyond bf16's largest, in hidden or head a NaN may come); the softmax is
- * taken in fp32, its sums, the losses and a target's own g in 64 bits. For
- * bf16, token_weight_i * g_iv / T is rounded to bf16 once before the two
- * products that make the gradients (p comes to it within 2^-11 of itself, as 0
- * below 2^-63.9 of the largest of its 64 columns); calls with fp32 copies of
- * hidden and head round nothing to bf16. scale * T comes to the products' sums
- * in fp32. Equal inputs give equal bits.
+ * and products below 2^-23 of a term left out). Of an infinity in hidden or
+ * head, and in fp32 of a value beyond bf16's largest, a NaN may come. The
+ * softmax is taken in fp32, its sums too within 64 columns (where the logits
+ * are summed in parts, of a vocabulary up to 8192, within a thread's columns of
+ * a row) and in 64 bits over them; the losses, a target's own g and logits'
+ * differences from lse are taken in 64 bits. For bf16, token_weight_i * g_iv / T
+ * is rounded to bf16 once before the two products that make the gradients (p
+ * comes to it within 2^-11 of itself, as 0 below 2^-63.9 of the largest of its
+ * 64 columns); calls with fp32 copies of hidden and head round nothing to bf16.
+ * scale * T comes to the products' sums in fp32. Equal inputs give equal bits.
  *   0 <= n <= 2^23 tokens, 1 <= v <= 2^22, 1 <= d <= 65536, top <= 1024, n *
  * d below about 2^34. Pointers need the alignment of their element type
  * only, ws 16 bytes; a head on 16 bytes whose d is a multiple of 8 is read

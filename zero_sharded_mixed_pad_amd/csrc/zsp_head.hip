@@ -125,8 +125,8 @@ __device__ __forceinline__ bool counts(const int64_t* target, const float* weigh
     return uint64_t(e) < uint64_t(v) && w != 0.0f;
 }
 
-// rows[0 .. count): the tokens that count, in order. One workgroup, 16 tokens
-// a thread at a time; the waves' counts are joined in LDS.
+// rows[0 .. count): the tokens that count, in order. One workgroup, kScanRun
+// tokens a thread at a time; the waves' counts are joined in LDS.
 constexpr int kScanThreads = 1024, kScanRun = 8;
 constexpr int64_t kFlagEntries = 8192, kFlagTokens = kScanThreads * kScanRun;
 __global__ __launch_bounds__(kScanThreads) void scan_kernel(const int64_t* target,

@@ -137,7 +137,10 @@ def parse():
     ap.add_argument("--layers", type=int, default=32)
     ap.add_argument("--tokens", type=int, nargs="+", default=[512, 1024, 4096])
     ap.add_argument("--depths", type=int, nargs="+", default=[1, 2])
-    return ap.parse_args()
+    args = ap.parse_args()
+    if args.head_loss and not args.prefetch:
+        ap.error("--head-loss goes with --prefetch")
+    return args
 
 
 # ---------------------------------------------------------------------------

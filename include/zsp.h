@@ -537,10 +537,10 @@ void zsp_tensor_list_destroy(zsp_tensor_list* list);
 #define ZSP_HEAD_GRAD_HEAD 2   /* grad_head is wanted */
 #define ZSP_HEAD_UNALIGNED 4   /* head may start off a 16-byte boundary */
 
-/* Workspace bytes of calls of up to n tokens: top as for zsp_head_distill, 0
- * for zsp_head_loss; flags of the above. (A call of fewer tokens may cut its
- * sums into more parts, or its tokens into larger chunks; the answer holds all
- * of them.) Host only. */
+/* Workspace bytes of calls of up to n tokens and `top` entries (0 for
+ * zsp_head_loss alone), with any of the gradients that flags (of the above)
+ * name. (A call of fewer tokens may cut its sums into more parts, or its tokens
+ * into larger chunks; the answer holds all of them.) Host only. */
 zsp_status zsp_head_workspace(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, int32_t top,
                               int32_t flags, int64_t* bytes);
 zsp_status zsp_head_loss(const void* hidden, const void* head, zsp_dtype dtype, int64_t n,

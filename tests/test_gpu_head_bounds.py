@@ -182,3 +182,18 @@ def test_the_longest_rows(n, dtype):
     run(x, w, index, None, zsp.head_workspace(n, v, d, dtype), out)
     assert not any(o.isnan().any() for o in out)
     near_the_definition(out, x, w, index, torch.ones(n, dtype=torch.bool, device="cuda"), 0.0, n)
+
+
+@pytest.mark.parametrize("n,v,d,dtype", [(300, 9000, 512, BF), (64, 700, 1024, F32)])
+def test_an_evaluation_in_a_training_steps_workspace(n, v, d, dtype):
+    """With fewer gradients, tokens and entries than it was sized for."""
+    x, w, index, logit = inputs(n, v, d, dtype, 4)
+    ws = zsp.head_workspace(n, v, d, dtype, top=4)
+    for m, top in ((n, 4), (n // 3, 2), (n // 3, 0)):
+        few = (x[:m], w, index[:m, :top].contiguous() if top else index[:m, 0].contiguous(),
+               logit[:m, :top].contiguous() if top else None)
+        whole, alone = outputs(x[:m], w), outputs(x[:m], w)
+        run(*few, ws, whole)
+        run(*few, ws, alone[:2] + [None, None])
+        for a, b in zip(whole[:2], alone[:2]):
+            assert torch.equal(a, b) and not a.isnan().any()

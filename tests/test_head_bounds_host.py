@@ -101,7 +101,21 @@ def test_workspaces_serve_fewer_tokens_whatever_the_sizes():
         n, v, d = log(0, 18), log(0, 20), log(0, 13)
         dtype = rng.choice([torch.bfloat16, torch.float32])
         top, grads = rng.choice([0, 0, 3]), (rng.random() < 0.7, rng.random() < 0.7)
-        ws_bytes = binding.zsp_head_workspace(n, v, d, dtype, top, *grads)
+        # of a head that may start anywhere: then too where it does not
+        ws_bytes = binding.zsp_head_workspace(n, v, d, dtype, top, *grads, aligned=rng.random() < 0.7)
         for m in {rng.randint(1, n), log(0, n.bit_length()) % n + 1, n}:
             assert call(m, v, d, dtype, top, ws_bytes, grads) == EINVAL
             assert "loss is not aligned" in zsp.last_error(), (n, m, v, d, dtype, top, grads)
+
+
+@pytest.mark.parametrize("n,v,d,dtype,top", [(773670, 897009, 68, torch.float32, 0), (3404901, 3013938, 4, torch.bfloat16, 0),
+                                             (130039, 848989, 193, torch.float32, 3), (4096, 32000, 4096, torch.bfloat16, 64),
+                                             (61, 1000, 1003, torch.float32, 1)])
+def test_a_workspace_serves_fewer_gradients_and_entries(n, v, d, dtype, top):
+    """A training step's serves an evaluation: losses alone may keep more tokens
+    at a time."""
+    ws_bytes = binding.zsp_head_workspace(n, v, d, dtype, top)
+    for grads in ((True, True), (True, False), (False, True), (False, False)):
+        for k in sorted({0, min(1, top), top // 2, top}):
+            assert call(n, v, d, dtype, k, ws_bytes, grads) == EINVAL
+            assert "loss is not aligned" in zsp.last_error(), (grads, k, zsp.last_error())

@@ -625,9 +625,10 @@ class TensorList:
 # ---- losses over the head --------------------------------------------------
 
 def zsp_head_workspace(n, v, d, dtype, top=0, grad_hidden=True, grad_head=True, aligned=True):
-    """Bytes of workspace of head_loss calls (top = 0) or head_distill calls
-    with `top` entries per token: up to n tokens, a head of v rows of d.
-    aligned False: for a head that may start off a 16-byte boundary."""
+    """Bytes of workspace of head_loss calls and, with `top`, head_distill calls
+    of up to so many entries per token: up to n tokens, a head of v rows of d,
+    any of the gradients named. aligned False: for a head that may start off a
+    16-byte boundary."""
     code = {torch.float32: F32, torch.bfloat16: BF16}.get(dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
@@ -641,7 +642,7 @@ def zsp_head_workspace(n, v, d, dtype, top=0, grad_hidden=True, grad_head=True, 
 
 def head_workspace(n, v, d, dtype, top=0, grad_hidden=True, grad_head=True, aligned=True,
                    device="cuda"):
-    """A workspace for such calls, of n tokens or fewer. Calls that may run at the same time, or
+    """A workspace for such calls. Calls that may run at the same time, or
     captured graphs that may be replayed so, each need their own."""
     return torch.empty(zsp_head_workspace(n, v, d, dtype, top, grad_hidden, grad_head, aligned),
                        dtype=torch.uint8, device=device)

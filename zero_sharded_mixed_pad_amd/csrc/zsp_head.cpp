@@ -182,15 +182,23 @@ zsp_status zsp_head_workspace(int64_t n, int64_t v, int64_t d, zsp_dtype dtype, 
                               int32_t flags, int64_t* bytes) {
     using namespace zsp;
     if (!bytes) return set_error(ZSP_EINVAL, "bytes is NULL");
-    HeadShape s;
-    const zsp_status st = make_shape(n, v, d, dtype, top, flags, &s);
-    if (st != ZSP_OK) return st;
-    // of every call of up to n tokens, whose parts of sums or chunks may be larger
-    s.split_bytes = head_split_most(s);
-    s.chunk = std::min(s.rows, s.chunk_most);
-    if (s.grad_head && !s.f32) s.xt_tokens = up(std::min<int64_t>(n, kHeadFew), 32);
-    lay_out(&s);
-    *bytes = s.bytes;
+    // the most of the calls with some of the gradients, which may keep more
+    // tokens at a time, and with up to n tokens, whose parts of sums or chunks may
+    // be larger
+    const int32_t grads = flags & (ZSP_HEAD_GRAD_HIDDEN | ZSP_HEAD_GRAD_HEAD);
+    int64_t most = 0;
+    for (int32_t some = 0; some <= grads; ++some) {
+        if (some & ~grads) continue;
+        HeadShape s;
+        const zsp_status st = make_shape(n, v, d, dtype, top, (flags & ~grads) | some, &s);
+        if (st != ZSP_OK) return st;
+        s.split_bytes = head_split_most(s);
+        s.chunk = std::min(s.rows, s.chunk_most);
+        if (s.grad_head && !s.f32) s.xt_tokens = up(std::min<int64_t>(n, kHeadFew), 32);
+        lay_out(&s);
+        most = std::max(most, s.bytes);
+    }
+    *bytes = most;
     return ZSP_OK;
 }
 

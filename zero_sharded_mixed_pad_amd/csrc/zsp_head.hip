@@ -2127,13 +2127,12 @@ void head_products(HeadShape* s) {
 }
 
 // By asking every number of tokens which form it takes (64 of them at a time,
-// and the in-place forms' 16 and 32: what the choice goes by does not change
+// and the in-place forms 16 and 32: what the choice goes by does not change
 // between), then each form for the most that it serves. Past kAsked tokens, all
 // forms that those may take.
 int64_t head_split_most(const HeadShape& s) {
     constexpr int64_t kAsked = 65536;
     const int64_t most = std::min(s.n, s.chunk_most);
-    const bool thin = s.in_place;
     int64_t bytes = 0;
     auto product = [&](auto make, bool low, bool raw) {
         struct Seen {
@@ -2158,8 +2157,10 @@ int64_t head_split_most(const HeadShape& s) {
                 return;
             note(t, len, in_place);
         };
-        for (int64_t len : {16, 32, 64}) ask(std::min<int64_t>(len, most), thin);
-        if (s.n > most) ask(64, false);  // a last chunk
+        // (a head that may start anywhere may still be read in place)
+        for (int64_t len : {16, 32, 64})
+            if (s.f32 && s.d % 4 == 0) ask(std::min<int64_t>(len, most), true);
+        if (!s.in_place || s.n > most) ask(std::min<int64_t>(64, most), false);  // or of a last chunk
         for (int64_t len = 128; len < std::min(most, kAsked); len += 64) ask(len, false);
         if (most > 64) ask(std::min(most, kAsked), false);
         if (most > kAsked)

@@ -1472,7 +1472,8 @@ __global__ __launch_bounds__(T) void raw_join_kernel(RawArgs q) {
     for (int i = t * 8; i < cols; i += T * 8) {
         float g[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = i + k < v ? c * __builtin_amdgcn_exp2f((s_l[i + k] - m) * a.log2e_t + shift) : 0.0f;
+        for (int k = 0; k < 8; ++k)
+            g[k] = i + k < v ? c * __builtin_amdgcn_exp2f((s_l[i + k] - m) * a.log2e_t + shift) : 0.0f;
         put_g8<F32>(a, r, i, g);
     }
     __threadfence_block();
@@ -2012,7 +2013,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             if ((e = pick_gemm<false, false, F32, kOut>(h, t, stream)) != hipSuccess) return e;
             JoinArgs j{nullptr, 0, blocks, count, first, rows + first, coef + first, l.entry,
                        nullptr, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
-                       c.temperature, log2e_t, 1.0 / c.temperature, c.loss, c.lse, p, gp, s.vp, g_plane, 1};
+                       c.temperature, log2e_t, 1.0 / c.temperature, c.loss, c.lse, p, gp, s.vp,
+                       g_plane, 1};
             RawArgs q{j, split, s.v, s.dp, len, t.ba, t.bb, t.segs, t.slot_bits};
             const int64_t pad = (len + kHeadDepth - 1) / kHeadDepth * kHeadDepth;
             const uint32_t grid = uint32_t(grads ? pad : len);
@@ -2021,10 +2023,9 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             else
                 raw_join_kernel<F32, 1024, kHeadRawColumns><<<grid, 1024, 0, stream>>>(q);
             if ((e = hipGetLastError()) != hipSuccess) return e;
-        } else if (len > 0 &&
-                   (e = pick_gemm<false, false, F32, kLogits>(l, bounded(l, tile_of(l, F32, true)), stream)) !=
-                       hipSuccess) {
-            return e;
+        } else if (len > 0) {
+            const HeadTiles t = bounded(l, tile_of(l, F32, true));
+            if ((e = pick_gemm<false, false, F32, kLogits>(l, t, stream)) != hipSuccess) return e;
         }
 
         if (!s.raw && len > 0) {
@@ -2036,7 +2037,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             const int32_t parts = grads ? int32_t(std::max<int64_t>(most, 1)) : 1;
             JoinArgs j{part, l.nblk, blocks, count, first, rows + first, coef + first, l.entry,
                        l.pick, teach ? teach + first * s.top_pad : nullptr, s.top, s.top_pad,
-                       c.temperature, log2e_t, 1.0 / c.temperature, c.loss, c.lse, p, gp, s.vp, g_plane, parts};
+                       c.temperature, log2e_t, 1.0 / c.temperature, c.loss, c.lse, p, gp, s.vp,
+                       g_plane, parts};
             const uint32_t grid = uint32_t(grads ? pad * parts : len);
             // One wave a token, where its row is short: no barrier, and four
             // times the tokens on a CU (16384 tokens x 512 x 256 with gradients
@@ -2061,7 +2063,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.factor = factor;
             h.rows = rows + first;
             h.split = split;
-            if ((e = pick_gemm<true, false, F32, kOut>(h, s.hidden_tiles[last], stream)) != hipSuccess) return e;
+            const HeadTiles& t = s.hidden_tiles[last];
+            if ((e = pick_gemm<true, false, F32, kOut>(h, t, stream)) != hipSuccess) return e;
         }
         if (few_tokens) {
             const OuterArgs o{xt, gp, static_cast<uint16_t*>(c.grad_head), count, s.v, s.d, s.dp,
@@ -2079,7 +2082,8 @@ hipError_t run_head(const HeadShape& s, const HeadCall& c, hipStream_t stream) {
             h.split = split;
             h.acc_in = ch > 0 ? acc : nullptr;
             h.acc_out = ch + 1 < s.nchunk ? acc : nullptr;
-            if ((e = pick_gemm<true, true, F32, kOut>(h, s.head_tiles[last], stream)) != hipSuccess) return e;
+            const HeadTiles& t = s.head_tiles[last];
+            if ((e = pick_gemm<true, true, F32, kOut>(h, t, stream)) != hipSuccess) return e;
         }
     }
     return hipSuccess;
@@ -2093,10 +2097,10 @@ bool head_fits_launch(const HeadShape& s) {
     return setup_grid(s).all() * kSetupThreads < int64_t(1) << 32;
 }
 
-// Whether the logits' sums are worth splitting: a row of them has to fit LDS
-// beside others, and the whole product to leave most of the card idle. With
-// rows of up to 32768 logits taken this way, 96 tokens x 32000 x 4096 with the
-// head's gradient take 231 us in place of 195.
+// The logits' sums are worth splitting where a row of them fits LDS beside others
+// and the whole product leaves most of the card idle. (With rows of up to 32768
+// logits taken this way, 96 tokens x 32000 x 4096 with the head's gradient take
+// 231 us in place of 195.) The gradients' products: of a chunk and of the last.
 void head_products(HeadShape* s) {
     auto tiles = [&](const GemmArgs& g, bool low) { return bounded(g, tile_of(g, s->f32, low)); };
     int64_t bytes = 0;
@@ -2152,9 +2156,8 @@ int64_t head_split_most(const HeadShape& s) {
             q.thin = in_place;
             const GemmArgs g = make(q, len);
             const HeadTiles t = tile_of(g, s.f32, low);
-            if (raw && split_of(tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb), stages_of(g.k), t.segs,
-                                t.slot_bits) == 1)
-                return;
+            const uint32_t tiles = tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb);
+            if (raw && split_of(tiles, stages_of(g.k), t.segs, t.slot_bits) == 1) return;
             note(t, len, in_place);
         };
         // (a head that may start anywhere may still be read in place)
@@ -2168,8 +2171,8 @@ int64_t head_split_most(const HeadShape& s) {
                 t.segs = s.f32 ? 6 : 1;
                 q.thin = false;
                 const GemmArgs g = make(q, kAsked);
-                if (!raw || split_may_pay(tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb), stages_of(g.k),
-                                          t.segs, t.slot_bits))
+                const uint32_t tiles = tiles_along(g.na, t.ba) * tiles_along(g.nb, t.bb);
+                if (!raw || split_may_pay(tiles, stages_of(g.k), t.segs, t.slot_bits))
                     note(t, most, false);
             }
         for (int i = 0; i < count; ++i) {

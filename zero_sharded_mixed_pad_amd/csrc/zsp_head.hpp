@@ -11,7 +11,8 @@
 
 namespace zsp {
 
-constexpr int32_t kHeadTile = 256;       // rows (of more than 64 tokens) and columns of P are padded to it
+constexpr int32_t kHeadTile = 256;       // columns of P, and rows of more than 64 tokens, are
+                                         // padded to it
 constexpr int32_t kHeadBlock = 64;       // vocabulary columns per partial of a softmax
 constexpr int32_t kHeadDepth = 64;       // d is padded to it
 constexpr int32_t kHeadMaxTop = 1024;    // teacher's entries per token
